@@ -9,6 +9,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass, field
 
@@ -40,6 +41,33 @@ class AffqmmError(RuntimeError):
 class CWeight(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("group", ctypes.c_int32), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("packed", ctypes.c_void_p)]
+
+
+class CCache(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("page", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class CStep(ctypes.Structure):
+    _fields_ = [("capacity", ctypes.c_int64), ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("ring_state", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("requests", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("rotary", ctypes.c_int32),
+                ("neighbour", ctypes.c_int32), ("axes", ctypes.c_int32)]
+
+
+class CRows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class CLanes(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -75,6 +103,12 @@ def lib() -> ctypes.CDLL:
             "affqmm_rows_bytes": (i32, [i32, i32, i64, i64, szp]),
             "affqmm_pack_rows": (i32, [wp, vp, vp]),
             "affqmm_embed_rows_copy": (i32, [wp, vp, vp, i64, i32, ctypes.c_uint16, vp, vp, vp]),
+            "affqmm_paged_plan": (i32, [i64, vp, vp, vp, vp, i64, i64, vp, i64, vp, i32, ctypes.POINTER(CStep), vp]),
+            "affqmm_rope_append": (i32, [ctypes.POINTER(CCache), ctypes.POINTER(CRope), *[ctypes.POINTER(CRows)] * 4,
+                                         i64, i32, vp, i64, vp, vp, vp]),
+            "affqmm_paged_attention_workspace_bytes": (i32, [ctypes.POINTER(CCache), i32, i32, szp]),
+            "affqmm_paged_attention": (i32, [ctypes.POINTER(CCache), *[ctypes.POINTER(CLanes)] * 2, vp, i64, i32, i32,
+                                             vp, i64, i64, vp, ctypes.c_float, i32, vp, vp, ctypes.c_size_t, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -425,4 +459,244 @@ def embed_rows_copy(w: PackedWeight, rows: torch.Tensor, ids: torch.Tensor, scal
                                         0 if scale is None else 1, sbits, out.data_ptr(),
                                         status.data_ptr() if status is not None else None, _stream_ptr(stream)),
            "affqmm_embed_rows_copy")
+    return out
+
+
+# ----------------------------------------------------------------------------- the paged key-value cache
+PAGED_MAX_BATCH = 16384              # requests of a call
+PAGED_MAX_TOKENS = 64                # query tokens of a request
+_KV_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+def _check_ints(t: torch.Tensor, name: str, shape: tuple, device=None, dtype=torch.int32, contiguous=True):
+    if (not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or (contiguous and not t.is_contiguous())
+            or (device is not None and t.device != device)):
+        raise ValueError(f"{name} must be a{' contiguous' if contiguous else ''} CUDA {dtype} {list(shape)} tensor"
+                         + (f" on {device}" if device is not None else ""))
+
+
+class KVCache:
+    """A pool of pages of keys and values: k and v [pages, page, heads, dim],
+    bf16 or float8_e4m3fn, with the values of a head contiguous and the other
+    axes in any order in memory (a head-major pool is a transposed view).  For
+    float8, k_scale and v_scale (float32 [heads], or None for 1) are what a
+    head's stored values are multiplied by.  The object keeps the tensors'
+    addresses: build it once per pool."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must be [pages, page, heads, dim] tensors of one type, shape, stride and device")
+        if k.dtype not in _KV_TYPES or not k.is_cuda:
+            raise ValueError("k and v must be CUDA bf16 or float8_e4m3fn tensors")
+        if k.stride(3) != 1 and k.shape[3] > 1:
+            raise ValueError("the values of a head must be contiguous")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                if k.dtype != torch.float8_e4m3fn:
+                    raise ValueError(f"{name} belongs to a float8 cache")
+                _check_ints(t, name, (k.shape[2],), k.device, torch.float32)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page, self.heads, self.dim = k.shape
+        self.device = k.device
+        self._c = CCache(_KV_TYPES[k.dtype], self.page, self.heads, self.dim, self.pages, *k.stride()[:3],
+                         k.data_ptr() if k.numel() else None, v.data_ptr() if v.numel() else None,
+                         k_scale.data_ptr() if k_scale is not None else None,
+                         v_scale.data_ptr() if v_scale is not None else None)
+        self._ref = ctypes.byref(self._c)
+        self._ws: dict = {}          # (tokens, query heads) -> workspace bytes
+
+    @classmethod
+    def empty(cls, pages: int, page: int, heads: int, dim: int, dtype=torch.bfloat16, device="cuda", k_scale=None,
+              v_scale=None) -> "KVCache":
+        k, v = (torch.empty(pages, page, heads, dim, dtype=dtype, device=device) for _ in "kv")
+        return cls(k, v, k_scale, v_scale)
+
+
+class Rope:
+    """Rotary positions: `turns` int64 [rotary / 2], pair i's turns a position
+    as a 64-bit fraction of a turn (rope_turns makes them), and `axis` uint8
+    [rotary / 2] or None, the axis of positions by which each pair turns.
+    neighbour=False pairs values i and i + rotary / 2, True 2i and 2i + 1."""
+
+    def __init__(self, turns: torch.Tensor, axis: torch.Tensor | None = None, neighbour: bool = False):
+        if turns.dim() != 1:
+            raise ValueError("turns must be one-dimensional")
+        _check_ints(turns, "turns", tuple(turns.shape), dtype=torch.int64)
+        if axis is not None:
+            _check_ints(axis, "axis", tuple(turns.shape), turns.device, torch.uint8)
+        self.turns, self.axis, self.neighbour, self.device = turns, axis, bool(neighbour), turns.device
+        self.rotary = 2 * turns.numel()
+        self._c = CRope(turns.data_ptr() if turns.numel() else None, axis.data_ptr() if axis is not None else None,
+                        self.rotary, int(self.neighbour), 1)
+        self._ref = ctypes.byref(self._c)
+
+
+def rope_turns(frequencies, device="cuda") -> torch.Tensor:
+    """turns of a Rope from its frequencies in radians a position (a sequence
+    or float64 tensor: base ** (-2i / rotary), scaled as the model scales it;
+    0 for a pair that does not turn)."""
+    f = torch.as_tensor(frequencies, dtype=torch.float64, device="cpu") / (2 * math.pi)
+    whole = torch.floor((f - torch.floor(f)) * 2.0 ** 64).tolist()
+    wrapped = [int(x) % (1 << 64) for x in whole]
+    return torch.tensor([x - (1 << 64) if x >> 63 else x for x in wrapped], dtype=torch.int64, device=device)
+
+
+class PagedStep:
+    """What paged_plan writes: starts int32 [batch + 1], lens int32 [batch],
+    ring_state int32 [2], slots / positions / requests int32 [capacity] and
+    status int32 [1].  Build one (PagedStep.empty) and use it again: a captured
+    step reads the same addresses every time."""
+
+    def __init__(self, starts, lens, ring_state, slots, positions, requests, status):
+        batch, capacity, device = lens.numel(), slots.numel(), lens.device
+        _check_ints(starts, "starts", (batch + 1,), device)
+        _check_ints(lens, "lens", (batch,))
+        _check_ints(ring_state, "ring_state", (2,), device)
+        for t, name in ((slots, "slots"), (positions, "positions"), (requests, "requests")):
+            _check_ints(t, name, (capacity,), device)
+        _check_ints(status, "status", (1,), device)
+        self.starts, self.lens, self.ring_state, self.status = starts, lens, ring_state, status
+        self.slots, self.positions, self.requests = slots, positions, requests
+        self.batch, self.capacity, self.device = batch, capacity, device
+        ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
+        self._c = CStep(capacity, *[ptr(t) for t in (starts, lens, ring_state, slots, positions, requests, status)])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, batch: int, capacity: int, device="cuda") -> "PagedStep":
+        make = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(make(batch + 1), make(batch), make(2), make(capacity), make(capacity), make(capacity), make(1))
+
+
+def paged_plan(lens: torch.Tensor, fresh: torch.Tensor, finished: torch.Tensor | None, table: torch.Tensor,
+               ring: torch.Tensor, ring_state: torch.Tensor, page: int, out: PagedStep, stream=None) -> PagedStep:
+    """affqmm_paged_plan: a step's block tables, slot maps, positions and
+    lengths.  lens, fresh int32 [batch]; finished bool [batch] or None; table
+    int32 [batch, wide] (rows may be strided), written where the step takes
+    pages; ring int32 [pool] of free pages, ring_state int32 [2] its head and
+    count.  out.lens and out.ring_state are the next step's lens and
+    ring_state; they must be other tensors than this step's."""
+    batch, dev = lens.numel(), out.device
+    if out.batch != batch:
+        raise ValueError(f"out is a step of {out.batch} requests, lens has {batch}")
+    _check_ints(lens, "lens", (batch,), dev)
+    _check_ints(fresh, "fresh", (batch,), dev)
+    if finished is not None:
+        _check_ints(finished, "finished", (batch,), dev, torch.bool)
+    if table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
+        raise ValueError("table must be two-dimensional, the entries of a row contiguous")
+    wide = table.shape[1]
+    _check_ints(table, "table", (batch, wide), dev, contiguous=False)
+    _check_ints(ring, "ring", (ring.numel(),), dev)
+    _check_ints(ring_state, "ring_state", (2,), dev)
+    sp = _stream_ptr(stream, dev.index)
+    _check(lib().affqmm_paged_plan(batch, lens.data_ptr(), fresh.data_ptr(),
+                                   finished.data_ptr() if finished is not None else None, table.data_ptr(),
+                                   table.stride(0), wide, ring.data_ptr(), ring.numel(), ring_state.data_ptr(), page,
+                                   out._ref, sp), "affqmm_paged_plan")
+    return out
+
+
+def _check_heads(t: torch.Tensor, name: str, shape: tuple, device):
+    if (not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != shape or t.stride(-1) != 1 or t.device != device):
+        raise ValueError(f"{name} must be a CUDA bf16 {list(shape)} tensor on {device}, the values of a head contiguous")
+
+
+def _rows(t: torch.Tensor) -> CRows:
+    s = t.stride()
+    return CRows(t.data_ptr(), s[0], s[1])
+
+
+def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                rope: Rope, cache: KVCache, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """affqmm_rope_append: rotary positions on q and k, and k and v written to
+    their slots of the cache.  q [tokens, query heads, dim], k and v [tokens,
+    cache heads, dim], bf16, of any token and head strides (views of the stacked
+    projection's output serve); positions int32 [tokens] or [axes, tokens];
+    slots int32 [tokens], -1 for a token that is not kept.  Returns q turned,
+    in `out` (which may be q)."""
+    dev, T = cache.device, q.shape[0]
+    heads, dim = q.shape[1], cache.dim
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, query heads, dim]")
+    _check_heads(q, "q", (T, heads, dim), dev)
+    _check_heads(k, "k", (T, cache.heads, dim), dev)
+    _check_heads(v, "v", (T, cache.heads, dim), dev)
+    if out is None:
+        out = torch.empty(T, heads, dim, dtype=torch.bfloat16, device=dev)
+    _check_heads(out, "out", (T, heads, dim), dev)
+    if (not positions.is_cuda or positions.dtype != torch.int32 or positions.device != dev or positions.dim() not in (1, 2)
+            or positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1)):
+        raise ValueError(f"positions must be a CUDA int32 [{T}] or [axes, {T}] tensor on {dev}")
+    if rope.device != dev:
+        raise ValueError(f"the rope must be on {dev}")
+    _check_ints(slots, "slots", (T,), dev)
+    if T == 0:
+        return out
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    c = rope._c
+    if c.axes != axes:
+        c.axes = axes
+    _check(lib().affqmm_rope_append(cache._ref, rope._ref, _rows(q), _rows(k), _rows(v), _rows(out), T, heads,
+                                    positions.data_ptr(), positions.stride(0) if axes > 1 else 0, slots.data_ptr(),
+                                    status.data_ptr() if status is not None else None, _stream_ptr(stream, dev.index)),
+           "affqmm_rope_append")
+    return out
+
+
+def paged_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> int:
+    need = cache._ws.get((tokens, heads))
+    if need is None:
+        got = ctypes.c_size_t(0)
+        with torch.cuda.device(cache.device):
+            _check(lib().affqmm_paged_attention_workspace_bytes(cache._ref, tokens, heads, ctypes.byref(got)),
+                   "affqmm_paged_attention_workspace_bytes")
+        need = cache._ws[(tokens, heads)] = got.value
+    return need
+
+
+def _lanes(t: torch.Tensor) -> CLanes:
+    s = t.stride()
+    return CLanes(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else CLanes(t.data_ptr(), s[0], 0, s[1])
+
+
+def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+                    window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, workspace: Workspace | None = None, stream=None) -> torch.Tensor:
+    """affqmm_paged_attention: each request's newest tokens against its pages.
+    q bf16 [batch, query heads, dim] (one new token) or [batch, tokens, query
+    heads, dim], any strides; table int32 [batch, wide]; lens int32 [batch], the
+    step's own tokens included; scale defaults to dim ** -0.5; window > 0 keeps
+    the last `window` keys of each token.  `lse` (float32, q's shape without its
+    last axis) gets the log of each row's sum of exponentials.  Returns `out`,
+    of q's shape."""
+    dev, dim, shape = cache.device, cache.dim, q.shape
+    if len(shape) == 4:
+        batch, tokens, heads, d = shape
+    elif len(shape) == 3:
+        (batch, heads, d), tokens = shape, 1
+    else:
+        raise ValueError("q must be [batch, query heads, dim] or [batch, tokens, query heads, dim]")
+    if d != dim:
+        raise ValueError(f"q has {d} values a head, the cache {dim}")
+    _check_heads(q, "q", shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _check_heads(out, "out", shape, dev)
+    if table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
+        raise ValueError("table must be two-dimensional, the entries of a row contiguous")
+    wide = table.shape[1]
+    _check_ints(table, "table", (batch, wide), dev, contiguous=False)
+    _check_ints(lens, "lens", (batch,), dev)
+    if lse is not None:
+        _check_ints(lse, "lse", tuple(shape[:-1]), dev, torch.float32)
+    sp = _stream_ptr(stream, dev.index)
+    buf = (workspace or default_workspace(dev.index, sp)).get(paged_attention_workspace_bytes(cache, tokens, heads))
+    _check(lib().affqmm_paged_attention(cache._ref, _lanes(q), _lanes(out), lse.data_ptr() if lse is not None else None,
+                                        batch, tokens, heads, table.data_ptr(), table.stride(0), wide, lens.data_ptr(),
+                                        dim ** -0.5 if scale is None else scale, window,
+                                        status.data_ptr() if status is not None else None, buf.data_ptr(), buf.numel(),
+                                        sp), "affqmm_paged_attention")
     return out

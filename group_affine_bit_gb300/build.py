@@ -18,8 +18,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libaffqmm.so")
 
-SOURCES = ["affqmm_api.cu", "plan.cu", "pack.cu", "decode.cu", "prompt.cu", "embed.cu", "hostio.cu"]
-HEADERS = ["affqmm_format.cuh", "affqmm_internal.h", "affqmm_async.cuh", "affqmm_tc.cuh"]
+SOURCES = ["affqmm_api.cu", "plan.cu", "pack.cu", "decode.cu", "prompt.cu", "embed.cu", "hostio.cu",
+           "paged_api.cu", "paged_plan.cu", "rope_append.cu", "paged_attn_64.cu", "paged_attn_128.cu",
+           "paged_attn_256.cu", "paged_attn_512.cu"]
+HEADERS = ["affqmm_format.cuh", "affqmm_internal.h", "affqmm_async.cuh", "affqmm_tc.cuh", "affqmm_paged.h", "paged_attn.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -11,6 +11,7 @@
 #include "affqmm.h"
 #include "affqmm_format.cuh"
 #include "affqmm_internal.h"
+#include "affqmm_paged.h"
 
 using namespace affqmm;
 
@@ -56,6 +57,17 @@ int device_info(DeviceInfo** out) {
     *out = &d;
     return AFFQMM_OK;
 }
+
+}  // namespace
+
+int affqmm::device_sms(int* sms) {
+    DeviceInfo* d = nullptr;
+    const int rc = device_info(&d);
+    if (rc == AFFQMM_OK) *sms = d->sms;
+    return rc;
+}
+
+namespace {
 
 int check_weight(const affqmm_weight* w) {
     if (!w) return AFFQMM_E_NULL;

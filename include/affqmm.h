@@ -365,6 +365,178 @@ AFFQMM_API int affqmm_test_fault_wait(int64_t cycles);
 AFFQMM_API int affqmm_run_noalloc(const affqmm_weight* w, const uint16_t* x, int64_t M, uint16_t* y,
                                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * The paged key-value cache: what stands between a layer's q/k/v stack
+ * (affqmm_run_stacked) and its o projection (affqmm_run).  A pool of pages of
+ * `page` tokens; request r's token i sits in page table[r][i / page], at
+ * token i % page of it; a slot names a token of the pool, page number * page
+ * + token.  The method's pages have no counterpart to these entry points.
+ */
+
+/* Most requests of a call, and most query tokens of a request. */
+#define AFFQMM_PAGED_MAX_BATCH 16384
+#define AFFQMM_PAGED_MAX_TOKENS 64
+/* Types of the cache's values. */
+#define AFFQMM_KV_BF16 0
+#define AFFQMM_KV_E4M3 1   /* 8-bit floats, times a scale of their key head */
+
+/* A cache: a non-owning view of the pool's keys and values.
+ *   page          tokens of a page, a power of two up to 65536
+ *   heads, dim    key heads, and values of a head: a multiple of 16 up to 512
+ *   pages         pages of the pool; pages * page < 2^31
+ *   *_stride      elements between pages, tokens and heads (any order in
+ *                 memory; the values of a head are contiguous), each a multiple
+ *                 of 16 bytes
+ *   k, v          device, 16-byte aligned
+ *   k_scale, v_scale  device, fp32 [heads] or NULL (1): with AFFQMM_KV_E4M3, a
+ *                 value is the stored one times its head's scale; NULL with
+ *                 AFFQMM_KV_BF16 */
+typedef struct {
+    int32_t type;
+    int32_t page;
+    int32_t heads;
+    int32_t dim;
+    int64_t pages;
+    int64_t page_stride, token_stride, head_stride;
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+} affqmm_kv_cache;
+
+/* What affqmm_paged_plan writes, all device memory.
+ *   starts      int32 [batch + 1]: first token of each request in the step,
+ *               and the number of tokens
+ *   lens        int32 [batch]: tokens in the cache after the step
+ *   ring_state  int32 [2]: the ring's head and count after the step
+ *   slots       int32 [capacity], 16-byte aligned: each token's slot, -1 where
+ *               it has none
+ *   positions   int32 [capacity], 16-byte aligned: each token's place in its
+ *               request, 0 beyond the last token
+ *   requests    int32 [capacity], 16-byte aligned: each token's request, -1
+ *               beyond the last token
+ *   status      int32 [1]: 0, or the sum of 1 (the pool ran out), 2 (a request
+ *               outgrew its row of the table), 4 (more tokens than `capacity`),
+ *               8 (a negative count, a length beyond the table's row, or a ring
+ *               that cannot hold the pages it is said to) */
+typedef struct {
+    int64_t capacity;
+    int32_t *starts, *lens, *ring_state, *slots, *positions, *requests, *status;
+} affqmm_paged_step;
+
+/* A step's block tables, slot maps, positions and lengths, from the requests'
+ * lengths, in one launch.
+ *   batch         requests, up to AFFQMM_PAGED_MAX_BATCH
+ *   lens          device, int32 [batch]: tokens in the cache before the step
+ *   fresh         device, int32 [batch]: tokens that the step adds
+ *   finished      device, uint8 [batch] or NULL: nonzero gives the request's
+ *                 pages back (its `fresh` counts as 0, its new length is 0)
+ *   table         device, int32 [batch, wide], rows table_stride apart: entries
+ *                 below ceil(len / page) are the request's pages; the entries of
+ *                 pages that the step takes are written
+ *   ring          device, int32 [pool]: the free pages' numbers, `count` of them
+ *                 from `head` on (around the end); returned pages are written
+ *                 behind them
+ *   ring_state    device, int32 [2]: {head, count}
+ * Pages are taken from the ring's front in the order of the requests; a
+ * request's pages are in the order of its tokens.  A request is served if its
+ * tokens lie within `capacity`, its row of the table can hold them, and the
+ * pages taken by it and those before it are there (a request that needs no new
+ * page always passes the last).  One that is not served keeps its length, its
+ * tokens have no slot, and *status says why.  Pages returned in a step can be
+ * taken in the next.  The outputs must not overlap the inputs (lens and
+ * ring_state among them): the same call on the same inputs writes the same.
+ * Errors: E_NULL, E_SHAPE (batch, wide, pool, stride), E_ARG (page, capacity,
+ * overlap), E_ALIGN, E_CUDA. */
+AFFQMM_API int affqmm_paged_plan(int64_t batch, const int32_t* lens, const int32_t* fresh, const uint8_t* finished,
+                                 int32_t* table, int64_t table_stride, int64_t wide, int32_t* ring, int64_t pool,
+                                 const int32_t* ring_state, int page, const affqmm_paged_step* step, void* stream);
+
+/* Rotary positions.
+ *   turns     device, uint64 [rotary / 2]: the turns that pair i makes a
+ *             position, as a fraction of a turn times 2^64 (whole turns
+ *             dropped): floor(2^64 frac(frequency_i / 2 pi)); 0 leaves a pair
+ *             as it is
+ *   axis      device, uint8 [rotary / 2] or NULL (0): the axis by whose
+ *             position pair i turns
+ *   rotary    values of a head that turn: even, up to the head's dim; the rest
+ *             is left as it is
+ *   neighbour 0: pair i is values i and i + rotary / 2; 1: values 2i, 2i + 1
+ *   axes      rows of `positions` */
+typedef struct {
+    const uint64_t* turns;
+    const uint8_t* axis;
+    int32_t rotary;
+    int32_t neighbour;
+    int32_t axes;
+} affqmm_rope;
+
+/* Rows of heads: bf16, the values of a head contiguous; strides in elements,
+ * multiples of 8; 16-byte aligned. */
+typedef struct {
+    uint16_t* p;
+    int64_t token_stride, head_stride;
+} affqmm_rows;
+
+/* Rotary positions on q and k, and k and v written to their slots of the cache:
+ *     phi = 2 pi frac(position[axis_i] turns_i / 2^64)
+ *     (a, b) -> (a cos phi - b sin phi, a sin phi + b cos phi)
+ * in fp32, rounded once: to bf16, or for an AFFQMM_KV_E4M3 cache to e4m3 of the
+ * value over its head's scale (saturating at +-448).
+ *   q, out    [tokens, heads_q, dim] rows (views of a stacked projection's
+ *             output serve); out.p may be q.p with the same strides
+ *   k, v      [tokens, cache heads, dim] rows
+ *   positions device, int32 [axes, tokens], rows position_stride apart; any value
+ *   slots     device, int32 [tokens]; -1 writes nothing to the cache (its row of
+ *             q is still written)
+ *   status    device uint32 or NULL: a slot outside the pool writes nothing and
+ *             sets bit 1 of *status (the caller zeroes it beforehand)
+ * Two tokens of a call must not name one slot.  k and v must not overlap the
+ * cache.
+ * Errors: E_NULL, E_SHAPE, E_ALIGN, E_ARG, E_CUDA. */
+AFFQMM_API int affqmm_rope_append(const affqmm_kv_cache* cache, const affqmm_rope* rope, const affqmm_rows* q,
+                                  const affqmm_rows* k, const affqmm_rows* v, const affqmm_rows* out, int64_t tokens,
+                                  int heads_q, const int32_t* positions, int64_t position_stride,
+                                  const int32_t* slots, uint32_t* status, void* stream);
+
+/* Lanes of heads: as affqmm_rows, with a stride between requests. */
+typedef struct {
+    uint16_t* p;
+    int64_t batch_stride, token_stride, head_stride;
+} affqmm_lanes;
+
+/* Workspace of affqmm_paged_attention for this cache and these numbers of
+ * query tokens and heads, on the current device; the batch and the lengths do
+ * not matter.  Errors: E_NULL, E_SHAPE, E_ARG, E_DEVICE, E_CUDA. */
+AFFQMM_API int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cache, int tokens, int heads_q,
+                                                      size_t* bytes);
+
+/* Attention of each request's newest tokens over its pages: token j of request
+ * b, of `tokens`, stands at position lens[b] - tokens + j and sees the keys up
+ * to its own position, and of those the last `window` where window > 0:
+ *     out = softmax(scale q k^T) v,     lse = log sum exp(scale q k^T)
+ *   q, out    [batch, tokens, heads_q, dim] lanes; query heads h * group ..
+ *             h * group + group - 1 (group = heads_q / cache heads) read key
+ *             head h
+ *   lse       device, fp32 [batch, tokens, heads_q] contiguous, or NULL
+ *   table     device, int32 [batch, wide], rows table_stride apart
+ *   lens      device, int32 [batch]: tokens in the cache, the step's own
+ *             included; nothing behind them is read
+ *   scale     of the scores; finite
+ *   status    device uint32 or NULL: bit 1 is set for a length below 0 or beyond
+ *             the table's row (taken as 0, as the row's end) and for a visible
+ *             entry of the table that is no page (its keys and values are zeros)
+ *   workspace as affqmm_run: its first AFFQMM_WORKSPACE_ZEROED bytes zero before
+ *             the first use, shared with the other calls of a stream
+ * A token that sees no key gets zeros, and lse -infinity.  What the cache holds
+ * outside the visible keys (NaN, say) does not matter.  Sums are fp32; the
+ * probabilities keep 16 bits beside a bf16 cache, 11 beside an e4m3 one.  The same inputs give the same bits on a device.
+ * Errors: E_NULL, E_SHAPE, E_ALIGN, E_ARG, E_WORKSPACE, E_DEVICE, E_CUDA. */
+AFFQMM_API int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, const affqmm_lanes* out,
+                                      float* lse, int64_t batch, int tokens, int heads_q, const int32_t* table,
+                                      int64_t table_stride, int64_t wide, const int32_t* lens, float scale,
+                                      int window, uint32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
