@@ -1,6 +1,7 @@
 // affqmm_paged.h -- host-side declarations shared by the paged cache's
 // translation units (not part of the public ABI).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -51,8 +52,8 @@ struct AttnParams {
     uint16_t* out;
     float* lse;                  // [batch, tokens, heads_q] or null
     int64_t q_bs, q_ts, q_hs, o_bs, o_ts, o_hs;   // elements
-    const uint8_t *k, *v;
-    int64_t page_bytes, token_bytes, head_bytes, pages;
+    int64_t pages;
+    int32_t axis1, axis2, axis3; // what the cache's tensor maps have as axes 1 .. 3: 0 token, 1 head, 2 page
     const float *k_scale, *v_scale;
     const int32_t* table;
     int64_t table_stride;
@@ -70,14 +71,15 @@ struct AttnParams {
 struct AttnShape {
     int ctas_per_sm = 0;
     int rows = 0;                // rows of a tile (8 NT)
+    int keys = 0;                // and its keys
     size_t slot_floats = 0;
 };
-constexpr int kAttnKeys = 64;    // keys of a tile
 // DP: head dim padded to 64, 128, 256 or 512; rows: (token, head) rows that share a key head.
 #define AFFQMM_ATTN_DECL(DP)                                                                            \
     AttnShape attn_shape_##DP(bool e4m3, int rows);                                                     \
     cudaError_t attn_allow_smem_##DP();                                                                 \
-    cudaError_t launch_attn_##DP(bool e4m3, int rows, const AttnParams& p, int grid, cudaStream_t st);
+    cudaError_t launch_attn_##DP(bool e4m3, int rows, const AttnParams& p, const CUtensorMap& k,        \
+                                 const CUtensorMap& v, int grid, cudaStream_t st);
 AFFQMM_ATTN_DECL(64)
 AFFQMM_ATTN_DECL(128)
 AFFQMM_ATTN_DECL(256)

@@ -1,5 +1,6 @@
 // paged_api.cu -- the C ABI of the paged key-value cache: host-side validation
 // and the launches.  See include/affqmm.h for the contract.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -31,17 +32,17 @@ int check_cache(const affqmm_kv_cache* c, bool memory) {
     if (page_shift_of(c->page) < 0) return AFFQMM_E_ARG;
     if (c->type == AFFQMM_KV_BF16 && (c->k_scale || c->v_scale)) return AFFQMM_E_ARG;
     if (c->heads < 1 || c->heads > 4096 || c->dim < 16 || c->dim > 512 || c->dim % 16) return AFFQMM_E_SHAPE;
-    if (c->pages < 0 || c->pages * c->page >= (int64_t)1 << 31 || c->pages >= kMost) return AFFQMM_E_SHAPE;
-    if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0) return AFFQMM_E_SHAPE;
+    if (c->pages < 1 || c->pages >= kMost || c->pages * c->page >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
+    const int64_t size[3] = {c->pages, c->page, c->heads}, stride[3] = {c->page_stride, c->token_stride, c->head_stride};
+    for (int i = 0; i < 3; ++i)
+        if (size[i] > 1 && (stride[i] < c->dim || stride[i] >= (int64_t)1 << 38)) return AFFQMM_E_SHAPE;
     if (!memory) return AFFQMM_OK;
-    if (c->pages > 0) {
-        if (!c->k || !c->v) return AFFQMM_E_NULL;
-        const int64_t each = c->type == AFFQMM_KV_E4M3 ? 16 : 8;
-        if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % each || c->token_stride % each ||
-            c->head_stride % each)
-            return AFFQMM_E_ALIGN;
-        if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return AFFQMM_E_ALIGN;
-    }
+    if (!c->k || !c->v) return AFFQMM_E_NULL;
+    const int64_t each = c->type == AFFQMM_KV_E4M3 ? 16 : 8;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return AFFQMM_E_ALIGN;
+    for (int i = 0; i < 3; ++i)
+        if (size[i] > 1 && stride[i] % each) return AFFQMM_E_ALIGN;
     return AFFQMM_OK;
 }
 
@@ -70,11 +71,70 @@ int allow_attn(int which) {
     return g_ok[dev][which] ? AFFQMM_OK : AFFQMM_E_CUDA;
 }
 
-int which_dim(int dim) { return dim <= 64 ? 0 : dim <= 128 ? 1 : dim <= 256 ? 2 : 3; }
+// The kernels' padded head dim: 64 << this.  (e4m3 rows of 64 bytes cannot be
+// TMA's destination one by one: pages of one token take the next.)
+int which_dim(const affqmm_kv_cache* c) {
+    if (c->dim <= 64 && c->type == AFFQMM_KV_E4M3 && c->page == 1) return 1;
+    return c->dim <= 64 ? 0 : c->dim <= 128 ? 1 : c->dim <= 256 ? 2 : 3;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (EncodeTiledFn) nullptr;
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+
+// Tensor maps of the pool's K and V: values, then tokens, heads and pages in
+// the order of their strides (axis[i] says which is which: 0 token, 1 head, 2
+// page), read in boxes of one panel (up to 128 bytes) of the rows that a page
+// gives a tile.
+int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, CUtensorMap* v, int32_t (&axis)[3]) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return AFFQMM_E_CUDA;
+    const bool e4m3 = c->type == AFFQMM_KV_E4M3;
+    const int es = e4m3 ? 1 : 2, panel = padded * es < 128 ? padded * es : 128;
+    const int box = c->page < keys ? c->page : keys;
+    int64_t size[3] = {c->page, c->heads, c->pages};
+    int64_t stride[3] = {c->token_stride * es, c->head_stride * es, c->page_stride * es};
+    // an axis of one is never stepped along, whatever its stride says
+    for (int i = 0; i < 3; ++i)
+        if (size[i] == 1) stride[i] = (int64_t)1 << 36;
+    int order[3] = {0, 1, 2};
+    for (int i = 1; i < 3; ++i)
+        for (int j = i; j > 0 && stride[order[j]] < stride[order[j - 1]]; --j) {
+            const int t = order[j];
+            order[j] = order[j - 1];
+            order[j - 1] = t;
+        }
+    cuuint64_t dims[4] = {(cuuint64_t)c->dim}, strides[3];
+    cuuint32_t boxes[4] = {(cuuint32_t)(panel / es)}, steps[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        axis[i] = order[i];
+        dims[i + 1] = (cuuint64_t)size[order[i]];
+        strides[i] = (cuuint64_t)stride[order[i]];
+        boxes[i + 1] = order[i] == 0 ? (cuuint32_t)box : 1u;
+    }
+    for (int kv = 0; kv < 2; ++kv)
+        if (enc(kv ? v : k, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv ? c->v : c->k, dims,
+                strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                panel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return AFFQMM_E_CUDA;
+    return AFFQMM_OK;
+}
 
 AttnShape attn_shape(const affqmm_kv_cache* c, int rows) {
     const bool e4m3 = c->type == AFFQMM_KV_E4M3;
-    switch (which_dim(c->dim)) {
+    switch (which_dim(c)) {
         case 0: return attn_shape_64(e4m3, rows);
         case 1: return attn_shape_128(e4m3, rows);
         case 2: return attn_shape_256(e4m3, rows);
@@ -229,20 +289,18 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     const AttnShape shape = attn_shape(cache, rows);
     if (!workspace || ws_bytes < attn_workspace(shape, sms)) return AFFQMM_E_WORKSPACE;
     if (!aligned(workspace, 256)) return AFFQMM_E_ALIGN;
-    const int which = which_dim(cache->dim);
+    const int which = which_dim(cache);
     if ((rc = allow_attn(which))) return rc;
 
     const bool e4m3 = cache->type == AFFQMM_KV_E4M3;
-    const int es = e4m3 ? 1 : 2;
     AttnParams p = {};
+    CUtensorMap k_map, v_map;
+    int32_t axis[3];
+    if ((rc = cache_maps(cache, 64 << which, shape.keys, &k_map, &v_map, axis))) return rc;
+    p.axis1 = axis[0], p.axis2 = axis[1], p.axis3 = axis[2];
     p.q = q->p, p.q_bs = q->batch_stride, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
     p.out = out->p, p.o_bs = out->batch_stride, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
     p.lse = lse;
-    p.k = static_cast<const uint8_t*>(cache->k);
-    p.v = static_cast<const uint8_t*>(cache->v);
-    p.page_bytes = cache->page_stride * es;
-    p.token_bytes = cache->token_stride * es;
-    p.head_bytes = cache->head_stride * es;
     p.pages = cache->pages;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
@@ -268,17 +326,18 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     // one CTA for each that the SMs hold, or for each tile that the tables have room for
     const int64_t row_keys = wide * cache->page;
     int64_t keys = row_keys;
-    if (window > 0 && keys > (int64_t)window + tokens + 14) keys = (int64_t)window + tokens + 14;   // from a multiple of 16 on
-    const int64_t tiles = batch * cache->heads * p.row_tiles * (keys < kAttnKeys ? 1 : (keys + kAttnKeys - 1) / kAttnKeys);
+    // a window's keys, from a multiple of a tile on
+    if (window > 0 && keys > (int64_t)window + tokens + shape.keys) keys = (int64_t)window + tokens + shape.keys;
+    const int64_t tiles = batch * cache->heads * p.row_tiles * (keys < shape.keys ? 1 : (keys + shape.keys - 1) / shape.keys);
     const int64_t most = (int64_t)sms * shape.ctas_per_sm;
     const int grid = (int)(tiles < most ? tiles : most);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (which) {
-        case 0: e = launch_attn_64(e4m3, rows, p, grid, st); break;
-        case 1: e = launch_attn_128(e4m3, rows, p, grid, st); break;
-        case 2: e = launch_attn_256(e4m3, rows, p, grid, st); break;
-        default: e = launch_attn_512(e4m3, rows, p, grid, st); break;
+        case 0: e = launch_attn_64(e4m3, rows, p, k_map, v_map, grid, st); break;
+        case 1: e = launch_attn_128(e4m3, rows, p, k_map, v_map, grid, st); break;
+        case 2: e = launch_attn_256(e4m3, rows, p, k_map, v_map, grid, st); break;
+        default: e = launch_attn_512(e4m3, rows, p, k_map, v_map, grid, st); break;
     }
     return e == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
 }

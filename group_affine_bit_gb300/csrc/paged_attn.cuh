@@ -9,13 +9,17 @@
 // read once, and the matrix work beside it is small (rows that share a key
 // head: query heads of the group x tokens, 1 .. 64 to a tile).
 //
-// Roles.  A CTA has four consumer warps, one producer warp for K, one for V
-// and one for q.  A tile is 64 keys.  The producers gather its rows through
-// the block table (the next tile's entries are fetched ahead) with 16-byte
-// asynchronous copies into a ring that K and V tiles share in turn; rows that
-// no query may see, or whose table entry is out of range, are filled with
-// zeros and not read.  They run ahead of the consumers across the borders of
-// requests, so the memory pipeline does not drain there.
+// Roles.  A CTA has four consumer warps, two producer warps and one for q.  A
+// tile is 64 or 128 keys.  The producers (one for K, one for V) gather it through the
+// block table with TMA, a box to a page's rows of the tile, in 128-byte panels
+// whose swizzle keeps the fragment loads free of bank conflicts; K and V tiles
+// take turns in one ring.  Rows of pages that no
+// query may see are not read, an entry that is no page reads as zeros, and
+// what lies in a tile beyond the visible keys is masked out by the consumers.
+// The producers run ahead across the borders of requests, so the memory
+// pipeline does not drain there.  (Gathering with 16-byte cp.async copies, two
+// producer warps, cost 54-97 cycles of a warp for each 512 bytes: 58 % of the
+// copy rate for e4m3 pages, 71 % at dim 256.)
 //
 // Arithmetic.  Keys are the M side of the matrix instruction (m16n8k16) and
 // query rows its N side, so that one to eight rows cost one instruction per 16
@@ -35,9 +39,13 @@
 //
 // Split.  All tiles of all (request, key head, row tile) units, in order, are
 // cut into equal runs, one per CTA, so a batch of ragged lengths loads every
-// SM alike; each CTA finds its run by a prefix sum over the lengths.  A unit
-// that several runs share is joined by the CTA that finishes last, in run
-// order: the same inputs give the same bits.
+// SM alike; each CTA finds its run by a prefix sum over the lengths.  The runs
+// that share a unit leave their parts in slots of the workspace and count in;
+// one of them joins the parts, always in run order, so that the same inputs
+// give the same bits.  A part that a run begins with is counted in by the q
+// warp while the consumers go on; a run that ends with a unit's first part
+// keeps it in registers if the others are in by then, as they mostly are;
+// else the last to count in joins.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,6 +53,7 @@
 #include "affqmm_async.cuh"
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
+#include "affqmm_tc.cuh"
 
 namespace affqmm {
 namespace attn {
@@ -52,11 +61,10 @@ namespace attn {
 constexpr int W = 4;                       // consumer warps
 constexpr int CONSUMERS = 32 * W;
 constexpr int THREADS = 32 * (W + 3);
-constexpr int KEYS = kAttnKeys;
 constexpr float LAZY = 8.f;                // log2 of how far a score may exceed the running maximum
 constexpr size_t SM_SMEM = 233472;         // shared memory of an SM, 1 KB of it taken by each CTA
 constexpr size_t CTA_SMEM = 232448;        // and what one CTA may have of it
-constexpr size_t STATIC_SMEM = 512;        // above the kernel's few static variables
+constexpr size_t STATIC_SMEM = 1024;       // the kernel's few static variables, and the ring's alignment
 constexpr int MAX_SLOTS = 16;
 
 template <int DP, int NT, bool E4M3>
@@ -64,22 +72,30 @@ struct Cfg {
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int ROWS = 8 * NT;
     static constexpr int PITCH = DP * ES;              // bytes of a cache row in shared memory
-    static constexpr int CH = PITCH / 16;              // its 16-byte chunks
+    static constexpr int PW = PITCH < 128 ? PITCH : 128;   // bytes of a row in one panel
+    static constexpr int PANELS = PITCH / PW;
+    // Rows of 128 bytes or less: two blocks of 16 keys to a warp, so that two chains of matrix
+    // instructions overlap and the barrier comes half as often (e4m3, dim 128).
+    static constexpr int KB = PITCH <= 128 && NT <= 2 ? 2 : 1;
+    static constexpr int KEYS = 16 * W * KB;
     static constexpr int TILE = KEYS * PITCH;
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int QBUF = (DP == 512 && NT > 1) ? 1 : 2;
     static constexpr int PN = E4M3 ? 1 : 2;            // numbers that make one P
-    static constexpr int PBYTES = PN * NT * KEYS * 16; // [PN][NT][64 keys][8 rows] of 16 bits
     static constexpr int LOW = NT * KEYS * 16;         // from the first numbers to the second
+    static constexpr int PBYTES = PN * LOW;            // [PN][NT][keys][8 rows] of 16 bits
     static constexpr int MT = DP / (16 * W);           // 16-dim tiles of a consumer warp
-    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + QBUF * ROWS * 4 + 1024;
-    static constexpr bool LIGHT = MT * NT * 4 + NT * 8 <= 64;   // registers allow two CTAs an SM
+    static constexpr int JOIN = NT <= 2 ? 32 : 64 / NT;         // parts whose weights a join holds at a time
+    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + QBUF * ROWS * 4 +
+                                    JOIN * ROWS * 4 + 512;
+    static constexpr bool LIGHT = MT * NT * 4 + NT * 8 <= 32;   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
-    static constexpr int CPS = (LIGHT && FIXED + 4 * TILE <= HALF) ? 2 : 1;
+    static constexpr int CPS = (LIGHT && FIXED + 3 * TILE <= HALF) ? 2 : 1;
     static constexpr size_t ROOM = (CPS == 2 ? HALF : CTA_SMEM - STATIC_SMEM) - FIXED;
     static constexpr int NS = ROOM / TILE > MAX_SLOTS ? MAX_SLOTS : (int)(ROOM / TILE);
     static constexpr size_t SMEM = FIXED + (size_t)NS * TILE;
-    static constexpr size_t SLOT_FLOATS = (size_t)W * MT * NT * 32 * 4 + 2 * ROWS;
+    static constexpr size_t STATS = (size_t)W * MT * NT * 128;  // of a partial slot: the accumulators, then [row]{m, l}
+    static constexpr size_t SLOT_FLOATS = STATS + 2 * ROWS;
     static_assert(NS >= 3, "ring too short");
 };
 
@@ -126,12 +142,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16u : 0u) : "memory");
-}
-// arrive on `bar` when this thread's copies so far have landed (counted in the barrier's own count)
-__device__ __forceinline__ void cp_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool consumer_any(bool v) {
@@ -141,18 +158,25 @@ __device__ __forceinline__ bool consumer_any(bool v) {
         : "=r"(r) : "r"((uint32_t)v) : "memory");
     return r != 0;
 }
-// 16-byte chunk `c` of row `row` of a tile whose rows have CH chunks: the
-// eight rows that one ldmatrix phase reads fall into eight bank groups.
-template <int CH>
+// 16-byte chunk `c` of row `row` of a tile: panels of PW bytes of every row,
+// swizzled as TMA swizzles rows of 128 (64) bytes, so that the eight rows that
+// one fragment load reads fall into eight bank groups.
+template <int PW, int KEYS>
 __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
-    if constexpr (CH >= 8) return (uint32_t)(row * CH + (c ^ (row & 7))) * 16u;
-    else return (uint32_t)(row * CH + (c ^ ((row >> 1) & (CH - 1)))) * 16u;
+    if constexpr (PW == 128) return (uint32_t)((c >> 3) * KEYS * 128 + row * 128 + ((c & 7) ^ (row & 7)) * 16);
+    else return (uint32_t)(row * 64 + (c ^ ((row >> 1) & 3)) * 16);
+}
+// The same of q, whose rows are whole (CH chunks).
+template <int CH>
+__device__ __forceinline__ uint32_t qchunk_at(int row, int c) {
+    return (uint32_t)(row * CH + (c ^ (row & 7))) * 16u;
 }
 
 // What a request's tiles cover: keys lo .. hi - 1, tiles counted from `base`.
 struct Span {
     int len, lo, hi, base, tiles;
 };
+template <int KEYS>
 __device__ __forceinline__ Span span_of(const AttnParams& p, int b) {
     Span s;
     const int64_t most = (int64_t)p.wide << p.page_shift;
@@ -161,12 +185,13 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int b) {
     s.len = max(len, 0);
     s.hi = s.len;
     s.lo = p.window > 0 ? max(0, s.len - p.tokens + 1 - p.window) : 0;
-    s.base = s.lo & ~15;
+    s.base = s.lo & ~(KEYS - 1);
     s.tiles = max(1, (s.hi - s.base + KEYS - 1) / KEYS);
     return s;
 }
 
 // The CTA's run, segment by segment: unit (request b, u = key head * row tiles + row tile), tiles t0 .. t1 - 1.
+template <int KEYS>
 struct Walk {
     int b, u, t, t0, t1;
     int64_t left;      // tiles of the run not yet handed out
@@ -180,7 +205,7 @@ struct Walk {
             if (++u == units) {
                 u = 0;
                 ++b;
-                s = span_of(p, b);
+                s = span_of<KEYS>(p, b);
             }
         }
         t0 = t;
@@ -192,42 +217,52 @@ struct Walk {
 };
 
 template <int DP, int NT, bool E4M3>
-__global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_kernel(
+    const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = Cfg<DP, NT, E4M3>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int KEYS = C::KEYS;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
     uint8_t* qbuf = ring + (size_t)C::NS * C::TILE;
     uint8_t* pbuf = qbuf + C::QBUF * C::QBYTES;
     float* red = reinterpret_cast<float*>(pbuf + 2 * C::PBYTES);      // [W][ROWS] maxima
     float* lred = red + W * C::ROWS;                                  // [W][ROWS] sums
     float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: what undoes q's power of two
-    uint64_t* bars = reinterpret_cast<uint64_t*>(qscale + C::QBUF * C::ROWS);
+    float* weight = qscale + C::QBUF * C::ROWS;                       // [JOIN][ROWS] of a join's parts
+    uint64_t* bars = reinterpret_cast<uint64_t*>(weight + C::JOIN * C::ROWS);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (MAX_SLOTS + s); };
     auto qfull = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + s); };
     auto qempty = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + 2 + s); };
+    const uint32_t stored = bar0 + 8u * (2 * MAX_SLOTS + 4);     // the run's first part is in its slot
+    const uint32_t counted = stored + 8u;                        // and has been counted in
+    const uint32_t finished = stored + 16u;                      // the run's last tile has been added
+    const uint32_t decided = stored + 24u;                       // whether the other parts of its unit are there
     __shared__ int64_t sums[THREADS / 32];
     __shared__ int64_t run_tiles, run_unit0, run_total, run_at;
     __shared__ int run_b;
-    __shared__ uint32_t last_flag;
+    __shared__ uint32_t last_flag, late_join, others_in;
 
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < C::NS; ++s) {
-            mbar_init(full(s), 32);
+            mbar_init(full(s), 1);
             mbar_init(empty(s), W);
         }
         for (int s = 0; s < C::QBUF; ++s) {
             mbar_init(qfull(s), 32);
             mbar_init(qempty(s), W);
         }
+        mbar_init(stored, W);
+        mbar_init(counted, 1);
+        mbar_init(finished, W);
+        mbar_init(decided, 1);
         fence_mbar_init();
     }
-    // columns beyond the head's dim stay zero: nothing is copied there
-    if (p.dim < DP) {
-        uint4* z = reinterpret_cast<uint4*>(ring);
-        for (int i = tid; i < C::NS * C::TILE / 16; i += THREADS) z[i] = make_uint4(0, 0, 0, 0);
+    if (wid == W && lane == 0) {
+        prefetch_tmap(&k_map);
+        prefetch_tmap(&v_map);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -240,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         for (int b = b0; b < b1; ++b) {
             if (blockIdx.x == 0 && p.user_status && (p.lens[b] < 0 || p.lens[b] > ((int64_t)p.wide << p.page_shift)))
                 atomicOr(p.user_status, 2u);
-            mine += (int64_t)span_of(p, b).tiles * units;
+            mine += (int64_t)span_of<KEYS>(p, b).tiles * units;
         }
         int64_t x = mine;
 #pragma unroll
@@ -259,13 +294,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         before += x - mine;
         // no run is empty: with fewer tiles than CTAs, the first `total` CTAs take one each
         const int64_t ctas = min((int64_t)gridDim.x, total), c = min((int64_t)blockIdx.x, ctas);
-        const int64_t r0 = total * c / ctas, r1 = c < ctas ? total * (c + 1) / ctas : r0;
+        int64_t r0, r1;
+        if (total < (int64_t)1 << 31) {   // the quotient in 32 bits: c total / ctas = c (total / ctas) + c (total % ctas) / ctas
+            const uint32_t n = (uint32_t)total, d = (uint32_t)ctas, per = n / d, over = n - per * d, cc = (uint32_t)c;
+            r0 = (int64_t)(cc * per + cc * over / d);
+            r1 = cc < d ? (int64_t)((cc + 1) * per + (cc + 1) * over / d) : r0;
+        } else {
+            r0 = total * c / ctas;
+            r1 = c < ctas ? total * (c + 1) / ctas : r0;
+        }
         if (tid == 0) run_tiles = r1 - r0, run_total = total;
         if (r1 > r0 && before <= r0 && r0 < before + mine) {
             int64_t at = before;
             int b = b0;
             for (;; ++b) {
-                const int64_t n = (int64_t)span_of(p, b).tiles * units;
+                const int64_t n = (int64_t)span_of<KEYS>(p, b).tiles * units;
                 if (r0 < at + n) break;
                 at += n;
             }
@@ -277,10 +320,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     }
     if (run_tiles == 0) return;
     const int64_t all_tiles = run_total, ctas = min((int64_t)gridDim.x, all_tiles);
-    Walk walk;
+    Walk<KEYS> walk;
     walk.b = run_b;
-    walk.s = span_of(p, walk.b);
-    walk.u = (int)(run_at / walk.s.tiles);
+    walk.s = span_of<KEYS>(p, walk.b);
+    walk.u = run_at < (int64_t)1 << 31 ? (int)run_at / walk.s.tiles : (int)(run_at / walk.s.tiles);
     walk.t = (int)(run_at - (int64_t)walk.u * walk.s.tiles);
     walk.unit0 = run_unit0 + (int64_t)walk.u * walk.s.tiles;
     walk.left = run_tiles;
@@ -292,70 +335,110 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     if (wid == W || wid == W + 1) {
         // ================= producers: K tiles take the ring's even turns, V tiles the odd ones
         const bool is_v = wid == W + 1;
-        const uint8_t* cache = is_v ? p.v : p.k;
-        constexpr int CH = C::CH, RPI = CH >= 32 ? 1 : 32 / CH;     // rows of one warp-wide copy
-        constexpr int IPR = CH > 32 ? CH / 32 : 1;                  // copies of one row
-        const int chunk = CH >= 32 ? lane : lane % CH, row_in = CH >= 32 ? 0 : lane / CH;
-        const int real_chunks = p.dim * C::ES / 16;
+        const CUtensorMap* map = is_v ? &v_map : &k_map;
+        const int box_shift = min(p.page_shift, KEYS == 128 ? 7 : 6), box = 1 << box_shift;
         const uint32_t page_mask = (1u << p.page_shift) - 1u;
         const uint32_t ring_u = smem_u32(ring);
+        const uint32_t box_bytes = (uint32_t)box * C::PW;
         int slot = is_v ? 1 : 0;
         uint32_t phase = 0;
-        while (walk.next(p, units)) {
-            const Span& s = walk.s;
+        int64_t turn = slot;                 // of the ring, over the whole run
+        while (ok && walk.next(p, units)) {
+            const Span s = walk.s;
             const int32_t* table = p.table + (int64_t)walk.b * p.table_stride;
-            const int64_t head = (int64_t)(walk.u / p.row_tiles) * p.head_bytes;
-            // the offset of the cache row of key `key`, or -1: a row of zeros
-            auto entry_of = [&](int key) { return key >= s.lo && key < s.hi ? table[key >> p.page_shift] : -1; };
-            auto offset_of = [&](int key, int entry) -> int64_t {
-                const bool seen = key >= s.lo && key < s.hi;
-                if (!seen) return -1;
-                if ((uint32_t)entry >= (uint64_t)p.pages) {
-                    if (p.user_status) atomicOr(p.user_status, 2u);
-                    return -1;
-                }
-                return (int64_t)entry * p.page_bytes + (int64_t)((uint32_t)key & page_mask) * p.token_bytes + head;
-            };
-            int key0 = s.base + walk.t0 * KEYS;
-            int e0 = entry_of(key0 + lane), e1 = entry_of(key0 + 32 + lane);
-            for (int t = walk.t0; t < walk.t1; ++t, key0 += KEYS) {
-                const int64_t off0 = offset_of(key0 + lane, e0), off1 = offset_of(key0 + 32 + lane, e1);
-                if (t + 1 < walk.t1) {
-                    e0 = entry_of(key0 + KEYS + lane);
-                    e1 = entry_of(key0 + KEYS + 32 + lane);
-                }
-                wait(empty(slot), phase ^ 1u);
-                if (!ok) break;
-                const uint32_t dst = ring_u + (uint32_t)slot * C::TILE;
-#pragma unroll 8
-                for (int i = 0; i < KEYS / RPI; ++i) {
-                    const int row = i * RPI + row_in;
-                    const int64_t off = __shfl_sync(~0u, i < KEYS / RPI / 2 ? off0 : off1, row & 31);
-#pragma unroll
-                    for (int c = 0; c < IPR; ++c) {
-                        const int ch = chunk + 32 * c;
-                        if (ch < real_chunks)
-                            cp16(dst + chunk_at<CH>(row, ch), cache + (off < 0 ? 0 : off + ch * 16), off >= 0);
+            const int head = walk.u / p.row_tiles;
+            // 32 entries of the table in the lanes' registers and the next 32 on their way, so that no tile
+            // waits for its entries; one that is no page becomes a page beyond the tensor, which reads as zeros
+            auto entries = [&](int first) {
+                const int e = first + lane;
+                int page = (int)p.pages;
+                if (((int64_t)e << p.page_shift) < s.hi && (((int64_t)e + 1) << p.page_shift) > s.lo) {
+                    page = table[e];
+                    if ((uint32_t)page >= (uint64_t)p.pages) {
+                        page = (int)p.pages;
+                        if (p.user_status) atomicOr(p.user_status, 2u);
                     }
                 }
-                cp_arrive(full(slot));
+                return page;
+            };
+            int key0 = s.base + walk.t0 * KEYS;
+            int have = (key0 >> p.page_shift) & ~31;
+            int cur = entries(have), nxt = entries(have + 32);
+            for (int t = walk.t0; t < walk.t1; ++t, key0 += KEYS) {
+                while ((key0 >> p.page_shift) - have >= 32) {
+                    have += 32;
+                    cur = nxt;
+                    nxt = entries(have + 32);
+                }
+                // the tile's boxes that hold a visible key
+                const int i0 = max(0, s.lo - key0) >> box_shift, i1 = (min(KEYS, s.hi - key0) + box - 1) >> box_shift;
+                wait(empty(slot), phase ^ 1u);
+                if (!ok) break;
+                const uint32_t dst = ring_u + (uint32_t)slot * C::TILE, bar = full(slot);
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::PANELS * box_bytes);
+                __syncwarp();
+                for (int i = i0; i < i1; ++i) {
+                    const int row = i << box_shift;
+                    int e = ((key0 + row) >> p.page_shift) - have;
+                    while (e >= 32) {        // pages of few tokens: a tile takes more than 32 entries
+                        have += 32;
+                        e -= 32;
+                        cur = nxt;
+                        nxt = entries(have + 32);
+                    }
+                    const int page = __shfl_sync(~0u, cur, e);
+                    const int token = (int)((uint32_t)(key0 + row) & page_mask);
+                    auto at = [&](int axis) { return axis == 0 ? token : axis == 1 ? head : page; };
+                    const int c1 = at(p.axis1), c2 = at(p.axis2), c3 = at(p.axis3);
+                    if (lane == 0)
+#pragma unroll
+                        for (int n = 0; n < C::PANELS; ++n)
+                            tma_load_4d(dst + n * KEYS * C::PW + row * C::PW, map, n * (C::PW / C::ES), c1, c2, c3, bar);
+                }
+                turn += 2;
                 slot += 2;
                 if (slot >= C::NS) slot -= C::NS, phase ^= 1u;
             }
-            if (!ok) break;
         }
+        // no copy is in flight when the CTA ends, whatever its consumers did
+        for (int64_t i = turn - 2; i >= 0 && i >= turn - C::NS; i -= 2)
+            if (!mbar_wait(full((int)(i % C::NS)), (uint32_t)(i / C::NS) & 1u)) ok = false;
         if (!ok && lane == 0) atomicOr(p.status, 1u);
-        asm volatile("cp.async.wait_all;" ::: "memory");
         return;
     }
+    // The parts of a unit that begins at tile `unit0`: the runs from c_first on.
+    struct Parts {
+        int64_t first;
+        int count;
+    };
+    auto parts_of = [&](int64_t unit0, int tiles) {
+        Parts x;
+        x.first = ((unit0 + 1) * ctas - 1) / all_tiles;
+        x.count = (int)(((unit0 + tiles) * ctas - 1) / all_tiles - x.first) + 1;
+        return x;
+    };
     if (wid == W + 2) {
-        // ================= q of each segment, rows (token, head of the group), in the matrix type
-        int qs = 0;
+        // ================= q of each segment, rows (token, head of the group), in the matrix type; and the
+        // counting in of parts, so that consumers do not wait for it: their own counter of a unit's parts is
+        // the first run's
+        int qs = 0, segment = 0;
         uint32_t phase = 0;
         const int rows = p.tokens * p.group;
+        bool early = false;                  // the run's first segment is a part, and not the run's last
+        Parts parts = {};
+        auto count_in = [&] {                // the first segment's part, once its consumers have stored it
+            wait(stored, 0);
+            if (lane == 0) {
+                fence_acq_rel_gpu();
+                const bool last = atomicAdd(p.counters + parts.first, 1u) == (uint32_t)parts.count - 1;
+                fence_acq_rel_gpu();
+                late_join = last;
+                mbar_arrive(counted);
+            }
+            early = false;
+        };
         while (walk.next(p, units)) {
             wait(qempty(qs), phase ^ 1u);
-            if (!ok) break;
             uint8_t* dst = qbuf + qs * C::QBYTES;
             const int hk = walk.u / p.row_tiles, r0 = (walk.u % p.row_tiles) * C::ROWS;
             constexpr int QCH = DP / 8;                             // 16-byte chunks of a row
@@ -401,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                             for (int e = 0; e < 4; ++e) {
                                 const int pair = 4 * h + e;         // dims 2 pair, 2 pair + 1 of the 16
                                 const int k = (pair >> 1) * 2 + (pair & 1) * 8;
-                                *reinterpret_cast<uint32_t*>(dst + chunk_at<QCH>(r, 2 * step + (k >> 3)) + (k & 7) * 2) = v[e];
+                                *reinterpret_cast<uint32_t*>(dst + qchunk_at<QCH>(r, 2 * step + (k >> 3)) + (k & 7) * 2) = v[e];
                             }
                         }
                     }
@@ -409,12 +492,34 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll
                     for (int c = 0; c < PER; ++c) {
                         const int ch = lane + 32 * c;
-                        if (ch < QCH) *reinterpret_cast<uint4*>(dst + chunk_at<QCH>(r, ch)) = w[c];
+                        if (ch < QCH) *reinterpret_cast<uint4*>(dst + qchunk_at<QCH>(r, ch)) = w[c];
                     }
                 }
             }
             mbar_arrive(qfull(qs));
             if (++qs == C::QBUF) qs = 0, phase ^= 1u;
+            if (early) count_in();
+            if (segment++ == 0 && walk.t0 > 0 && walk.left > 0) {
+                early = true;
+                parts = parts_of(walk.unit0, walk.s.tiles);
+            }
+        }
+        if (walk.t0 == 0 && walk.t1 < walk.s.tiles) {
+            // the run ends with its unit's first part: the other parts' runs mostly began with theirs, so
+            // look for them while the last tiles are added
+            if (lane == 0) {
+                const Parts x = parts_of(walk.unit0, walk.s.tiles);
+                const uint32_t* counter = p.counters + x.first;
+                uint32_t in = 0;
+                const long long t_begin = clock64();
+                for (;;) {
+                    const bool over = mbar_try_wait(finished, 0);
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(in) : "l"(counter) : "memory");
+                    if (over || in == (uint32_t)x.count - 1 || clock64() - t_begin > kWaitLimitCycles) break;
+                }
+                others_in = in == (uint32_t)x.count - 1;
+                mbar_arrive(decided);
+            }
         }
         if (!ok && lane == 0) atomicOr(p.status, 1u);
         return;
@@ -422,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 
     // ===================== consumers
     const int g = lane >> 2, t2 = (lane & 3) * 2;
-    constexpr int MT = C::MT, QCH = DP / 8;
+    constexpr int MT = C::MT, QCH = DP / 8, KB = C::KB;
     int slot = 0, qs = 0;
     uint32_t phase = 0, qphase = 0;
     const uint32_t ring_u = smem_u32(ring), qbuf_u = smem_u32(qbuf), pbuf_u = smem_u32(pbuf);
@@ -434,21 +539,190 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         if (lane == 0) mbar_arrive(empty(slot));
         if (++slot == C::NS) slot = 0, phase ^= 1u;
     };
+    auto clear = [&] {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+    };
+    auto slot_of = [&](const Parts& x, int i) { return p.slots + (size_t)(2 * (x.first + i) + (i == 0 ? 1 : 0)) * C::SLOT_FLOATS; };
 
+    // this run's part of a unit, to its slot
+    auto store_part = [&](bool first) {
+        float4* part = reinterpret_cast<float4*>(p.slots + (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * C::SLOT_FLOATS);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                __stcg(part + ((wid * MT + mt) * NT + nt) * 32 + lane,
+                       make_float4(acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]));
+        if (wid == 0 && g == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                __stcg(reinterpret_cast<float4*>(reinterpret_cast<float*>(part) + C::STATS + 2 * (8 * nt + t2)),
+                       make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]));
+    };
+
+    // The parts of a unit joined, in run order: acc, m and l of the whole.  `own`: this run has the first part,
+    // in registers; the same sums come out as if it were read from its slot.
+    auto join = [&](const Parts& x, bool own) {
+        constexpr int JOIN = C::JOIN, TPR = CONSUMERS / C::ROWS, PER = JOIN / TPR;   // threads of a row, and its parts to a thread
+        constexpr int MOST = C::CPS == 2 ? 8 : 16, BATCH = MT * NT >= MOST ? 1 : MOST / (MT * NT);    // parts whose loads are in flight at once
+        const int row = tid % C::ROWS, p0 = tid / C::ROWS;
+        if (own && wid == 0 && g == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) red[8 * nt + t2 + e] = m[nt][e], red[C::ROWS + 8 * nt + t2 + e] = l[nt][e];
+        consumer_sync();
+        float top = NINF, sum = 0.f;
+        if (!own) clear();
+        for (int c0 = 0; c0 < x.count; c0 += JOIN) {
+            const int n = min(JOIN, x.count - c0);
+            const bool mine0 = own && c0 == 0;           // part 0 of this chunk is in registers
+            float2 st[PER];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int i = p0 + k * TPR;
+                st[k] = make_float2(NINF, 0.f);
+                if (i < n) {
+                    if (mine0 && i == 0) st[k] = make_float2(red[row], red[C::ROWS + row]);
+                    else st[k] = __ldcg(reinterpret_cast<const float2*>(slot_of(x, c0 + i) + C::STATS + 2 * row));
+                }
+            }
+            float4 a[BATCH][MT][NT];
+            auto fetch = [&](int i0) {
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            if (i0 + i < n)
+                                a[i][mt][nt] = __ldcg(reinterpret_cast<const float4*>(slot_of(x, c0 + i0 + i)) +
+                                                      ((wid * MT + mt) * NT + nt) * 32 + lane);
+            };
+            fetch(mine0 ? 1 : 0);                        // with the statistics, in one round trip
+            float high = NINF;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) high = fmaxf(high, st[k].x);
+            weight[tid] = high;
+            consumer_sync();
+#pragma unroll
+            for (int i = 0; i < TPR; ++i) high = fmaxf(high, weight[i * C::ROWS + row]);
+            high = fmaxf(high, top);
+            const float f = top == high ? 1.f : exp2_approx(top - high);
+            sum *= f;
+            top = high;
+            if (p0 == 0) red[row] = f;
+            consumer_sync();
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int i = p0 + k * TPR;
+                if (i < n) {
+                    const float w = st[k].x == top ? 1.f : exp2_approx(st[k].x - top);
+                    weight[i * C::ROWS + row] = w;
+                    sum += w * st[k].y;
+                }
+            }
+            consumer_sync();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 k = *reinterpret_cast<const float2*>(red + 8 * nt + t2);
+                if (mine0) k = *reinterpret_cast<const float2*>(weight + 8 * nt + t2);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    acc[mt][nt][0] *= k.x, acc[mt][nt][1] *= k.y, acc[mt][nt][2] *= k.x, acc[mt][nt][3] *= k.y;
+            }
+            for (int i0 = mine0 ? 1 : 0; i0 < n;) {
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    if (i0 + i < n)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float2 w = *reinterpret_cast<const float2*>(weight + (i0 + i) * C::ROWS + 8 * nt + t2);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                acc[mt][nt][0] = fmaf(w.x, a[i][mt][nt].x, acc[mt][nt][0]);
+                                acc[mt][nt][1] = fmaf(w.y, a[i][mt][nt].y, acc[mt][nt][1]);
+                                acc[mt][nt][2] = fmaf(w.x, a[i][mt][nt].z, acc[mt][nt][2]);
+                                acc[mt][nt][3] = fmaf(w.y, a[i][mt][nt].w, acc[mt][nt][3]);
+                            }
+                        }
+                i0 += BATCH;
+                if (i0 < n) fetch(i0);
+            }
+            consumer_sync();                             // `weight` and `red` serve the next chunk
+        }
+        weight[tid] = sum;
+        if (p0 == 0) red[row] = top;
+        consumer_sync();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nt + t2 + e;
+                m[nt][e] = red[r];
+                float z = 0.f;
+#pragma unroll
+                for (int i = 0; i < TPR; ++i) z += weight[i * C::ROWS + r];
+                l[nt][e] = z;
+            }
+        if (tid == 0) p.counters[x.first] = 0;           // every part has counted in: zero for the next call
+        consumer_sync();                                 // `weight` and `red` serve what follows
+    };
+
+    auto write_out = [&](int b, int u, int len, float v_scale) {
+        if (!ok) return;
+        const int hk = u / p.row_tiles, r0 = (u % p.row_tiles) * C::ROWS;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * nt + t2 + e;
+                const int j = r / p.group, hq = hk * p.group + (r - j * p.group);
+                if (j >= p.tokens) continue;
+                // a row that sees no key is zero; otherwise its sum is positive, or NaN as its scores are
+                const bool none = len - p.tokens + j + 1 <= 0;
+                const float inv = v_scale / l[nt][e];
+                uint16_t* o = p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int d = (wid * MT + mt) * 16 + (E4M3 ? 2 * g : g);
+                    const __nv_bfloat16 x = __float2bfloat16_rn(none ? 0.f : acc[mt][nt][e] * inv);
+                    const __nv_bfloat16 y = __float2bfloat16_rn(none ? 0.f : acc[mt][nt][e + 2] * inv);
+                    if (d < p.dim) {
+                        if constexpr (E4M3) {
+                            *reinterpret_cast<__nv_bfloat162*>(o + d) = __nv_bfloat162(x, y);
+                        } else {
+                            *reinterpret_cast<__nv_bfloat16*>(o + d) = x;
+                            *reinterpret_cast<__nv_bfloat16*>(o + d + 8) = y;
+                        }
+                    }
+                }
+                if (p.lse && wid == 0 && g == 0)
+                    p.lse[((int64_t)b * p.tokens + j) * p.heads_q + hq] =
+                        none ? NINF : (m[nt][e] == NINF ? 0.f : m[nt][e] * 0.69314718055994531f) + logf(l[nt][e]);
+            }
+    };
+
+    bool early = false, last = false;        // the run's first segment is a part, and not the last; its last is a part
+    int early_b = 0, early_u = 0;
+    int64_t early_unit0 = 0;
     while (walk.next(p, units)) {
         const Span s = walk.s;
         const int hk = walk.u / p.row_tiles, r0 = (walk.u % p.row_tiles) * C::ROWS;
+        const float k_scale = p.k_scale ? p.k_scale[hk] : 1.f, v_scale = p.v_scale ? p.v_scale[hk] : 1.f;
+        clear();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = NINF;
             l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
         }
         wait(qfull(qs), qphase);
-        const float sc_all = p.scale_log2 * (p.k_scale ? p.k_scale[hk] : 1.f);
+        const float sc_all = p.scale_log2 * k_scale;
         float sc[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -458,36 +732,43 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 
         for (int t = walk.t0; t < walk.t1; ++t) {
             const int key0 = s.base + t * KEYS;
-            // ---- S^T: this warp's 16 keys x all rows
-            float sT[NT][4];
+            // ---- S^T: this warp's 16 KB keys x all rows
+            float sT[KB][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sT[nt][e] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sT[kb][nt][e] = 0.f;
             wait(full(slot), phase);
             {
                 const uint32_t kt = ring_u + (uint32_t)slot * C::TILE;
-                const int krow = 16 * wid + (lane & 15);
 #pragma unroll
                 for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
-                    uint32_t a0[4], a1[4];
-                    if constexpr (E4M3) {
-                        uint32_t r[4];
-                        ldsm4(kt + chunk_at<C::CH>(krow, 2 * s2 + (lane >> 4)), r);
-                        a0[0] = e4m3_f16x2(r[0]), a0[2] = e4m3_f16x2(r[0] >> 16);
-                        a0[1] = e4m3_f16x2(r[1]), a0[3] = e4m3_f16x2(r[1] >> 16);
-                        a1[0] = e4m3_f16x2(r[2]), a1[2] = e4m3_f16x2(r[2] >> 16);
-                        a1[1] = e4m3_f16x2(r[3]), a1[3] = e4m3_f16x2(r[3] >> 16);
-                    } else {
-                        ldsm4(kt + chunk_at<C::CH>(krow, 4 * s2 + (lane >> 4)), a0);
-                        ldsm4(kt + chunk_at<C::CH>(krow, 4 * s2 + 2 + (lane >> 4)), a1);
+                    uint32_t a0[KB][4], a1[KB][4];
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const int krow = 16 * (wid + W * kb) + (lane & 15);
+                        if constexpr (E4M3) {
+                            uint32_t r[4];
+                            ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 2 * s2 + (lane >> 4)), r);
+                            a0[kb][0] = e4m3_f16x2(r[0]), a0[kb][2] = e4m3_f16x2(r[0] >> 16);
+                            a0[kb][1] = e4m3_f16x2(r[1]), a0[kb][3] = e4m3_f16x2(r[1] >> 16);
+                            a1[kb][0] = e4m3_f16x2(r[2]), a1[kb][2] = e4m3_f16x2(r[2] >> 16);
+                            a1[kb][1] = e4m3_f16x2(r[3]), a1[kb][3] = e4m3_f16x2(r[3] >> 16);
+                        } else {
+                            ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + (lane >> 4)), a0[kb]);
+                            ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + 2 + (lane >> 4)), a1[kb]);
+                        }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint32_t b[4];
-                        ldsm4(q_u + chunk_at<QCH>(8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
-                        mma<E4M3>(sT[nt], a0, b[0], b[1]);
-                        mma<E4M3>(sT[nt], a1, b[2], b[3]);
+                        ldsm4(q_u + qchunk_at<QCH>(8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a0[kb], b[0], b[1]);
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a1[kb], b[2], b[3]);
                     }
                 }
             }
@@ -497,44 +778,55 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             // every key of the tile visible to every row?
             const bool whole = key0 + KEYS <= s.len - p.tokens + 1 && (p.window <= 0 || key0 >= s.len - p.window);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sT[nt][e] *= sc[nt][e & 1];
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sT[kb][nt][e] *= sc[nt][e & 1];
             if (!whole) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + 16 * wid + g + (e >> 1) * 8;
-                        const int end = s.len - p.tokens + (r0 + 8 * nt + t2 + (e & 1)) / p.group + 1;
-                        if (key >= end || key >= s.hi || (p.window > 0 && key < end - p.window)) sT[nt][e] = NINF;
+                    for (int e = 0; e < 2; ++e) {
+                        const int end = min(s.len - p.tokens + (r0 + 8 * nt + t2 + e) / p.group + 1, s.hi);
+                        const int begin = p.window > 0 ? end - p.window : 0;
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) {
+                            const int key = key0 + 16 * (wid + W * kb) + g;
+                            if (key >= end || key < begin) sT[kb][nt][e] = NINF;
+                            if (key + 8 >= end || key + 8 < begin) sT[kb][nt][e + 2] = NINF;
+                        }
                     }
             }
             bool need = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) need |= sT[nt][e] > m[nt][e & 1] + LAZY;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + LAZY;
 
             // ---- P^T = 2^(s - m), to [nt][key][row]
-            uint32_t p_u = pbuf_u + turn * C::PBYTES;
-            float pT[NT][4];
+            const uint32_t p_u = pbuf_u + turn * C::PBYTES;
+            float pT[KB][NT][4];
             auto make_p = [&] {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
+                    const float m0 = m[nt][0] == NINF ? 0.f : m[nt][0], m1 = m[nt][1] == NINF ? 0.f : m[nt][1];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float mm = m[nt][e & 1] == NINF ? 0.f : m[nt][e & 1];
-                        pT[nt][e] = exp2_approx(sT[nt][e] - mm);
-                    }
-                    const uint32_t at = p_u + nt * KEYS * 16 + (16 * wid + g) * 16 + t2 * 2;
+                    for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const uint32_t hi = pack2<E4M3>(pT[nt][e], pT[nt][e + 1]);
-                        st_shared(at + e * 64, hi);
-                        if constexpr (!E4M3)
-                            st_shared(at + e * 64 + C::LOW, pack2<false>(pT[nt][e] - __uint_as_float(hi << 16),
-                                                                         pT[nt][e + 1] - __uint_as_float(hi & 0xffff0000u)));
+                        for (int e = 0; e < 4; ++e) pT[kb][nt][e] = exp2_approx(sT[kb][nt][e] - (e & 1 ? m1 : m0));
+                        const uint32_t at = p_u + (nt * KEYS + 16 * (wid + W * kb) + g) * 16 + t2 * 2;
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const uint32_t hi = pack2<E4M3>(pT[kb][nt][e], pT[kb][nt][e + 1]);
+                            st_shared(at + e * 64, hi);
+                            if constexpr (!E4M3)
+                                st_shared(at + e * 64 + C::LOW,
+                                          pack2<false>(pT[kb][nt][e] - __uint_as_float(hi << 16),
+                                                       pT[kb][nt][e + 1] - __uint_as_float(hi & 0xffff0000u)));
+                        }
                     }
                 }
             };
@@ -545,7 +837,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(sT[nt][e], sT[nt][e + 2]);
+                        float x = NINF;
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) x = fmaxf(x, fmaxf(sT[kb][nt][e], sT[kb][nt][e + 2]));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
@@ -569,19 +863,34 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 consumer_sync();
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) l[nt][e & 1] += pT[nt][e];
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) l[nt][e & 1] += pT[kb][nt][e];
 
-            // ---- O^T += V^T P^T: this warp's dims, all 64 keys
+            // ---- O^T += V^T P^T: this warp's dims, all keys of the tile
             wait(full(slot), phase);
             {
                 const uint32_t vt = ring_u + (uint32_t)slot * C::TILE;
+                if (!whole) {
+                    // Rows outside the visible keys are not the cache's (a box reads whole pages, and skips
+                    // those that nobody sees): zeros, so that P = 0 meets a number there.
+                    constexpr int PCH = C::PITCH / 16;
+                    uint8_t* v = ring + (size_t)slot * C::TILE;
+                    const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
+                    for (int i = tid; i < (z0 + KEYS - z1) * PCH; i += CONSUMERS) {
+                        const int r = i / PCH, row = r < z0 ? r : z1 + r - z0;
+                        *reinterpret_cast<uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();        // before TMA writes the slot again
+                    consumer_sync();
+                }
                 // V^T fragments of 16-dim tile mt: keys 32 kp .. 32 kp + 31, two k-steps
                 auto v_frags = [&](int kp, int mt, uint32_t (&f)[2][4]) {
                     if constexpr (E4M3) {
                         uint32_t r[4];
-                        ldsm4t(vt + chunk_at<C::CH>(32 * kp + lane, wid * MT + mt), r);
+                        ldsm4t(vt + chunk_at<C::PW, KEYS>(32 * kp + lane, wid * MT + mt), r);
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const uint32_t x = __byte_perm(r[h], 0, 0x3120);   // (key, key + 1) of dim 2g, then of 2g + 1
@@ -591,8 +900,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     } else {
                         const int key = 32 * kp + (lane & 7) + ((lane >> 4) << 3);
                         const int c = 2 * (wid * MT + mt) + ((lane >> 3) & 1);
-                        ldsm4t(vt + chunk_at<C::CH>(key, c), f[0]);
-                        ldsm4t(vt + chunk_at<C::CH>(key + 16, c), f[1]);
+                        ldsm4t(vt + chunk_at<C::PW, KEYS>(key, c), f[0]);
+                        ldsm4t(vt + chunk_at<C::PW, KEYS>(key + 16, c), f[1]);
                     }
                 };
                 auto p_frags = [&](int kp, uint32_t (&b)[C::PN][NT][4]) {
@@ -600,15 +909,16 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     for (int n = 0; n < C::PN; ++n)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            ldsm4t(p_u + n * C::LOW + nt * KEYS * 16 + (32 * kp + lane) * 16, b[n][nt]);
+                            ldsm4t(p_u + n * C::LOW + (nt * KEYS + 32 * kp + lane) * 16, b[n][nt]);
                 };
-                // Keys that some rows see and others do not meet P = 0 in the others' columns, where an
-                // infinity or NaN of V must not become one of the output: such a tile is added row by row.
+                // Keys that some tokens see and others do not meet P = 0 in the others' columns, where an
+                // infinity or NaN must not become one of the output: with such values among them the tokens
+                // are added one by one, each with the keys that it sees and in the same order.
                 bool apart = false;
                 if (!whole && p.tokens > 1) {
                     constexpr uint32_t EXP = E4M3 ? 0x7c00u : 0x7f80u;
 #pragma unroll 1
-                    for (int kp = 0; kp < 2; ++kp)
+                    for (int kp = 0; kp < KEYS / 32; ++kp)
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             uint32_t f[2][4];
@@ -623,7 +933,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 }
                 if (!apart) {
 #pragma unroll
-                    for (int kp = 0; kp < 2; ++kp) {
+                    for (int kp = 0; kp < KEYS / 32; ++kp) {
                         uint32_t b[C::PN][NT][4];
                         p_frags(kp, b);
 #pragma unroll
@@ -642,9 +952,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 } else {
 #pragma unroll 1
                     for (int j = 0; j < p.tokens; ++j) {
-                        const int end = s.len - p.tokens + j + 1, begin = p.window > 0 ? end - p.window : 0;
+                        const int end = s.len - p.tokens + j + 1, begin = p.window > 0 ? max(0, end - p.window) : 0;
 #pragma unroll 1
-                        for (int kp = 0; kp < 2; ++kp) {
+                        for (int kp = 0; kp < KEYS / 32; ++kp) {
                             uint32_t b[C::PN][NT][4];
                             p_frags(kp, b);
 #pragma unroll
@@ -659,7 +969,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                                 }
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                    float d[4] = {acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]};
 #pragma unroll
                                     for (int n = 0; n < C::PN; ++n) {
                                         mma<E4M3>(d, f[0], b[n][nt][0], b[n][nt][1]);
@@ -667,7 +977,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                                     }
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
-                                        if ((r0 + 8 * nt + t2 + (e & 1)) / p.group == j) acc[mt][nt][e] += d[e];
+                                        if ((r0 + 8 * nt + t2 + (e & 1)) / p.group == j) acc[mt][nt][e] = d[e];
                                 }
                             }
                         }
@@ -679,8 +989,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         }
 
         // ---- the end of a segment
+        const bool part = walk.t0 > 0 || walk.t1 < s.tiles, end_of_run = walk.left <= 0;
         __syncwarp();
-        if (lane == 0) mbar_arrive(qempty(qs));
+        if (lane == 0) {
+            mbar_arrive(qempty(qs));
+            if (end_of_run) mbar_arrive(finished);
+        }
         if (++qs == C::QBUF) qs = 0, qphase ^= 1u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -702,115 +1016,55 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int w = 0; w < W; ++w) x += lred[w * C::ROWS + 8 * nt + t2 + e];
                 l[nt][e] = x;
             }
-
-        bool write = true;
-        if (walk.t0 > 0 || walk.t1 < s.tiles) {
-            // a part of the unit: publish it, and join the parts if every other run has published
-            const int64_t c_first = ((walk.unit0 + 1) * ctas - 1) / all_tiles;
-            const int64_t c_last = ((walk.unit0 + s.tiles) * ctas - 1) / all_tiles;
-            const int mine = 2 * blockIdx.x + (walk.t0 > 0 ? 0 : 1);
-            float4* part = reinterpret_cast<float4*>(p.slots + (size_t)mine * C::SLOT_FLOATS);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    part[((wid * MT + mt) * NT + nt) * 32 + lane] =
-                        make_float4(acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]);
-            float* stats = reinterpret_cast<float*>(part) + (size_t)W * MT * NT * 128;   // [row]{m, l}
-            if (wid == 0 && g == 0)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    *reinterpret_cast<float4*>(stats + 2 * (8 * nt + t2)) = make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
-            __threadfence();
-            consumer_sync();
-            if (tid == 0) {
-                const uint32_t parts = (uint32_t)(c_last - c_first + 1);
-                uint32_t* counter = p.counters + c_first;
-                const uint32_t before = atomicAdd(counter, 1u);
-                const bool last = before == parts - 1;
-                if (last) *counter = 0;   // every run has counted in: zero again for the next call
-                __threadfence();
-                last_flag = last;
-            }
-            consumer_sync();
-            write = last_flag != 0;
-            if (write) {
-                __threadfence();
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    m[nt][0] = m[nt][1] = NINF;
-                    l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-                }
-                auto slot_of = [&](int64_t c) { return p.slots + (size_t)(2 * c + (c == c_first ? 1 : 0)) * C::SLOT_FLOATS; };
-                for (int64_t c = c_first; c <= c_last; ++c) {
-                    const float* st = slot_of(c) + (size_t)W * MT * NT * 128;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(st + 2 * (8 * nt + t2)));
-                        m[nt][0] = fmaxf(m[nt][0], v.x);
-                        m[nt][1] = fmaxf(m[nt][1], v.z);
-                    }
-                }
-#pragma unroll 2
-                for (int64_t c = c_first; c <= c_last; ++c) {
-                    const float* base = slot_of(c);
-                    const float* st = base + (size_t)W * MT * NT * 128;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(st + 2 * (8 * nt + t2)));
-                        const float f0 = v.x == m[nt][0] ? 1.f : exp2_approx(v.x - m[nt][0]);
-                        const float f1 = v.z == m[nt][1] ? 1.f : exp2_approx(v.z - m[nt][1]);
-                        l[nt][0] += f0 * v.y;
-                        l[nt][1] += f1 * v.w;
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const float4 a = __ldcg(reinterpret_cast<const float4*>(base) + ((wid * MT + mt) * NT + nt) * 32 + lane);
-                            acc[mt][nt][0] += f0 * a.x;
-                            acc[mt][nt][1] += f1 * a.y;
-                            acc[mt][nt][2] += f0 * a.z;
-                            acc[mt][nt][3] += f1 * a.w;
-                        }
-                    }
-                }
-            }
+        if (!part) {
+            write_out(walk.b, walk.u, s.len, v_scale);
+        } else if (!end_of_run) {
+            // the run's first part: to its slot, and on with the next segment; the q warp counts it in
+            store_part(false);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(stored);
+            early = true;
+            early_b = walk.b, early_u = walk.u, early_unit0 = walk.unit0;
+        } else {
+            last = true;
         }
-        if (write && ok) {
-            const float vs = p.v_scale ? p.v_scale[hk] : 1.f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = r0 + 8 * nt + t2 + e;
-                    const int j = r / p.group, hq = hk * p.group + (r - j * p.group);
-                    if (j >= p.tokens) continue;
-                    // a row that sees no key is zero; otherwise its sum is positive, or NaN as its scores are
-                    const int end = s.len - p.tokens + j + 1;
-                    const bool none = end <= 0;
-                    const float inv = none ? 0.f : vs / l[nt][e];
-                    uint16_t* o = p.out + (int64_t)walk.b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const int d = (wid * MT + mt) * 16 + (E4M3 ? 2 * g : g);
-                        const __nv_bfloat16 x = __float2bfloat16_rn(none ? 0.f : acc[mt][nt][e] * inv);
-                        const __nv_bfloat16 y = __float2bfloat16_rn(none ? 0.f : acc[mt][nt][e + 2] * inv);
-                        if (d < p.dim) {
-                            if constexpr (E4M3) {
-                                *reinterpret_cast<__nv_bfloat162*>(o + d) = __nv_bfloat162(x, y);
-                            } else {
-                                *reinterpret_cast<__nv_bfloat16*>(o + d) = x;
-                                *reinterpret_cast<__nv_bfloat16*>(o + d + 8) = y;
-                            }
-                        }
-                    }
-                    if (p.lse && wid == 0 && g == 0)
-                        p.lse[((int64_t)walk.b * p.tokens + j) * p.heads_q + hq] =
-                            none ? NINF : (m[nt][e] == NINF ? 0.f : m[nt][e] * 0.69314718055994531f) + logf(l[nt][e]);
+    }
+    // ---- the run's last part, and its first where that was the last of its unit to be counted in
+    for (int i = 0; i < 2; ++i) {
+        bool write = false, direct = false;
+        int b, u;
+        Parts x;
+        if (i == 0) {
+            if (!last) continue;
+            b = walk.b, u = walk.u;
+            x = parts_of(walk.unit0, walk.s.tiles);
+            if (walk.t0 == 0) {
+                wait(decided, 0);
+                direct = ok && others_in != 0;
+            }
+            write = direct;
+            if (!direct) {
+                store_part(walk.t0 == 0);
+                consumer_sync();
+                if (tid == 0) {
+                    fence_acq_rel_gpu();
+                    last_flag = atomicAdd(p.counters + x.first, 1u) == (uint32_t)x.count - 1;
+                    fence_acq_rel_gpu();
                 }
+                consumer_sync();
+                write = last_flag != 0;
+            }
+        } else {
+            if (!early) continue;
+            wait(counted, 0);
+            write = ok && late_join != 0;
+            b = early_b, u = early_u;
+            if (write) x = parts_of(early_unit0, span_of<KEYS>(p, b).tiles);
         }
+        if (!write) continue;
+        join(x, direct);
+        const int hk = u / p.row_tiles;
+        write_out(b, u, span_of<KEYS>(p, b).len, p.v_scale ? p.v_scale[hk] : 1.f);
     }
     if (!ok && lane == 0) atomicOr(p.status, 1u);
 }
@@ -826,27 +1080,30 @@ AttnShape shape() {
     AttnShape s;
     s.ctas_per_sm = C::CPS;
     s.rows = C::ROWS;
+    s.keys = C::KEYS;
     s.slot_floats = C::SLOT_FLOATS;
     return s;
 }
 template <int DP, int NT, bool E4M3>
-cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
-    return launch_pdl(paged_attn_kernel<DP, NT, E4M3>, dim3((unsigned)grid), THREADS, Cfg<DP, NT, E4M3>::SMEM, st, p);
+cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
+    return launch_pdl(paged_attn_kernel<DP, NT, E4M3>, dim3((unsigned)grid), THREADS, Cfg<DP, NT, E4M3>::SMEM, st, p,
+                      k, v);
 }
 
 // Row tiles hold 8 NT rows, the fewest that take all rows at once, up to 64
-// (16 at dim 512, whose tiles fill shared memory); more rows go to several
-// tiles, each of which reads the keys again.
-#define AFFQMM_ATTN_SWITCH(DP, rows, CALL)                   \
-    if ((rows) <= 8) { CALL(DP, 1); }                        \
-    if ((rows) <= 16 || (DP) == 512) { CALL(DP, 2); }        \
-    if constexpr ((DP) < 512) {                              \
-        if ((rows) <= 32) { CALL(DP, 4); }                   \
-        CALL(DP, 8);                                         \
-    }
-#define AFFQMM_ATTN_SHAPE(DP, NT) return e4m3 ? attn::shape<DP, NT, true>() : attn::shape<DP, NT, false>()
+// (32 at dim 256, whose accumulators fill the registers, and 16 at dim 512,
+// whose tiles fill shared memory); more rows go to several tiles, each of
+// which reads the keys again, the later ones mostly from L2.
+constexpr int most_nt(int dp) { return dp <= 128 ? 8 : dp == 256 ? 4 : 2; }
+#define AFFQMM_ATTN_SWITCH(DP, rows, CALL)                                          \
+    if ((rows) <= 8) { CALL(DP, 1); }                                               \
+    if ((rows) <= 16 || attn::most_nt(DP) == 2) { CALL(DP, 2); }                    \
+    if constexpr (attn::most_nt(DP) >= 4)                                           \
+        if ((rows) <= 32 || attn::most_nt(DP) == 4) { CALL(DP, 4); }                \
+    if constexpr (attn::most_nt(DP) >= 8) { CALL(DP, 8); }
+#define AFFQMM_ATTN_SHAPE(DP, NT) return e4m3 ? attn::shape<(DP), NT, true>() : attn::shape<(DP), NT, false>()
 #define AFFQMM_ATTN_LAUNCH(DP, NT) \
-    return e4m3 ? attn::launch<DP, NT, true>(p, grid, st) : attn::launch<DP, NT, false>(p, grid, st)
+    return e4m3 ? attn::launch<DP, NT, true>(p, k, v, grid, st) : attn::launch<DP, NT, false>(p, k, v, grid, st)
 #define AFFQMM_ATTN_ALLOW(DP, NT)                                           \
     if (cudaError_t e = attn::allow<DP, NT, true>(); e != cudaSuccess) return e; \
     if (cudaError_t e = attn::allow<DP, NT, false>(); e != cudaSuccess) return e
@@ -863,13 +1120,12 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
     cudaError_t attn_allow_smem_##DP() {                                                                  \
         AFFQMM_ATTN_ALLOW(DP, 1);                                                                         \
         AFFQMM_ATTN_ALLOW(DP, 2);                                                                         \
-        if constexpr ((DP) < 512) {                                                                       \
-            AFFQMM_ATTN_ALLOW(DP < 512 ? DP : 64, 4);                                                     \
-            AFFQMM_ATTN_ALLOW(DP < 512 ? DP : 64, 8);                                                     \
-        }                                                                                                 \
+        if constexpr (attn::most_nt(DP) >= 4) { AFFQMM_ATTN_ALLOW((DP <= 256 ? DP : 64), 4); }            \
+        if constexpr (attn::most_nt(DP) >= 8) { AFFQMM_ATTN_ALLOW((DP <= 128 ? DP : 64), 8); }            \
         return cudaSuccess;                                                                               \
     }                                                                                                     \
-    cudaError_t launch_attn_##DP(bool e4m3, int rows, const AttnParams& p, int grid, cudaStream_t st) {    \
+    cudaError_t launch_attn_##DP(bool e4m3, int rows, const AttnParams& p, const CUtensorMap& k,          \
+                                 const CUtensorMap& v, int grid, cudaStream_t st) {                       \
         AFFQMM_ATTN_SWITCH(DP, rows, AFFQMM_ATTN_LAUNCH)                                                  \
         return cudaErrorInvalidValue;                                                                     \
     }                                                                                                     \

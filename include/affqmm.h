@@ -383,10 +383,11 @@ AFFQMM_API int affqmm_run_noalloc(const affqmm_weight* w, const uint16_t* x, int
 /* A cache: a non-owning view of the pool's keys and values.
  *   page          tokens of a page, a power of two up to 65536
  *   heads, dim    key heads, and values of a head: a multiple of 16 up to 512
- *   pages         pages of the pool; pages * page < 2^31
+ *   pages         pages of the pool, at least one; pages * page < 2^31
  *   *_stride      elements between pages, tokens and heads (any order in
  *                 memory; the values of a head are contiguous), each a multiple
- *                 of 16 bytes
+ *                 of 16 bytes and at least dim (that of an axis of one does not
+ *                 matter)
  *   k, v          device, 16-byte aligned
  *   k_scale, v_scale  device, fp32 [heads] or NULL (1): with AFFQMM_KV_E4M3, a
  *                 value is the stored one times its head's scale; NULL with
