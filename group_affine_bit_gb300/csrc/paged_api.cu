@@ -329,6 +329,7 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     // a window's keys, from a multiple of a tile on
     if (window > 0 && keys > (int64_t)window + tokens + shape.keys) keys = (int64_t)window + tokens + shape.keys;
     const int64_t tiles = batch * cache->heads * p.row_tiles * (keys < shape.keys ? 1 : (keys + shape.keys - 1) / shape.keys);
+    if (tiles >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
     const int64_t most = (int64_t)sms * shape.ctas_per_sm;
     const int grid = (int)(tiles < most ? tiles : most);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -86,7 +86,7 @@ struct Cfg {
     static constexpr int PBYTES = PN * LOW;            // [PN][NT][keys][8 rows] of 16 bits
     static constexpr int MT = DP / (16 * W);           // 16-dim tiles of a consumer warp
     static constexpr int JOIN = NT <= 2 ? 32 : 64 / NT;         // parts whose weights a join holds at a time
-    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + QBUF * ROWS * 4 +
+    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + 3 * QBUF * ROWS * 4 +
                                     JOIN * ROWS * 4 + 512;
     static constexpr bool LIGHT = MT * NT * 4 + NT * 8 <= 32;   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
@@ -138,6 +138,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
+}
+// Count a part in: what this CTA stored before is visible to who sees the count, and what others stored to us.
+__device__ __forceinline__ uint32_t count_part(uint32_t* counter) {
+    uint32_t before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
 }
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -194,8 +200,8 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int b) {
 template <int KEYS>
 struct Walk {
     int b, u, t, t0, t1;
-    int64_t left;      // tiles of the run not yet handed out
-    int64_t unit0;     // number of the unit's first tile
+    int left;          // tiles of the run not yet handed out
+    uint32_t unit0;    // number of the unit's first tile
     Span s;
     __device__ __forceinline__ bool next(const AttnParams& p, int units) {
         if (left <= 0) return false;
@@ -209,12 +215,19 @@ struct Walk {
             }
         }
         t0 = t;
-        t1 = (int)min((int64_t)s.tiles, t0 + left);
+        t1 = min(s.tiles, t0 + left);
         left -= t1 - t0;
         t = t1;
         return true;
     }
 };
+
+// The CTA whose run has tile x, runs being tiles floor(c total / ctas) .. floor((c + 1) total / ctas) - 1 of CTA c.
+__device__ __forceinline__ uint32_t run_of(uint32_t x, uint32_t total, uint32_t ctas) {
+    const uint64_t top = (uint64_t)(x + 1) * ctas - 1;
+    if (top < (uint64_t)1 << 32) return (uint32_t)top / total;
+    return (uint32_t)(top / total);
+}
 
 template <int DP, int NT, bool E4M3>
 __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_kernel(
@@ -228,7 +241,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     float* red = reinterpret_cast<float*>(pbuf + 2 * C::PBYTES);      // [W][ROWS] maxima
     float* lred = red + W * C::ROWS;                                  // [W][ROWS] sums
     float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: what undoes q's power of two
-    float* weight = qscale + C::QBUF * C::ROWS;                       // [JOIN][ROWS] of a join's parts
+    int* row_token = reinterpret_cast<int*>(qscale + C::QBUF * C::ROWS);   // [QBUF][ROWS] token of a row, -1: none
+    int* row_head = row_token + C::QBUF * C::ROWS;                    // [QBUF][ROWS] and its query head
+    float* weight = reinterpret_cast<float*>(row_head + C::QBUF * C::ROWS);                       // [JOIN][ROWS] of a join's parts
     uint64_t* bars = reinterpret_cast<uint64_t*>(weight + C::JOIN * C::ROWS);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -238,14 +253,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     const uint32_t stored = bar0 + 8u * (2 * MAX_SLOTS + 4);     // the run's first part is in its slot
     const uint32_t counted = stored + 8u;                        // and has been counted in
     const uint32_t finished = stored + 16u;                      // the run's last tile has been added
+    const uint32_t joined = stored + 32u;                        // parts of other runs are in the ring
     const uint32_t decided = stored + 24u;                       // whether the other parts of its unit are there
-    __shared__ int64_t sums[THREADS / 32];
-    __shared__ int64_t run_tiles, run_unit0, run_total, run_at;
-    __shared__ int run_b;
+    __shared__ uint32_t sums[THREADS / 32], found_unit0;
+    __shared__ int found_b;
     __shared__ uint32_t last_flag, late_join, others_in;
 
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
+#pragma unroll 1
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), W);
@@ -258,6 +274,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         mbar_init(counted, 1);
         mbar_init(finished, W);
         mbar_init(decided, 1);
+        mbar_init(joined, 1);
         fence_mbar_init();
     }
     if (wid == W && lane == 0) {
@@ -266,67 +283,75 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this CTA's run of tiles: a prefix sum over the requests' tiles
+    // ---- this CTA's run of tiles: a prefix sum over the requests' tiles.  Up to 256 requests, every warp makes it
+    // for itself, eight requests to a lane, without a barrier; beyond, the CTA's threads share the requests.
     const int units = p.heads_kv * p.row_tiles;
+    uint32_t all_tiles, ctas, run_tiles, run_unit0, run_at;
+    int run_b;
     {
-        const int each = (p.batch + THREADS - 1) / THREADS;
-        const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
-        int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            if (blockIdx.x == 0 && p.user_status && (p.lens[b] < 0 || p.lens[b] > ((int64_t)p.wide << p.page_shift)))
-                atomicOr(p.user_status, 2u);
-            mine += (int64_t)span_of<KEYS>(p, b).tiles * units;
-        }
-        int64_t x = mine;
+        const bool alone = p.batch <= 256;
+        const int sharers = alone ? 32 : THREADS, me = alone ? lane : tid;
+        const int each = (p.batch + sharers - 1) / sharers;
+        const int b0 = min(me * each, p.batch), b1 = min(b0 + each, p.batch);
+        uint32_t mine = 0;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) mine += (uint32_t)(span_of<KEYS>(p, b).tiles * units);
+        uint32_t x = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(~0u, x, d);
+            const uint32_t y = __shfl_up_sync(~0u, x, d);
             if (lane >= d) x += y;
         }
-        if (lane == 31) sums[wid] = x;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < wid) before += sums[w];
-            total += sums[w];
-        }
-        before += x - mine;
-        // no run is empty: with fewer tiles than CTAs, the first `total` CTAs take one each
-        const int64_t ctas = min((int64_t)gridDim.x, total), c = min((int64_t)blockIdx.x, ctas);
-        int64_t r0, r1;
-        if (total < (int64_t)1 << 31) {   // the quotient in 32 bits: c total / ctas = c (total / ctas) + c (total % ctas) / ctas
-            const uint32_t n = (uint32_t)total, d = (uint32_t)ctas, per = n / d, over = n - per * d, cc = (uint32_t)c;
-            r0 = (int64_t)(cc * per + cc * over / d);
-            r1 = cc < d ? (int64_t)((cc + 1) * per + (cc + 1) * over / d) : r0;
-        } else {
-            r0 = total * c / ctas;
-            r1 = c < ctas ? total * (c + 1) / ctas : r0;
-        }
-        if (tid == 0) run_tiles = r1 - r0, run_total = total;
-        if (r1 > r0 && before <= r0 && r0 < before + mine) {
-            int64_t at = before;
-            int b = b0;
-            for (;; ++b) {
-                const int64_t n = (int64_t)span_of<KEYS>(p, b).tiles * units;
-                if (r0 < at + n) break;
-                at += n;
+        uint32_t before = x - mine;
+        all_tiles = __shfl_sync(~0u, x, 31);
+        if (!alone) {
+            if (lane == 31) sums[wid] = x;
+            __syncthreads();
+            all_tiles = 0;
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < wid) before += sums[w];
+                all_tiles += sums[w];
             }
-            run_b = b;
-            run_at = r0 - at;
-            run_unit0 = at;
         }
-        __syncthreads();
+        // no run is empty: with fewer tiles than CTAs, the first `all_tiles` CTAs take one each
+        ctas = min(gridDim.x, all_tiles);
+        const uint32_t c = min(blockIdx.x, ctas), per = all_tiles / ctas, over = all_tiles - per * ctas;
+        const uint32_t r0 = c * per + c * over / ctas;
+        run_tiles = c < ctas ? (c + 1) * per + (c + 1) * over / ctas - r0 : 0;
+        const bool here = run_tiles > 0 && before <= r0 && r0 - before < mine;
+        int b = b0;
+        if (here)
+#pragma unroll 1
+            for (;; ++b) {
+                const uint32_t n = (uint32_t)(span_of<KEYS>(p, b).tiles * units);
+                if (r0 - before < n) break;
+                before += n;
+            }
+        if (alone) {
+            const int src = __ffs(__ballot_sync(~0u, here)) - 1;
+            run_b = __shfl_sync(~0u, b, src & 31);
+            run_unit0 = __shfl_sync(~0u, before, src & 31);
+        } else {
+            if (here) found_b = b, found_unit0 = before;
+            __syncthreads();
+            run_b = found_b;
+            run_unit0 = found_unit0;
+        }
+        run_at = r0 - run_unit0;
     }
+    if (blockIdx.x == 0 && p.user_status)
+#pragma unroll 1
+        for (int b = tid; b < p.batch; b += THREADS)
+            if (p.lens[b] < 0 || p.lens[b] > ((int64_t)p.wide << p.page_shift)) atomicOr(p.user_status, 2u);
+    __syncthreads();                         // the barriers are set up
     if (run_tiles == 0) return;
-    const int64_t all_tiles = run_total, ctas = min((int64_t)gridDim.x, all_tiles);
     Walk<KEYS> walk;
     walk.b = run_b;
     walk.s = span_of<KEYS>(p, walk.b);
-    walk.u = run_at < (int64_t)1 << 31 ? (int)run_at / walk.s.tiles : (int)(run_at / walk.s.tiles);
-    walk.t = (int)(run_at - (int64_t)walk.u * walk.s.tiles);
-    walk.unit0 = run_unit0 + (int64_t)walk.u * walk.s.tiles;
-    walk.left = run_tiles;
+    walk.u = (int)(run_at / (uint32_t)walk.s.tiles);
+    walk.t = (int)run_at - walk.u * walk.s.tiles;
+    walk.unit0 = run_unit0 + (uint32_t)(walk.u * walk.s.tiles);
+    walk.left = (int)run_tiles;
     bool ok = true;                       // no bounded wait has given up; after one, no wait is made
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok) ok = mbar_wait(bar, parity);
@@ -349,8 +374,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             const int head = walk.u / p.row_tiles;
             // 32 entries of the table in the lanes' registers and the next 32 on their way, so that no tile
             // waits for its entries; one that is no page becomes a page beyond the tensor, which reads as zeros
-            auto entries = [&](int first) {
-                const int e = first + lane;
+            auto entries = [&](int e) {
                 int page = (int)p.pages;
                 if (((int64_t)e << p.page_shift) < s.hi && (((int64_t)e + 1) << p.page_shift) > s.lo) {
                     page = table[e];
@@ -362,14 +386,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 return page;
             };
             int key0 = s.base + walk.t0 * KEYS;
-            int have = (key0 >> p.page_shift) & ~31;
-            int cur = entries(have), nxt = entries(have + 32);
+            int have = ((key0 >> p.page_shift) & ~31) - 64, cur = 0, nxt = 0;   // two steps before the first
+#pragma unroll 1
             for (int t = walk.t0; t < walk.t1; ++t, key0 += KEYS) {
-                while ((key0 >> p.page_shift) - have >= 32) {
-                    have += 32;
-                    cur = nxt;
-                    nxt = entries(have + 32);
-                }
                 // the tile's boxes that hold a visible key
                 const int i0 = max(0, s.lo - key0) >> box_shift, i1 = (min(KEYS, s.hi - key0) + box - 1) >> box_shift;
                 wait(empty(slot), phase ^ 1u);
@@ -377,14 +396,16 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 const uint32_t dst = ring_u + (uint32_t)slot * C::TILE, bar = full(slot);
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::PANELS * box_bytes);
                 __syncwarp();
+#pragma unroll 1
                 for (int i = i0; i < i1; ++i) {
                     const int row = i << box_shift;
                     int e = ((key0 + row) >> p.page_shift) - have;
-                    while (e >= 32) {        // pages of few tokens: a tile takes more than 32 entries
+#pragma unroll 1
+                    while (e >= 32) {
                         have += 32;
                         e -= 32;
                         cur = nxt;
-                        nxt = entries(have + 32);
+                        nxt = entries(have + 32 + lane);
                     }
                     const int page = __shfl_sync(~0u, cur, e);
                     const int token = (int)((uint32_t)(key0 + row) & page_mask);
@@ -401,20 +422,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             }
         }
         // no copy is in flight when the CTA ends, whatever its consumers did
+#pragma unroll 1
         for (int64_t i = turn - 2; i >= 0 && i >= turn - C::NS; i -= 2)
             if (!mbar_wait(full((int)(i % C::NS)), (uint32_t)(i / C::NS) & 1u)) ok = false;
         if (!ok && lane == 0) atomicOr(p.status, 1u);
         return;
     }
-    // The parts of a unit that begins at tile `unit0`: the runs from c_first on.
+    // The parts of a unit that begins at tile `unit0`: the runs from `first` on.
     struct Parts {
-        int64_t first;
+        uint32_t first;
         int count;
     };
-    auto parts_of = [&](int64_t unit0, int tiles) {
+    auto parts_of = [&](uint32_t unit0, int tiles) {
         Parts x;
-        x.first = ((unit0 + 1) * ctas - 1) / all_tiles;
-        x.count = (int)(((unit0 + tiles) * ctas - 1) / all_tiles - x.first) + 1;
+        x.first = run_of(unit0, all_tiles, ctas);
+        x.count = (int)(run_of(unit0 + tiles - 1, all_tiles, ctas) - x.first) + 1;
         return x;
     };
     if (wid == W + 2) {
@@ -429,10 +451,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         auto count_in = [&] {                // the first segment's part, once its consumers have stored it
             wait(stored, 0);
             if (lane == 0) {
-                fence_acq_rel_gpu();
-                const bool last = atomicAdd(p.counters + parts.first, 1u) == (uint32_t)parts.count - 1;
-                fence_acq_rel_gpu();
-                late_join = last;
+                late_join = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
                 mbar_arrive(counted);
             }
             early = false;
@@ -442,57 +461,75 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             uint8_t* dst = qbuf + qs * C::QBYTES;
             const int hk = walk.u / p.row_tiles, r0 = (walk.u % p.row_tiles) * C::ROWS;
             constexpr int QCH = DP / 8;                             // 16-byte chunks of a row
-            constexpr int PER = QCH > 32 ? QCH / 32 : 1;
-            for (int r = 0; r < C::ROWS; ++r) {
-                const bool in = r0 + r < rows;
-                const int j = in ? (r0 + r) / p.group : 0, hq = hk * p.group + (r0 + r - j * p.group);
-                const uint16_t* src = p.q + (int64_t)walk.b * p.q_bs + (int64_t)j * p.q_ts + (int64_t)hq * p.q_hs;
-                uint4 w[PER];
-#pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    const int ch = lane + 32 * c;
-                    w[c] = (in && ch < QCH && ch * 8 < p.dim) ? *reinterpret_cast<const uint4*>(src + ch * 8)
-                                                               : make_uint4(0, 0, 0, 0);
+            const uint16_t* base = p.q + (int64_t)walk.b * p.q_bs;
+            // which token and query head each row is, for the consumers too
+#pragma unroll 1
+            for (int r = lane; r < C::ROWS; r += 32) {
+                const int at = r0 + r, j = at / p.group;
+                const bool in = at < rows;
+                row_token[qs * C::ROWS + r] = in ? j : -1;
+                row_head[qs * C::ROWS + r] = hk * p.group + (at - j * p.group);
+            }
+            __syncwarp();
+            auto source = [&](int r, int ch) {
+                const int j = row_token[qs * C::ROWS + r];
+                return (j >= 0 && ch * 8 < p.dim) ? base + (int64_t)j * p.q_ts + (int64_t)row_head[qs * C::ROWS + r] * p.q_hs + ch * 8
+                                                  : nullptr;
+            };
+            if constexpr (!E4M3) {
+                const uint32_t to = smem_u32(dst);
+#pragma unroll 1
+                for (int i = lane; i < C::ROWS * QCH; i += 32) {    // in flight together
+                    const uint16_t* src = source(i / QCH, i % QCH);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + qchunk_at<QCH>(i / QCH, i % QCH)),
+                                 "l"(src ? src : p.q), "r"(src ? 16u : 0u) : "memory");
                 }
-                if constexpr (E4M3) {
-                    // a power of two that brings the row's largest magnitude into [2^13, 2^14)
-                    uint32_t big = 0;
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            } else {
+                constexpr int PER = QCH > 32 ? QCH / 32 : 1, GO = 4;   // rows in flight
+#pragma unroll 1
+                for (int g0 = 0; g0 < C::ROWS; g0 += GO) {
+                    uint4 w[GO][PER];
 #pragma unroll
-                    for (int c = 0; c < PER; ++c) {
-                        const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                    for (int r = 0; r < GO; ++r)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) big = max(big, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
-                    }
-                    big = __reduce_max_sync(~0u, big);
-                    int up = 13 - ((int)(big >> 7) - 127);
-                    if (big >= 0x7f80u) up = 0;                     // an infinity or NaN stays one
-                    up = min(up, 126);
-                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                    if (lane == 0) qscale[qs * C::ROWS + r] = __uint_as_float((uint32_t)(127 - up) << 23);
+                        for (int c = 0; c < PER; ++c) {
+                            const uint16_t* src = lane + 32 * c < QCH ? source(g0 + r, lane + 32 * c) : nullptr;
+                            w[r][c] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+                        }
 #pragma unroll
-                    for (int c = 0; c < PER; ++c) {
-                        const int ch = lane + 32 * c;
-                        uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                    for (int r = 0; r < GO; ++r) {
+                        // a power of two that brings the row's largest magnitude into [2^13, 2^14)
+                        uint32_t big = 0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = pack2<true>(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
-                        if (ch < QCH) {
-                            // within 16 dims, the order in which an 8-bit K fragment holds them: a thread's
-                            // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
-                            const int step = ch >> 1, h = ch & 1;   // dims 16 step + 8 h ..
+                        for (int c = 0; c < PER; ++c) {
+                            const uint32_t v[4] = {w[r][c].x, w[r][c].y, w[r][c].z, w[r][c].w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int pair = 4 * h + e;         // dims 2 pair, 2 pair + 1 of the 16
-                                const int k = (pair >> 1) * 2 + (pair & 1) * 8;
-                                *reinterpret_cast<uint32_t*>(dst + qchunk_at<QCH>(r, 2 * step + (k >> 3)) + (k & 7) * 2) = v[e];
+                            for (int e = 0; e < 4; ++e) big = max(big, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
+                        }
+                        big = __reduce_max_sync(~0u, big);
+                        int up = 13 - ((int)(big >> 7) - 127);
+                        if (big >= 0x7f80u) up = 0;                 // an infinity or NaN stays one
+                        up = min(up, 126);
+                        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+                        if (lane == 0) qscale[qs * C::ROWS + g0 + r] = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+                        for (int c = 0; c < PER; ++c) {
+                            const int ch = lane + 32 * c;
+                            const uint32_t v[4] = {w[r][c].x, w[r][c].y, w[r][c].z, w[r][c].w};
+                            if (ch < QCH) {
+                                // within 16 dims, the order in which an 8-bit K fragment holds them: a thread's
+                                // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
+                                const int step = ch >> 1, h = ch & 1;   // dims 16 step + 8 h ..
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int pair = 4 * h + e;         // dims 2 pair, 2 pair + 1 of the 16
+                                    const int k = (pair >> 1) * 2 + (pair & 1) * 8;
+                                    *reinterpret_cast<uint32_t*>(dst + qchunk_at<QCH>(g0 + r, 2 * step + (k >> 3)) + (k & 7) * 2) =
+                                        pack2<true>(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
+                                }
                             }
                         }
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < PER; ++c) {
-                        const int ch = lane + 32 * c;
-                        if (ch < QCH) *reinterpret_cast<uint4*>(dst + qchunk_at<QCH>(r, ch)) = w[c];
                     }
                 }
             }
@@ -548,6 +585,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
     };
     auto slot_of = [&](const Parts& x, int i) { return p.slots + (size_t)(2 * (x.first + i) + (i == 0 ? 1 : 0)) * C::SLOT_FLOATS; };
+    int join_round = 0;                      // of `joined`
 
     // this run's part of a unit, to its slot
     auto store_part = [&](bool first) {
@@ -566,10 +604,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     };
 
     // The parts of a unit joined, in run order: acc, m and l of the whole.  `own`: this run has the first part,
-    // in registers; the same sums come out as if it were read from its slot.
+    // in registers; the same sums come out as if it were read from its slot.  The ring is free by now, so the
+    // other parts come by bulk copies, as many at once as it holds: one round trip for them all.
     auto join = [&](const Parts& x, bool own) {
-        constexpr int JOIN = C::JOIN, TPR = CONSUMERS / C::ROWS, PER = JOIN / TPR;   // threads of a row, and its parts to a thread
-        constexpr int MOST = C::CPS == 2 ? 8 : 16, BATCH = MT * NT >= MOST ? 1 : MOST / (MT * NT);    // parts whose loads are in flight at once
+        constexpr uint32_t BYTES = C::SLOT_FLOATS * sizeof(float);
+        constexpr int ROOM = C::NS * C::TILE / BYTES < C::JOIN ? C::NS * C::TILE / BYTES : C::JOIN;
+        constexpr int TPR = CONSUMERS / C::ROWS;         // threads of a row
         const int row = tid % C::ROWS, p0 = tid / C::ROWS;
         if (own && wid == 0 && g == 0)
 #pragma unroll
@@ -578,83 +618,60 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int e = 0; e < 2; ++e) red[8 * nt + t2 + e] = m[nt][e], red[C::ROWS + 8 * nt + t2 + e] = l[nt][e];
         consumer_sync();
         float top = NINF, sum = 0.f;
-        if (!own) clear();
-        for (int c0 = 0; c0 < x.count; c0 += JOIN) {
-            const int n = min(JOIN, x.count - c0);
-            const bool mine0 = own && c0 == 0;           // part 0 of this chunk is in registers
-            float2 st[PER];
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int i = p0 + k * TPR;
-                st[k] = make_float2(NINF, 0.f);
-                if (i < n) {
-                    if (mine0 && i == 0) st[k] = make_float2(red[row], red[C::ROWS + row]);
-                    else st[k] = __ldcg(reinterpret_cast<const float2*>(slot_of(x, c0 + i) + C::STATS + 2 * row));
-                }
+        if (own) top = red[row], sum = red[C::ROWS + row];
+        else clear();
+        consumer_sync();                                 // `red` has been read
+        if (p0 > 0) sum = 0.f;                           // a row's sum is kept by its threads in pieces
+#pragma unroll 1
+        for (int c0 = 0; c0 < x.count; c0 += ROOM) {
+            const int n = min(ROOM, x.count - c0), i0 = own && c0 == 0 ? 1 : 0;
+            if (tid == 0 && ok) {
+                asm volatile("fence.proxy.async;" ::: "memory");   // others' stores, before the copies read them
+                mbar_arrive_expect_tx(joined, (n - i0) * BYTES);
+#pragma unroll 1
+                for (int i = i0; i < n; ++i) bulk_g2s(ring_u + i * BYTES, slot_of(x, c0 + i), BYTES, joined);
             }
-            float4 a[BATCH][MT][NT];
-            auto fetch = [&](int i0) {
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            if (i0 + i < n)
-                                a[i][mt][nt] = __ldcg(reinterpret_cast<const float4*>(slot_of(x, c0 + i0 + i)) +
-                                                      ((wid * MT + mt) * NT + nt) * 32 + lane);
-            };
-            fetch(mine0 ? 1 : 0);                        // with the statistics, in one round trip
-            float high = NINF;
-#pragma unroll
-            for (int k = 0; k < PER; ++k) high = fmaxf(high, st[k].x);
-            weight[tid] = high;
-            consumer_sync();
-#pragma unroll
-            for (int i = 0; i < TPR; ++i) high = fmaxf(high, weight[i * C::ROWS + row]);
-            high = fmaxf(high, top);
+            wait(joined, join_round++ & 1);
+            const float* parts = reinterpret_cast<const float*>(ring);
+            const float* stats = parts + C::STATS + 2 * row;
+            float high = top;
+#pragma unroll 1
+            for (int i = i0; i < n; ++i) high = fmaxf(high, stats[i * C::SLOT_FLOATS]);
             const float f = top == high ? 1.f : exp2_approx(top - high);
             sum *= f;
             top = high;
             if (p0 == 0) red[row] = f;
-            consumer_sync();
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int i = p0 + k * TPR;
-                if (i < n) {
-                    const float w = st[k].x == top ? 1.f : exp2_approx(st[k].x - top);
-                    weight[i * C::ROWS + row] = w;
-                    sum += w * st[k].y;
-                }
+#pragma unroll 1
+            for (int i = p0 < i0 ? p0 + TPR : p0; i < n; i += TPR) {
+                const float2 st = *reinterpret_cast<const float2*>(stats + i * C::SLOT_FLOATS);
+                const float w = st.x == top ? 1.f : exp2_approx(st.x - top);
+                weight[i * C::ROWS + row] = w;
+                sum = fmaf(w, st.y, sum);
             }
             consumer_sync();
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float2 k = *reinterpret_cast<const float2*>(red + 8 * nt + t2);
-                if (mine0) k = *reinterpret_cast<const float2*>(weight + 8 * nt + t2);
+                const float2 k = *reinterpret_cast<const float2*>(red + 8 * nt + t2);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     acc[mt][nt][0] *= k.x, acc[mt][nt][1] *= k.y, acc[mt][nt][2] *= k.x, acc[mt][nt][3] *= k.y;
             }
-            for (int i0 = mine0 ? 1 : 0; i0 < n;) {
+#pragma unroll 1
+            for (int i = i0; i < n; ++i)
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-                    if (i0 + i < n)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 w = *reinterpret_cast<const float2*>(weight + i * C::ROWS + 8 * nt + t2);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float2 w = *reinterpret_cast<const float2*>(weight + (i0 + i) * C::ROWS + 8 * nt + t2);
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                acc[mt][nt][0] = fmaf(w.x, a[i][mt][nt].x, acc[mt][nt][0]);
-                                acc[mt][nt][1] = fmaf(w.y, a[i][mt][nt].y, acc[mt][nt][1]);
-                                acc[mt][nt][2] = fmaf(w.x, a[i][mt][nt].z, acc[mt][nt][2]);
-                                acc[mt][nt][3] = fmaf(w.y, a[i][mt][nt].w, acc[mt][nt][3]);
-                            }
-                        }
-                i0 += BATCH;
-                if (i0 < n) fetch(i0);
-            }
-            consumer_sync();                             // `weight` and `red` serve the next chunk
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const float4 a = *(reinterpret_cast<const float4*>(parts + i * C::SLOT_FLOATS) +
+                                           ((wid * MT + mt) * NT + nt) * 32 + lane);
+                        acc[mt][nt][0] = fmaf(w.x, a.x, acc[mt][nt][0]);
+                        acc[mt][nt][1] = fmaf(w.y, a.y, acc[mt][nt][1]);
+                        acc[mt][nt][2] = fmaf(w.x, a.z, acc[mt][nt][2]);
+                        acc[mt][nt][3] = fmaf(w.y, a.w, acc[mt][nt][3]);
+                    }
+                }
+            consumer_sync();                             // the ring, `weight` and `red` serve the next parts
         }
         weight[tid] = sum;
         if (p0 == 0) red[row] = top;
@@ -674,47 +691,72 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         consumer_sync();                                 // `weight` and `red` serve what follows
     };
 
-    auto write_out = [&](int b, int u, int len, float v_scale) {
-        if (!ok) return;
-        const int hk = u / p.row_tiles, r0 = (u % p.row_tiles) * C::ROWS;
+    // Rows out: normalised and rounded into the segment's q buffer (which has been read), then 16 bytes a thread.
+    // A row that sees no key (whose sum is zero) is zero.
+    auto write_out = [&](int b, int u, float v_scale, int buf) {
+        uint8_t* stage = qbuf + buf * C::QBYTES;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 8 * nt + t2 + e;
-                const int j = r / p.group, hq = hk * p.group + (r - j * p.group);
-                if (j >= p.tokens) continue;
-                // a row that sees no key is zero; otherwise its sum is positive, or NaN as its scores are
-                const bool none = len - p.tokens + j + 1 <= 0;
-                const float inv = v_scale / l[nt][e];
-                uint16_t* o = p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs;
+                const int r = 8 * nt + t2 + e;
+                const float inv = l[nt][e] == 0.f ? 0.f : __fdividef(v_scale, l[nt][e]);
+                if (wid == 0 && g == 0) red[r] = m[nt][e], red[C::ROWS + r] = l[nt][e];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int d = (wid * MT + mt) * 16 + (E4M3 ? 2 * g : g);
-                    const __nv_bfloat16 x = __float2bfloat16_rn(none ? 0.f : acc[mt][nt][e] * inv);
-                    const __nv_bfloat16 y = __float2bfloat16_rn(none ? 0.f : acc[mt][nt][e + 2] * inv);
-                    if (d < p.dim) {
-                        if constexpr (E4M3) {
-                            *reinterpret_cast<__nv_bfloat162*>(o + d) = __nv_bfloat162(x, y);
-                        } else {
-                            *reinterpret_cast<__nv_bfloat16*>(o + d) = x;
-                            *reinterpret_cast<__nv_bfloat16*>(o + d + 8) = y;
-                        }
+                    uint8_t* to = stage + qchunk_at<QCH>(r, d >> 3) + (d & 7) * 2;
+                    if constexpr (E4M3) {
+                        *reinterpret_cast<uint32_t*>(to) = pack2<false>(acc[mt][nt][e] * inv, acc[mt][nt][e + 2] * inv);
+                    } else {
+                        *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(acc[mt][nt][e] * inv);
+                        *reinterpret_cast<__nv_bfloat16*>(stage + qchunk_at<QCH>(r, (d >> 3) + 1) + (d & 7) * 2) =
+                            __float2bfloat16_rn(acc[mt][nt][e + 2] * inv);
                     }
                 }
-                if (p.lse && wid == 0 && g == 0)
-                    p.lse[((int64_t)b * p.tokens + j) * p.heads_q + hq] =
-                        none ? NINF : (m[nt][e] == NINF ? 0.f : m[nt][e] * 0.69314718055994531f) + logf(l[nt][e]);
             }
+        consumer_sync();
+        const int hk = u / p.row_tiles, r0 = (u - hk * p.row_tiles) * C::ROWS;
+#pragma unroll 1
+        for (int i = tid; i < C::ROWS * QCH; i += CONSUMERS) {
+            const int r = i / QCH, ch = i % QCH, j = (r0 + r) / p.group, hq = hk * p.group + r0 + r - j * p.group;
+            if (!ok || j >= p.tokens) continue;
+            if (ch * 8 < p.dim)
+                *reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs + ch * 8) =
+                    *reinterpret_cast<const uint4*>(stage + qchunk_at<QCH>(r, ch));
+            if (p.lse && ch == 0) {
+                const float top = red[r], sum = red[C::ROWS + r];
+                p.lse[((int64_t)b * p.tokens + j) * p.heads_q + hq] = ((top == NINF ? 0.f : top) + __log2f(sum)) * 0.69314718055994531f;
+            }
+        }
+        consumer_sync();                                 // `red` serves the next segment
     };
 
-    bool early = false, last = false;        // the run's first segment is a part, and not the last; its last is a part
+    bool early = false;                      // the run's first segment is a part, and not the last
     int early_b = 0, early_u = 0;
-    int64_t early_unit0 = 0;
-    while (walk.next(p, units)) {
+    float early_scale = 1.f;
+    Parts early_parts = {};
+    for (;;) {
+        int b, u, buf = 0;
+        float v_scale;
+        Parts parts = {};
+        bool part, direct = false;
+        if (!walk.next(p, units)) {
+            // after the run: if its first segment's part was the last of its unit to be counted in, join that unit
+            if (!early) break;
+            early = false;
+            wait(counted, 0);
+            if (!ok || late_join == 0) break;
+            b = early_b, u = early_u, v_scale = early_scale, parts = early_parts, part = true;
+        } else {
         const Span s = walk.s;
         const int hk = walk.u / p.row_tiles, r0 = (walk.u % p.row_tiles) * C::ROWS;
-        const float k_scale = p.k_scale ? p.k_scale[hk] : 1.f, v_scale = p.v_scale ? p.v_scale[hk] : 1.f;
+        const float k_scale = p.k_scale ? p.k_scale[hk] : 1.f;
+        v_scale = p.v_scale ? p.v_scale[hk] : 1.f;
+        const bool end_of_run = walk.left <= 0;
+        b = walk.b, u = walk.u;
+        part = walk.t0 > 0 || walk.t1 < s.tiles;
+        if (part) parts = parts_of(walk.unit0, s.tiles);
         clear();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -730,6 +772,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? sc_all * qscale[qs * C::ROWS + 8 * nt + t2 + e] : sc_all;
         const uint32_t q_u = qbuf_u + qs * C::QBYTES;
 
+#pragma unroll 1
         for (int t = walk.t0; t < walk.t1; ++t) {
             const int key0 = s.base + t * KEYS;
             // ---- S^T: this warp's 16 KB keys x all rows
@@ -743,7 +786,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             wait(full(slot), phase);
             {
                 const uint32_t kt = ring_u + (uint32_t)slot * C::TILE;
-#pragma unroll
+#pragma unroll 2
                 for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
                     uint32_t a0[KB][4], a1[KB][4];
 #pragma unroll
@@ -788,7 +831,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int end = min(s.len - p.tokens + (r0 + 8 * nt + t2 + e) / p.group + 1, s.hi);
+                        const int end = min(s.len - p.tokens + row_token[qs * C::ROWS + 8 * nt + t2 + e] + 1, s.hi);
                         const int begin = p.window > 0 ? end - p.window : 0;
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
@@ -830,9 +873,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     }
                 }
             };
-            make_p();
-            if (consumer_any(need)) {
-                // a new maximum for every row: the four warps' maxima meet in shared memory
+            for (;;) {
+                make_p();
+                if (!consumer_any(need)) break;
+                // a new maximum for every row: the four warps' maxima meet in shared memory; then P again
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -859,8 +903,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] *= f, acc[mt][nt][e + 2] *= f;
                     }
-                make_p();
-                consumer_sync();
+                need = false;
             }
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
@@ -879,6 +922,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     constexpr int PCH = C::PITCH / 16;
                     uint8_t* v = ring + (size_t)slot * C::TILE;
                     const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
+#pragma unroll 1
                     for (int i = tid; i < (z0 + KEYS - z1) * PCH; i += CONSUMERS) {
                         const int r = i / PCH, row = r < z0 ? r : z1 + r - z0;
                         *reinterpret_cast<uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH)) = make_uint4(0, 0, 0, 0);
@@ -932,7 +976,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     apart = __any_sync(~0u, apart);
                 }
                 if (!apart) {
-#pragma unroll
+#pragma unroll 1
                     for (int kp = 0; kp < KEYS / 32; ++kp) {
                         uint32_t b[C::PN][NT][4];
                         p_frags(kp, b);
@@ -977,7 +1021,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                                     }
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
-                                        if ((r0 + 8 * nt + t2 + (e & 1)) / p.group == j) acc[mt][nt][e] = d[e];
+                                        if (row_token[qs * C::ROWS + 8 * nt + t2 + (e & 1)] == j) acc[mt][nt][e] = d[e];
                                 }
                             }
                         }
@@ -989,13 +1033,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         }
 
         // ---- the end of a segment
-        const bool part = walk.t0 > 0 || walk.t1 < s.tiles, end_of_run = walk.left <= 0;
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(qempty(qs));
-            if (end_of_run) mbar_arrive(finished);
-        }
+        buf = qs;
         if (++qs == C::QBUF) qs = 0, qphase ^= 1u;
+        __syncwarp();
+        if (lane == 0 && end_of_run) mbar_arrive(finished);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1016,55 +1057,34 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int w = 0; w < W; ++w) x += lred[w * C::ROWS + 8 * nt + t2 + e];
                 l[nt][e] = x;
             }
-        if (!part) {
-            write_out(walk.b, walk.u, s.len, v_scale);
-        } else if (!end_of_run) {
+        if (part && !end_of_run) {
             // the run's first part: to its slot, and on with the next segment; the q warp counts it in
             store_part(false);
             __syncwarp();
             if (lane == 0) mbar_arrive(stored);
             early = true;
-            early_b = walk.b, early_u = walk.u, early_unit0 = walk.unit0;
-        } else {
-            last = true;
+            early_b = b, early_u = u, early_scale = v_scale, early_parts = parts;
+            if (lane == 0) mbar_arrive(qempty(buf));
+            continue;
         }
-    }
-    // ---- the run's last part, and its first where that was the last of its unit to be counted in
-    for (int i = 0; i < 2; ++i) {
-        bool write = false, direct = false;
-        int b, u;
-        Parts x;
-        if (i == 0) {
-            if (!last) continue;
-            b = walk.b, u = walk.u;
-            x = parts_of(walk.unit0, walk.s.tiles);
+        if (part) {
             if (walk.t0 == 0) {
                 wait(decided, 0);
                 direct = ok && others_in != 0;
             }
-            write = direct;
             if (!direct) {
                 store_part(walk.t0 == 0);
                 consumer_sync();
-                if (tid == 0) {
-                    fence_acq_rel_gpu();
-                    last_flag = atomicAdd(p.counters + x.first, 1u) == (uint32_t)x.count - 1;
-                    fence_acq_rel_gpu();
-                }
+                if (tid == 0) last_flag = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
                 consumer_sync();
-                write = last_flag != 0;
+                if (last_flag == 0) continue;
             }
-        } else {
-            if (!early) continue;
-            wait(counted, 0);
-            write = ok && late_join != 0;
-            b = early_b, u = early_u;
-            if (write) x = parts_of(early_unit0, span_of<KEYS>(p, b).tiles);
         }
-        if (!write) continue;
-        join(x, direct);
-        const int hk = u / p.row_tiles;
-        write_out(b, u, span_of<KEYS>(p, b).len, p.v_scale ? p.v_scale[hk] : 1.f);
+        }
+        if (part) join(parts, direct);
+        write_out(b, u, v_scale, buf);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty(buf));
     }
     if (!ok && lane == 0) atomicOr(p.status, 1u);
 }

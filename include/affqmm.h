@@ -520,7 +520,8 @@ AFFQMM_API int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cac
  *             h * group + group - 1 (group = heads_q / cache heads) read key
  *             head h
  *   lse       device, fp32 [batch, tokens, heads_q] contiguous, or NULL
- *   table     device, int32 [batch, wide], rows table_stride apart
+ *   table     device, int32 [batch, wide], rows table_stride apart; batch x key
+ *             heads x wide x page below 2^37
  *   lens      device, int32 [batch]: tokens in the cache, the step's own
  *             included; nothing behind them is read
  *   scale     of the scores; finite
