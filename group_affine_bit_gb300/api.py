@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass, field
 
 import torch
@@ -103,12 +104,11 @@ def lib() -> ctypes.CDLL:
             "affqmm_rows_bytes": (i32, [i32, i32, i64, i64, szp]),
             "affqmm_pack_rows": (i32, [wp, vp, vp]),
             "affqmm_embed_rows_copy": (i32, [wp, vp, vp, i64, i32, ctypes.c_uint16, vp, vp, vp]),
-            "affqmm_paged_plan": (i32, [i64, vp, vp, vp, vp, i64, i64, vp, i64, vp, i32, ctypes.POINTER(CStep), vp]),
-            "affqmm_rope_append": (i32, [ctypes.POINTER(CCache), ctypes.POINTER(CRope), *[ctypes.POINTER(CRows)] * 4,
-                                         i64, i32, vp, i64, vp, vp, vp]),
-            "affqmm_paged_attention_workspace_bytes": (i32, [ctypes.POINTER(CCache), i32, i32, szp]),
-            "affqmm_paged_attention": (i32, [ctypes.POINTER(CCache), *[ctypes.POINTER(CLanes)] * 2, vp, i64, i32, i32,
-                                             vp, i64, i64, vp, ctypes.c_float, i32, vp, vp, ctypes.c_size_t, vp]),
+            "affqmm_paged_plan": (i32, [i64, vp, vp, vp, vp, i64, i64, vp, i64, vp, i32, vp, vp]),
+            "affqmm_rope_append": (i32, [vp, vp, vp, vp, vp, vp, i64, i32, vp, i64, vp, vp, vp]),
+            "affqmm_paged_attention_workspace_bytes": (i32, [vp, i32, i32, szp]),
+            "affqmm_paged_attention": (i32, [vp, vp, vp, vp, i64, i32, i32, vp, i64, i64, vp, ctypes.c_float, i32, vp, vp,
+                                             ctypes.c_size_t, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -466,6 +466,9 @@ def embed_rows_copy(w: PackedWeight, rows: torch.Tensor, ids: torch.Tensor, scal
 PAGED_MAX_BATCH = 16384              # requests of a call
 PAGED_MAX_TOKENS = 64                # query tokens of a request
 _KV_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+_BF16, _I32, _F32, _BOOL = torch.bfloat16, torch.int32, torch.float32, torch.bool
+# affqmm_rows and affqmm_lanes as bytes: a small part of what a ctypes structure costs a call
+_ROWS, _LANES = struct.Struct("Pqq").pack, struct.Struct("Pqqq").pack
 
 
 def _check_ints(t: torch.Tensor, name: str, shape: tuple, device=None, dtype=torch.int32, contiguous=True):
@@ -498,12 +501,12 @@ class KVCache:
                 _check_ints(t, name, (k.shape[2],), k.device, torch.float32)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.page, self.heads, self.dim = k.shape
-        self.device = k.device
+        self.device, self._dev = k.device, k.get_device()
         self._c = CCache(_KV_TYPES[k.dtype], self.page, self.heads, self.dim, self.pages, *k.stride()[:3],
                          k.data_ptr() if k.numel() else None, v.data_ptr() if v.numel() else None,
                          k_scale.data_ptr() if k_scale is not None else None,
                          v_scale.data_ptr() if v_scale is not None else None)
-        self._ref = ctypes.byref(self._c)
+        self._ref = ctypes.addressof(self._c)
         self._ws: dict = {}          # (tokens, query heads) -> workspace bytes
 
     @classmethod
@@ -526,10 +529,17 @@ class Rope:
         if axis is not None:
             _check_ints(axis, "axis", tuple(turns.shape), turns.device, torch.uint8)
         self.turns, self.axis, self.neighbour, self.device = turns, axis, bool(neighbour), turns.device
-        self.rotary = 2 * turns.numel()
-        self._c = CRope(turns.data_ptr() if turns.numel() else None, axis.data_ptr() if axis is not None else None,
-                        self.rotary, int(self.neighbour), 1)
-        self._ref = ctypes.byref(self._c)
+        self.rotary, self._dev = 2 * turns.numel(), turns.get_device()
+        self._c: dict = {}           # axes of the positions -> the C view
+
+    def cstruct(self, axes: int) -> int:
+        """The address of the C view for positions of `axes` axes."""
+        c = self._c.get(axes)
+        if c is None:
+            c = self._c[axes] = CRope(self.turns.data_ptr() if self.rotary else None,
+                                      self.axis.data_ptr() if self.axis is not None else None, self.rotary,
+                                      int(self.neighbour), axes)
+        return ctypes.addressof(c)
 
 
 def rope_turns(frequencies, device="cuda") -> torch.Tensor:
@@ -558,10 +568,10 @@ class PagedStep:
         _check_ints(status, "status", (1,), device)
         self.starts, self.lens, self.ring_state, self.status = starts, lens, ring_state, status
         self.slots, self.positions, self.requests = slots, positions, requests
-        self.batch, self.capacity, self.device = batch, capacity, device
+        self.batch, self.capacity, self.device, self._dev = batch, capacity, device, lens.get_device()
         ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
         self._c = CStep(capacity, *[ptr(t) for t in (starts, lens, ring_state, slots, positions, requests, status)])
-        self._ref = ctypes.byref(self._c)
+        self._ref = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, batch: int, capacity: int, device="cuda") -> "PagedStep":
@@ -577,35 +587,25 @@ def paged_plan(lens: torch.Tensor, fresh: torch.Tensor, finished: torch.Tensor |
     pages; ring int32 [pool] of free pages, ring_state int32 [2] its head and
     count.  out.lens and out.ring_state are the next step's lens and
     ring_state; they must be other tensors than this step's."""
-    batch, dev = lens.numel(), out.device
-    if out.batch != batch:
-        raise ValueError(f"out is a step of {out.batch} requests, lens has {batch}")
-    _check_ints(lens, "lens", (batch,), dev)
-    _check_ints(fresh, "fresh", (batch,), dev)
-    if finished is not None:
-        _check_ints(finished, "finished", (batch,), dev, torch.bool)
-    if table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError("table must be two-dimensional, the entries of a row contiguous")
-    wide = table.shape[1]
-    _check_ints(table, "table", (batch, wide), dev, contiguous=False)
-    _check_ints(ring, "ring", (ring.numel(),), dev)
-    _check_ints(ring_state, "ring_state", (2,), dev)
-    sp = _stream_ptr(stream, dev.index)
-    _check(lib().affqmm_paged_plan(batch, lens.data_ptr(), fresh.data_ptr(),
-                                   finished.data_ptr() if finished is not None else None, table.data_ptr(),
-                                   table.stride(0), wide, ring.data_ptr(), ring.numel(), ring_state.data_ptr(), page,
-                                   out._ref, sp), "affqmm_paged_plan")
+    dev = out._dev
+    shape, tshape, tstride = lens.shape, table.shape, table.stride()
+    batch = out.batch
+    if not (shape == (batch,) == fresh.shape and len(tshape) == 2 and tshape[0] == batch and ring.dim() == 1
+            and ring_state.shape == (2,) and lens.dtype is fresh.dtype is table.dtype is ring.dtype is ring_state.dtype is _I32
+            and lens.get_device() == fresh.get_device() == table.get_device() == ring.get_device()
+            == ring_state.get_device() == dev
+            and lens.is_contiguous() and fresh.is_contiguous() and ring.is_contiguous() and ring_state.is_contiguous()
+            and (tstride[1] == 1 or tshape[1] <= 1)
+            and (finished is None or (finished.dtype is _BOOL and finished.shape == shape
+                                      and finished.get_device() == dev and finished.is_contiguous()))):
+        raise ValueError(f"paged_plan wants contiguous CUDA int32 lens and fresh [{batch}] (the requests of out), ring "
+                         f"[pool] and ring_state [2], table [{batch}, wide] with contiguous rows, and bool finished "
+                         f"[{batch}] or None, all on {out.device}")
+    _check((_lib or lib()).affqmm_paged_plan(
+        batch, lens.data_ptr(), fresh.data_ptr(), finished.data_ptr() if finished is not None else None,
+        table.data_ptr(), tstride[0], tshape[1], ring.data_ptr(), ring.shape[0], ring_state.data_ptr(), page, out._ref,
+        _stream_ptr(stream, dev)), "affqmm_paged_plan")
     return out
-
-
-def _check_heads(t: torch.Tensor, name: str, shape: tuple, device):
-    if (not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != shape or t.stride(-1) != 1 or t.device != device):
-        raise ValueError(f"{name} must be a CUDA bf16 {list(shape)} tensor on {device}, the values of a head contiguous")
-
-
-def _rows(t: torch.Tensor) -> CRows:
-    s = t.stride()
-    return CRows(t.data_ptr(), s[0], s[1])
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -617,32 +617,31 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     projection's output serve); positions int32 [tokens] or [axes, tokens];
     slots int32 [tokens], -1 for a token that is not kept.  Returns q turned,
     in `out` (which may be q)."""
-    dev, T = cache.device, q.shape[0]
-    heads, dim = q.shape[1], cache.dim
-    if q.dim() != 3:
+    dev, dim = cache._dev, cache.dim
+    shape, kshape, pshape = q.shape, k.shape, positions.shape
+    if len(shape) != 3:
         raise ValueError("q must be [tokens, query heads, dim]")
-    _check_heads(q, "q", (T, heads, dim), dev)
-    _check_heads(k, "k", (T, cache.heads, dim), dev)
-    _check_heads(v, "v", (T, cache.heads, dim), dev)
+    T = shape[0]
     if out is None:
-        out = torch.empty(T, heads, dim, dtype=torch.bfloat16, device=dev)
-    _check_heads(out, "out", (T, heads, dim), dev)
-    if (not positions.is_cuda or positions.dtype != torch.int32 or positions.device != dev or positions.dim() not in (1, 2)
-            or positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1)):
-        raise ValueError(f"positions must be a CUDA int32 [{T}] or [axes, {T}] tensor on {dev}")
-    if rope.device != dev:
-        raise ValueError(f"the rope must be on {dev}")
-    _check_ints(slots, "slots", (T,), dev)
+        out = torch.empty(shape, dtype=_BF16, device=cache.device)
+    sq, sk, sv, so, sp = q.stride(), k.stride(), v.stride(), out.stride(), positions.stride()
+    if not (shape[2] == dim and out.shape == shape and kshape == (T, cache.heads, dim) == v.shape
+            and q.dtype is k.dtype is v.dtype is out.dtype is _BF16 and sq[2] == sk[2] == sv[2] == so[2] == 1
+            and q.get_device() == k.get_device() == v.get_device() == out.get_device() == positions.get_device()
+            == slots.get_device() == rope._dev == dev
+            and positions.dtype is slots.dtype is _I32 and len(pshape) in (1, 2) and pshape[-1] == T
+            and (sp[-1] == 1 or T <= 1) and slots.shape == (T,) and slots.is_contiguous()):
+        raise ValueError(f"rope_append wants CUDA bf16 q and out [tokens, query heads, {dim}], k and v [tokens, "
+                         f"{cache.heads}, {dim}], the values of a head contiguous, int32 positions [tokens] or [axes, "
+                         f"tokens] and slots [tokens], and the rope, all on {cache.device}")
     if T == 0:
         return out
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    c = rope._c
-    if c.axes != axes:
-        c.axes = axes
-    _check(lib().affqmm_rope_append(cache._ref, rope._ref, _rows(q), _rows(k), _rows(v), _rows(out), T, heads,
-                                    positions.data_ptr(), positions.stride(0) if axes > 1 else 0, slots.data_ptr(),
-                                    status.data_ptr() if status is not None else None, _stream_ptr(stream, dev.index)),
-           "affqmm_rope_append")
+    axes = pshape[0] if len(pshape) == 2 else 1
+    _check((_lib or lib()).affqmm_rope_append(
+        cache._ref, rope.cstruct(axes), _ROWS(q.data_ptr(), sq[0], sq[1]), _ROWS(k.data_ptr(), sk[0], sk[1]),
+        _ROWS(v.data_ptr(), sv[0], sv[1]), _ROWS(out.data_ptr(), so[0], so[1]), T, shape[1], positions.data_ptr(),
+        sp[0] if axes > 1 else 0, slots.data_ptr(), status.data_ptr() if status is not None else None,
+        _stream_ptr(stream, dev)), "affqmm_rope_append")
     return out
 
 
@@ -657,11 +656,6 @@ def paged_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> 
     return need
 
 
-def _lanes(t: torch.Tensor) -> CLanes:
-    s = t.stride()
-    return CLanes(t.data_ptr(), s[0], s[1], s[2]) if len(s) == 4 else CLanes(t.data_ptr(), s[0], 0, s[1])
-
-
 def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
                     window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     status: torch.Tensor | None = None, workspace: Workspace | None = None, stream=None) -> torch.Tensor:
@@ -672,31 +666,31 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     the last `window` keys of each token.  `lse` (float32, q's shape without its
     last axis) gets the log of each row's sum of exponentials.  Returns `out`,
     of q's shape."""
-    dev, dim, shape = cache.device, cache.dim, q.shape
+    dev, dim, shape = cache._dev, cache.dim, q.shape
     if len(shape) == 4:
         batch, tokens, heads, d = shape
     elif len(shape) == 3:
         (batch, heads, d), tokens = shape, 1
     else:
         raise ValueError("q must be [batch, query heads, dim] or [batch, tokens, query heads, dim]")
-    if d != dim:
-        raise ValueError(f"q has {d} values a head, the cache {dim}")
-    _check_heads(q, "q", shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _check_heads(out, "out", shape, dev)
-    if table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError("table must be two-dimensional, the entries of a row contiguous")
-    wide = table.shape[1]
-    _check_ints(table, "table", (batch, wide), dev, contiguous=False)
-    _check_ints(lens, "lens", (batch,), dev)
-    if lse is not None:
-        _check_ints(lse, "lse", tuple(shape[:-1]), dev, torch.float32)
-    sp = _stream_ptr(stream, dev.index)
-    buf = (workspace or default_workspace(dev.index, sp)).get(paged_attention_workspace_bytes(cache, tokens, heads))
-    _check(lib().affqmm_paged_attention(cache._ref, _lanes(q), _lanes(out), lse.data_ptr() if lse is not None else None,
-                                        batch, tokens, heads, table.data_ptr(), table.stride(0), wide, lens.data_ptr(),
-                                        dim ** -0.5 if scale is None else scale, window,
-                                        status.data_ptr() if status is not None else None, buf.data_ptr(), buf.numel(),
-                                        sp), "affqmm_paged_attention")
+        out = torch.empty(shape, dtype=_BF16, device=cache.device)
+    sq, so, st, tshape = q.stride(), out.stride(), table.stride(), table.shape
+    if not (d == dim and out.shape == shape and q.dtype is out.dtype is _BF16 and sq[-1] == so[-1] == 1
+            and q.get_device() == out.get_device() == table.get_device() == lens.get_device() == dev
+            and table.dtype is lens.dtype is _I32 and len(tshape) == 2 and tshape[0] == batch
+            and (st[1] == 1 or tshape[1] <= 1) and lens.shape == (batch,) and lens.is_contiguous()
+            and (lse is None or (lse.dtype is _F32 and lse.shape == shape[:-1] and lse.get_device() == dev
+                                 and lse.is_contiguous()))):
+        raise ValueError(f"paged_attention wants CUDA bf16 q and out of one shape, {dim} contiguous values a head, int32 "
+                         f"table [{batch}, wide] with contiguous rows and lens [{batch}], and float32 lse {list(shape[:-1])} "
+                         f"or None, all on {cache.device}")
+    sp = _stream_ptr(stream, dev)
+    buf = (workspace or default_workspace(dev, sp)).get(
+        cache._ws.get((tokens, heads)) or paged_attention_workspace_bytes(cache, tokens, heads))
+    _check((_lib or lib()).affqmm_paged_attention(
+        cache._ref, _LANES(q.data_ptr(), sq[0], sq[-3], sq[-2]), _LANES(out.data_ptr(), so[0], so[-3], so[-2]),
+        lse.data_ptr() if lse is not None else None, batch, tokens, heads, table.data_ptr(), st[0], tshape[1],
+        lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
+        status.data_ptr() if status is not None else None, buf.data_ptr(), buf.numel(), sp), "affqmm_paged_attention")
     return out
