@@ -9,12 +9,14 @@
 // ones behind the back, so nothing that is read here is also written, and the
 // same call on the same inputs writes the same values.
 //
-// One launch.  Every CTA makes the prefix sums for itself (two block scans of
-// at most 16 requests a thread, from L2) and keeps them in shared memory,
-// eight bytes a request, rather than waiting for another CTA's; then each
-// takes its share of the tokens, four to a thread, finds their request by
-// bisection and writes slot, position and request with 16-byte stores.  The
-// call is bound by latency: lengths, scan, table or ring entry, store.
+// One launch.  Every CTA makes the prefix sums for itself, from L2, rather than
+// waiting for another CTA's: its requests are loaded once, into registers (1 to
+// 16 a thread, by the batch), scanned in two rounds (tokens and returned pages,
+// then needed pages, which depend on which requests fit) and kept in shared
+// memory, twelve bytes a request.  Then each CTA takes its share of the tokens,
+// four to a thread, finds their request by bisection and writes slot, position
+// and request with 16-byte stores.  The call is bound by latency: lengths,
+// scans, table or ring entry, store.
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
 
@@ -27,28 +29,31 @@ constexpr uint32_t PL_SERVED = 1u << 31, PL_FINISHED = 1u << 30;
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, PL_MOST); }
 
-// Exclusive prefix sum over the block's threads (saturating, so the order of
-// the additions does not matter); `total` gets the block's sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
+// Exclusive prefix sums of two values over the block's threads (saturating, so
+// the order of the additions does not matter), and their totals.
+struct Pair {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* warp_sums, Pair* total) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    uint32_t x = v;
+    Pair x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, x, d);
-        if (lane >= d) x = sat_add(x, y);
+        const uint32_t a = __shfl_up_sync(~0u, x.a, d), b = __shfl_up_sync(~0u, x.b, d);
+        if (lane >= d) x.a = sat_add(x.a, a), x.b = sat_add(x.b, b);
     }
     if (lane == 31) warp_sums[wid] = x;
     __syncthreads();
-    uint32_t w = warp_sums[lane];
+    Pair w = warp_sums[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, w, d);
-        if (lane >= d) w = sat_add(w, y);
+        const uint32_t a = __shfl_up_sync(~0u, w.a, d), b = __shfl_up_sync(~0u, w.b, d);
+        if (lane >= d) w.a = sat_add(w.a, a), w.b = sat_add(w.b, b);
     }
-    *total = __shfl_sync(~0u, w, 31);
-    const uint32_t before_warp = __shfl_sync(~0u, w, (wid + 31) & 31);
-    const uint32_t up = __shfl_up_sync(~0u, x, 1);
-    return sat_add(wid ? before_warp : 0u, lane ? up : 0u);
+    *total = {__shfl_sync(~0u, w.a, 31), __shfl_sync(~0u, w.b, 31)};
+    const Pair before = {__shfl_sync(~0u, w.a, (wid + 31) & 31), __shfl_sync(~0u, w.b, (wid + 31) & 31)};
+    const Pair up = {__shfl_up_sync(~0u, x.a, 1), __shfl_up_sync(~0u, x.b, 1)};
+    return {sat_add(wid ? before.a : 0u, lane ? up.a : 0u), sat_add(wid ? before.b : 0u, lane ? up.b : 0u)};
 }
 
 struct Ask {
@@ -67,83 +72,93 @@ __device__ __forceinline__ Ask ask_of(const PlanParams& p, int i) {
     return a;
 }
 
+template <int EACH>
 __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
     extern __shared__ uint32_t plan_smem[];
     uint32_t* starts = plan_smem;                   // [batch + 1] first token of each request
     uint32_t* first = plan_smem + p.batch + 1;      // [batch] first page taken (or given back), and the flags
-    __shared__ uint32_t warp_sums[4][32];
+    uint32_t* length = first + p.batch;             // [batch] tokens in the cache
+    __shared__ Pair warp_sums[2][32];
     __shared__ uint32_t flags, taken;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x;
     const uint32_t page_mask = (1u << p.page_shift) - 1u;
     if (tid == 0) flags = 0, taken = 0;
+    // requests i0 .. i0 + EACH - 1 are this thread's
+    const int i0 = tid * EACH;
+    Ask ask[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        ask[k] = {0, 0, false, false};
+        if (i0 + k < p.batch) ask[k] = ask_of(p, i0 + k);
+    }
     const int32_t head_in = p.ring_state[0], free_in = p.ring_state[1];
     const bool ring_ok = head_in >= 0 && head_in < p.pool && free_in >= 0 && free_in <= p.pool;
     const uint32_t head = ring_ok ? (uint32_t)head_in : 0u, free = ring_ok ? (uint32_t)free_in : 0u;
     const uint32_t pool = (uint32_t)p.pool;
 
-    // requests i0 .. i1 - 1 are this thread's
-    const int each = (p.batch + PL_THREADS - 1) / PL_THREADS;
-    const int i0 = min(tid * each, p.batch), i1 = min(i0 + each, p.batch);
-    uint32_t sum = 0, total;
-    for (int i = i0; i < i1; ++i) sum = sat_add(sum, ask_of(p, i).fresh);
-    const uint32_t token0 = block_scan(sum, warp_sums[0], &total);
-
-    uint32_t need_sum = 0, back_sum = 0, bits = ring_ok ? 0u : 8u, at = token0;
-    for (int i = i0; i < i1; ++i) {
-        const Ask a = ask_of(p, i);
-        const uint32_t held = (a.len + page_mask) >> p.page_shift;
-        starts[i] = at;
-        at = sat_add(at, a.fresh);
-        const bool wide_ok = (uint64_t)a.len + a.fresh <= (uint64_t)p.wide << p.page_shift;
-        const bool room = at <= (uint32_t)p.capacity;
-        const bool fits = !a.done && !a.bad && wide_ok && room;
-        if (a.bad) bits |= 8u;
-        if (!a.done && !wide_ok) bits |= 2u;
-        if (!a.done && !room) bits |= 4u;
-        need_sum = sat_add(need_sum, fits ? ((a.len + a.fresh + page_mask) >> p.page_shift) - held : 0u);
-        back_sum = sat_add(back_sum, a.done ? held : 0u);
+    Pair sum = {0, 0}, total, needed;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        sum.a = sat_add(sum.a, ask[k].fresh);
+        sum.b = sat_add(sum.b, ask[k].done ? (ask[k].len + page_mask) >> p.page_shift : 0u);
     }
-    if (tid == 0) starts[p.batch] = total;
-    uint32_t need_total, back_total;
-    const uint32_t need0 = block_scan(need_sum, warp_sums[1], &need_total);
-    const uint32_t back0 = block_scan(back_sum, warp_sums[2], &back_total);
+    const Pair at0 = block_scan(sum, warp_sums[0], &total);
+    const uint32_t tokens = total.a, back_total = total.b;
     const bool back_ok = (uint64_t)free + back_total <= pool;   // else the ring's count and the requests disagree
-    if (!back_ok) bits |= 8u;
-
-    uint32_t need_at = need0, back_at = back0, got = 0;
-    for (int i = i0; i < i1; ++i) {
-        const Ask a = ask_of(p, i);
-        const uint32_t held = (a.len + page_mask) >> p.page_shift;
-        const uint32_t end = sat_add(starts[i], a.fresh);
-        const bool fits = !a.done && !a.bad && (uint64_t)a.len + a.fresh <= (uint64_t)p.wide << p.page_shift &&
-                          end <= (uint32_t)p.capacity;
-        const uint32_t need = fits ? ((a.len + a.fresh + page_mask) >> p.page_shift) - held : 0u;
+    uint32_t bits = (ring_ok ? 0u : 8u) | (back_ok ? 0u : 8u), at = at0.a;
+    uint32_t need[EACH];
+    bool fits[EACH];
+    Pair want = {0, 0};
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const Ask& a = ask[k];
+        const uint32_t end = sat_add(at, a.fresh);
+        const bool wide_ok = (uint64_t)a.len + a.fresh <= (uint64_t)p.wide << p.page_shift, room = end <= (uint32_t)p.capacity;
+        need[k] = 0;
+        fits[k] = false;
+        if (i0 + k < p.batch) {
+            starts[i0 + k] = at;
+            length[i0 + k] = a.len;
+            fits[k] = !a.done && !a.bad && wide_ok && room;
+            if (a.bad) bits |= 8u;
+            if (!a.done && !wide_ok) bits |= 2u;
+            if (!a.done && !room) bits |= 4u;
+            if (fits[k]) need[k] = ((a.len + a.fresh + page_mask) >> p.page_shift) - ((a.len + page_mask) >> p.page_shift);
+            if (blockIdx.x == 0) p.starts[i0 + k] = (int32_t)at;
+        }
+        at = end;
+        want.a = sat_add(want.a, need[k]);
+    }
+    if (tid == 0) starts[p.batch] = tokens;
+    uint32_t need_at = block_scan(want, warp_sums[1], &needed).a, back_at = at0.b, got = 0;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const Ask& a = ask[k];
         const uint32_t before = need_at;
-        need_at = sat_add(need_at, need);
-        const bool served = fits && (need == 0 || need_at <= free);
-        if (fits && !served) bits |= 1u;
-        if (served && need) got = need_at;
+        need_at = sat_add(need_at, need[k]);
+        const bool served = fits[k] && (need[k] == 0 || need_at <= free);
+        if (fits[k] && !served) bits |= 1u;
+        if (served && need[k]) got = need_at;
         uint32_t word = served ? (before | PL_SERVED) : before;
         if (a.done) {
             word = back_at | PL_FINISHED;
-            back_at = sat_add(back_at, held);
+            back_at = sat_add(back_at, (a.len + page_mask) >> p.page_shift);
         }
-        first[i] = word;
-        if (blockIdx.x == 0) {
-            p.starts[i] = (int32_t)starts[i];
-            p.lens_out[i] = a.done ? 0 : (served ? (int32_t)(a.len + a.fresh) : p.lens[i]);
+        if (i0 + k < p.batch) {
+            first[i0 + k] = word;
+            if (blockIdx.x == 0)
+                p.lens_out[i0 + k] = a.done ? 0 : a.bad ? p.lens[i0 + k] : (int32_t)(a.len + (served ? a.fresh : 0u));
         }
     }
     if (bits) atomicOr(&flags, bits);
     if (got) atomicMax(&taken, got);
     __syncthreads();
     if (blockIdx.x == 0 && tid == 0) {
-        p.starts[p.batch] = (int32_t)total;
-        const uint32_t back = back_ok ? back_total : 0u;
+        p.starts[p.batch] = (int32_t)tokens;
         const uint32_t moved = head + taken;
         p.ring_state_out[0] = (int32_t)(moved >= pool ? moved - pool : moved);
-        p.ring_state_out[1] = (int32_t)(free - taken + back);
+        p.ring_state_out[1] = (int32_t)(free - taken + (back_ok ? back_total : 0u));
         p.status[0] = (int32_t)flags;
     }
 
@@ -152,7 +167,7 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
     for (int64_t qd = (int64_t)blockIdx.x * PL_THREADS + tid; qd < quads; qd += (int64_t)gridDim.x * PL_THREADS) {
         const uint32_t t0 = (uint32_t)qd << 2;
         int r = p.batch;
-        if (t0 < total) {   // the last request that starts at or before t0
+        if (t0 < tokens) {   // the last request that starts at or before t0
             int lo = 0, hi = p.batch;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -162,17 +177,20 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
             r = lo;
         }
         int32_t slot[4], pos[4], req[4];
-        uint32_t len = 0, word = 0;
+        uint32_t len = 0, word = 0, have_pg = 0;
+        int32_t page = -1;       // page have_pg of request `have`: one entry serves the tokens in it
         int have = -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t t = t0 + e;
             slot[e] = -1, pos[e] = 0, req[e] = -1;
-            if (t < total) {
+            if (t < tokens) {
                 while (starts[r + 1] <= t) ++r;
+                bool look = false;
                 if (have != r) {
                     have = r;
-                    len = (uint32_t)p.lens[r];
+                    look = true;
+                    len = length[r];
                     word = first[r];
                 }
                 const uint32_t place = len + (t - starts[r]);
@@ -181,15 +199,13 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
                 if (word & PL_SERVED) {
                     const uint32_t held = (len + page_mask) >> p.page_shift, pg = place >> p.page_shift;
                     int32_t* entry = p.table + (int64_t)r * p.table_stride + pg;
-                    int32_t page;
-                    if (pg >= held) {
+                    if (look || pg != have_pg) {
+                        have_pg = pg;
                         uint32_t x = head + (word & PL_MOST) + (pg - held);
                         if (x >= pool) x -= pool;
-                        page = p.ring[x];
-                        if ((place & page_mask) == 0) *entry = page;
-                    } else {
-                        page = *entry;
+                        page = pg >= held ? p.ring[x] : *entry;
                     }
+                    if (pg >= held && (place & page_mask) == 0) *entry = page;
                     slot[e] = (int32_t)(((uint32_t)page << p.page_shift) | (place & page_mask));
                 }
             }
@@ -210,13 +226,22 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
         for (int i = blockIdx.x * (PL_THREADS / 32) + (tid >> 5); i < p.batch; i += warps) {
             const uint32_t word = first[i];
             if ((word & (PL_SERVED | PL_FINISHED)) != PL_FINISHED) continue;
-            const Ask a = ask_of(p, i);
-            const uint32_t held = (a.len + page_mask) >> p.page_shift;
-            for (uint32_t j = lane; j < held; j += 32) {
-                uint32_t x = head + free + (word & PL_MOST) + j;
-                if (x >= pool) x -= pool;
-                if (x >= pool) x -= pool;
-                p.ring[x] = p.table[(int64_t)i * p.table_stride + j];
+            const uint32_t held = (length[i] + page_mask) >> p.page_shift;
+            const int32_t* row = p.table + (int64_t)i * p.table_stride;
+            constexpr int GO = 8;    // loads in flight
+            for (uint32_t j0 = lane; j0 < held; j0 += 32 * GO) {
+                int32_t page[GO];
+#pragma unroll
+                for (int k = 0; k < GO; ++k)
+                    if (j0 + 32 * k < held) page[k] = row[j0 + 32 * k];
+#pragma unroll
+                for (int k = 0; k < GO; ++k)
+                    if (j0 + 32 * k < held) {
+                        uint32_t x = head + free + (word & PL_MOST) + j0 + 32 * k;
+                        if (x >= pool) x -= pool;
+                        if (x >= pool) x -= pool;
+                        p.ring[x] = page[k];
+                    }
             }
         }
     }
@@ -224,19 +249,27 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
 
 }  // namespace
 
+namespace {
+template <int EACH>
+cudaError_t launch_each(const PlanParams& p, unsigned grid, size_t smem, cudaStream_t st) {
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel<EACH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(paged_plan_kernel<EACH>, dim3(grid), PL_THREADS, smem, st, p);
+}
+}  // namespace
+
 cudaError_t launch_paged_plan(const PlanParams& p, int sms, cudaStream_t st) {
-    const size_t smem = ((size_t)2 * p.batch + 1) * sizeof(uint32_t);
+    const size_t smem = ((size_t)3 * p.batch + 1) * sizeof(uint32_t);
     // a CTA for each 4096 tokens and for each 256 requests, up to one an SM
     int64_t grid = ((int64_t)p.capacity + 4095) / 4096;
     if (grid < (p.batch + 255) / 256) grid = (p.batch + 255) / 256;
     if (grid > sms) grid = sms;
     if (grid < 1) grid = 1;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (2 * AFFQMM_PAGED_MAX_BATCH + 1) * (int)sizeof(uint32_t));
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(paged_plan_kernel, dim3((unsigned)grid), PL_THREADS, smem, st, p);
+    if (p.batch <= PL_THREADS) return launch_each<1>(p, (unsigned)grid, smem, st);
+    if (p.batch <= 4 * PL_THREADS) return launch_each<4>(p, (unsigned)grid, smem, st);
+    return launch_each<16>(p, (unsigned)grid, smem, st);
 }
 
 }  // namespace affqmm

@@ -18,7 +18,9 @@
 // Bound by memory: each value is read once and written once, 16 bytes a
 // thread.  One CTA takes one token, so that the token's sines are made once
 // and serve every head from shared memory; with few tokens several CTAs share
-// a token's heads.
+// a token's heads.  The instructions beside the bytes are kept few: v and what
+// does not turn is copied as it is (bf16), and a piece's head comes from one
+// multiplication.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -28,7 +30,7 @@
 namespace affqmm {
 namespace {
 
-constexpr int RA_THREADS = 256;
+constexpr int RA_THREADS = 128;
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -71,111 +73,112 @@ __device__ __forceinline__ void put1(const Row& r, int d, float x) {
     else *reinterpret_cast<__nv_bfloat16*>(r.p + 2 * d) = __float2bfloat16_rn(x);
 }
 
+__device__ __forceinline__ void copy8(const Row& r, int d, const uint16_t* src) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src + d);
+    if (r.bytes) {
+        float x[8];
+        unpack8(w, x);
+        put8(r, d, x);
+    } else {
+        *reinterpret_cast<uint4*>(r.p + 2 * d) = w;
+    }
+}
+
+// n / d by m = ceil(2^32 / d), exact for n < 2^32 / d (heads <= 8192, pieces <= 512)
+__device__ __forceinline__ int over(int n, uint32_t m, int d) { return d == 1 ? n : (int)__umulhi((uint32_t)n, m); }
+
 // WIDE: eight neighbouring values (half pairs: twice eight) to a thread, where
 // rotary / 2 (half pairs) or rotary / 8 allows it; otherwise a pair or a
-// single value to a thread.
+// single value to a thread.  The pieces of a head: `spun` that turn, `still`
+// that do not, and `per_v` of v; m_*: their reciprocals.
 template <bool NEIGHBOUR, bool WIDE>
-__global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(RopeParams p) {
-    __shared__ __align__(16) float2 turn[256];   // (cos, sin) of the token's pairs
+__global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(RopeParams p, int spun, int still, int per_v, uint32_t m_spun,
+                                                                 uint32_t m_still, uint32_t m_v) {
+    __shared__ __align__(16) float cosines[256], sines[256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t t = blockIdx.x;
-    const int half = p.rotary >> 1, D = p.dim;
+    const int half = p.rotary >> 1, step = gridDim.y * RA_THREADS, idx0 = blockIdx.y * RA_THREADS + threadIdx.x;
+    const int32_t slot = p.slots[t];
     for (int i = threadIdx.x; i < half; i += RA_THREADS) {
         const int a = p.axis ? min((int)p.axis[i], p.axes - 1) : 0;
         const int64_t pos = p.positions[a * p.pos_stride + t];
         const int64_t phase = (int64_t)((uint64_t)pos * (uint64_t)p.turns[i]);   // modulo a whole turn
-        float s, c;
-        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-        turn[i] = make_float2(c, s);
+        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sines[i], &cosines[i]);
     }
-    const int32_t slot = p.slots[t];
     const int64_t page = slot >> p.page_shift;
     const bool kept = slot >= 0 && page < p.pages;
     if (slot < -1 || (slot >= 0 && !kept))
         if (p.status && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, 2u);
     const int64_t at = page * p.page_bytes + (int64_t)(slot & ((1 << p.page_shift) - 1)) * p.token_bytes;
-    __syncthreads();
-
-    const int spun = WIDE ? (NEIGHBOUR ? p.rotary >> 3 : p.rotary >> 4) : half;   // work items that turn, of a head
-    const int per = spun + (WIDE ? (D - p.rotary) >> 3 : D - p.rotary);
-    const int per_v = WIDE ? D >> 3 : D;
-    const int turned = (p.heads_q + p.heads_kv) * per, items = turned + p.heads_kv * per_v;
-    for (int idx = blockIdx.y * RA_THREADS + threadIdx.x; idx < items; idx += gridDim.y * RA_THREADS) {
+    const uint16_t *q = p.q + t * p.q_ts, *k = p.k + t * p.k_ts, *v = p.v + t * p.v_ts;
+    uint16_t* out = p.out + t * p.o_ts;
+    // the source and the target of head h of q and k
+    auto ends = [&](int h, const uint16_t*& src, Row& dst) {
+        const int hk = h - p.heads_q;
+        if (hk < 0) {
+            src = q + h * p.q_hs;
+            dst.p = reinterpret_cast<uint8_t*>(out + h * p.o_hs);
+            dst.bytes = false;
+        } else {
+            src = k + hk * p.k_hs;
+            dst.p = p.kc + at + hk * p.head_bytes;
+            dst.bytes = p.e4m3;
+            dst.scale = p.k_scale ? p.k_scale[hk] : 1.f;
+        }
+    };
+    const int heads = p.heads_q + (kept ? p.heads_kv : 0);
+    if (kept)
+#pragma unroll 2
+        for (int i = idx0; i < p.heads_kv * per_v; i += step) {
+            const int h = over(i, m_v, per_v), d = i - h * per_v;
+            const Row dst = {p.vc + at + h * p.head_bytes, p.v_scale ? p.v_scale[h] : 1.f, (bool)p.e4m3};
+            if (WIDE) copy8(dst, 8 * d, v + h * p.v_hs);
+            else put1(dst, d, __uint_as_float((uint32_t)v[h * p.v_hs + d] << 16));
+        }
+    for (int i = idx0; i < heads * still; i += step) {
+        const int h = over(i, m_still, still), d = i - h * still;
         const uint16_t* src;
         Row dst;
-        int it;
-        bool value = false;
-        if (idx < turned) {
-            const int h = idx / per;
-            it = idx - h * per;
-            if (h < p.heads_q) {
-                src = p.q + t * p.q_ts + h * p.q_hs;
-                dst.p = reinterpret_cast<uint8_t*>(p.out + t * p.o_ts + h * p.o_hs);
-                dst.bytes = false;
-            } else {
-                if (!kept) continue;
-                const int hk = h - p.heads_q;
-                src = p.k + t * p.k_ts + hk * p.k_hs;
-                dst.p = p.kc + at + hk * p.head_bytes;
-                dst.bytes = p.e4m3;
-                dst.scale = p.k_scale ? p.k_scale[hk] : 1.f;
-            }
+        ends(h, src, dst);
+        if (WIDE) copy8(dst, p.rotary + 8 * d, src);
+        else put1(dst, p.rotary + d, __uint_as_float((uint32_t)src[p.rotary + d] << 16));
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int i = idx0; i < heads * spun; i += step) {
+        const int h = over(i, m_spun, spun), piece = i - h * spun;
+        const uint16_t* src;
+        Row dst;
+        ends(h, src, dst);
+        if constexpr (!WIDE) {
+            const int da = NEIGHBOUR ? 2 * piece : piece, db = NEIGHBOUR ? 2 * piece + 1 : piece + half;
+            const float a = __uint_as_float((uint32_t)src[da] << 16), b = __uint_as_float((uint32_t)src[db] << 16);
+            put1(dst, da, a * cosines[piece] - b * sines[piece]);
+            put1(dst, db, a * sines[piece] + b * cosines[piece]);
+        } else if constexpr (NEIGHBOUR) {
+            float x[8], y[8];
+            unpack8(*reinterpret_cast<const uint4*>(src + 8 * piece), x);
+            const float4 c = *reinterpret_cast<const float4*>(cosines + 4 * piece), s = *reinterpret_cast<const float4*>(sines + 4 * piece);
+            y[0] = x[0] * c.x - x[1] * s.x, y[1] = x[0] * s.x + x[1] * c.x;
+            y[2] = x[2] * c.y - x[3] * s.y, y[3] = x[2] * s.y + x[3] * c.y;
+            y[4] = x[4] * c.z - x[5] * s.z, y[5] = x[4] * s.z + x[5] * c.z;
+            y[6] = x[6] * c.w - x[7] * s.w, y[7] = x[6] * s.w + x[7] * c.w;
+            put8(dst, 8 * piece, y);
         } else {
-            if (!kept) continue;
-            const int hk = (idx - turned) / per_v;
-            it = idx - turned - hk * per_v;
-            src = p.v + t * p.v_ts + hk * p.v_hs;
-            dst.p = p.vc + at + hk * p.head_bytes;
-            dst.bytes = p.e4m3;
-            dst.scale = p.v_scale ? p.v_scale[hk] : 1.f;
-            value = true;
-        }
-        if constexpr (WIDE) {
-            if (value || it >= spun) {   // as it is
-                const int d = value ? 8 * it : p.rotary + 8 * (it - spun);
-                float x[8];
-                unpack8(*reinterpret_cast<const uint4*>(src + d), x);
-                put8(dst, d, x);
-            } else if constexpr (NEIGHBOUR) {
-                float x[8], y[8];
-                unpack8(*reinterpret_cast<const uint4*>(src + 8 * it), x);
-                const float4* cs = reinterpret_cast<const float4*>(turn + 4 * it);
+            const uint4 wa = *reinterpret_cast<const uint4*>(src + 8 * piece), wb = *reinterpret_cast<const uint4*>(src + half + 8 * piece);
+            float a[8], b[8], ya[8], yb[8];
+            unpack8(wa, a);
+            unpack8(wb, b);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float4 w = cs[e];
-                    y[4 * e] = x[4 * e] * w.x - x[4 * e + 1] * w.y;
-                    y[4 * e + 1] = x[4 * e] * w.y + x[4 * e + 1] * w.x;
-                    y[4 * e + 2] = x[4 * e + 2] * w.z - x[4 * e + 3] * w.w;
-                    y[4 * e + 3] = x[4 * e + 2] * w.w + x[4 * e + 3] * w.z;
-                }
-                put8(dst, 8 * it, y);
-            } else {
-                float a[8], b[8], ya[8], yb[8];
-                unpack8(*reinterpret_cast<const uint4*>(src + 8 * it), a);
-                unpack8(*reinterpret_cast<const uint4*>(src + half + 8 * it), b);
-                const float4* cs = reinterpret_cast<const float4*>(turn + 8 * it);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 w = cs[e];
-                    ya[2 * e] = a[2 * e] * w.x - b[2 * e] * w.y;
-                    yb[2 * e] = a[2 * e] * w.y + b[2 * e] * w.x;
-                    ya[2 * e + 1] = a[2 * e + 1] * w.z - b[2 * e + 1] * w.w;
-                    yb[2 * e + 1] = a[2 * e + 1] * w.w + b[2 * e + 1] * w.z;
-                }
-                put8(dst, 8 * it, ya);
-                put8(dst, half + 8 * it, yb);
+            for (int e = 0; e < 8; e += 4) {
+                const float4 c = *reinterpret_cast<const float4*>(cosines + 8 * piece + e), s = *reinterpret_cast<const float4*>(sines + 8 * piece + e);
+                ya[e] = a[e] * c.x - b[e] * s.x, yb[e] = a[e] * s.x + b[e] * c.x;
+                ya[e + 1] = a[e + 1] * c.y - b[e + 1] * s.y, yb[e + 1] = a[e + 1] * s.y + b[e + 1] * c.y;
+                ya[e + 2] = a[e + 2] * c.z - b[e + 2] * s.z, yb[e + 2] = a[e + 2] * s.z + b[e + 2] * c.z;
+                ya[e + 3] = a[e + 3] * c.w - b[e + 3] * s.w, yb[e + 3] = a[e + 3] * s.w + b[e + 3] * c.w;
             }
-        } else {
-            if (value || it >= spun) {
-                const int d = value ? it : p.rotary + it - spun;
-                put1(dst, d, __uint_as_float((uint32_t)src[d] << 16));
-            } else {
-                const int da = NEIGHBOUR ? 2 * it : it, db = NEIGHBOUR ? 2 * it + 1 : it + half;
-                const float a = __uint_as_float((uint32_t)src[da] << 16), b = __uint_as_float((uint32_t)src[db] << 16);
-                const float2 w = turn[it];
-                put1(dst, da, a * w.x - b * w.y);
-                put1(dst, db, a * w.y + b * w.x);
-            }
+            put8(dst, 8 * piece, ya);
+            put8(dst, half + 8 * piece, yb);
         }
     }
 }
@@ -184,19 +187,18 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(RopeParams p) {
 
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t st) {
     const bool wide = p.neighbour ? p.rotary % 8 == 0 : p.rotary % 16 == 0;
-    const int per = wide ? (p.neighbour ? p.dim / 8 : p.rotary / 16 + (p.dim - p.rotary) / 8) : p.dim - p.rotary / 2;
-    const int items = (p.heads_q + p.heads_kv) * per + p.heads_kv * (wide ? p.dim / 8 : p.dim);
-    // with few tokens, as many CTAs a token as fill the SMs and find an item for each thread
-    int64_t split = (sms + p.tokens - 1) / p.tokens;
-    const int most = (items + RA_THREADS - 1) / RA_THREADS;
+    const int spun = wide ? (p.neighbour ? p.rotary / 8 : p.rotary / 16) : p.rotary / 2;
+    const int still = wide ? (p.dim - p.rotary) / 8 : p.dim - p.rotary, per_v = wide ? p.dim / 8 : p.dim;
+    auto reciprocal = [](int d) { return d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u; };
+    // with few tokens, as many CTAs a token as fill the SMs and find a piece for each thread
+    int64_t split = (2 * sms + p.tokens - 1) / p.tokens;
+    const int most = ((p.heads_q + p.heads_kv) * (spun > still ? spun : still) + RA_THREADS - 1) / RA_THREADS;
     if (split > most) split = most;
     if (split < 1) split = 1;
     const dim3 grid((unsigned)p.tokens, (unsigned)split);
-    if (p.neighbour)
-        return wide ? launch_pdl(rope_append_kernel<true, true>, grid, RA_THREADS, 0, st, p)
-                    : launch_pdl(rope_append_kernel<true, false>, grid, RA_THREADS, 0, st, p);
-    return wide ? launch_pdl(rope_append_kernel<false, true>, grid, RA_THREADS, 0, st, p)
-                : launch_pdl(rope_append_kernel<false, false>, grid, RA_THREADS, 0, st, p);
+    auto* kernel = p.neighbour ? (wide ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
+                               : (wide ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
+    return launch_pdl(kernel, grid, RA_THREADS, 0, st, p, spun, still, per_v, reciprocal(spun), reciprocal(still), reciprocal(per_v));
 }
 
 }  // namespace affqmm
