@@ -60,6 +60,7 @@ struct AttnParams {
     const int32_t* lens;
     int32_t batch, tokens, heads_q, heads_kv, group, dim, wide, page_shift, window;
     int32_t row_tiles;           // tiles of 8 NT (token, head) rows
+    uint32_t m_group, m_row_tiles;   // ceil(2^32 / d) of the two
     float scale_log2;            // softmax scale times log2(e)
     uint32_t* user_status;       // or null
     uint32_t* status;            // workspace: status word, merge counters, partial slots

@@ -142,6 +142,8 @@ AttnShape attn_shape(const affqmm_kv_cache* c, int rows) {
     }
 }
 
+uint32_t reciprocal(int d) { return d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u; }
+
 int check_heads(const affqmm_kv_cache* c, int tokens, int heads_q) {
     if (tokens < 1 || tokens > AFFQMM_PAGED_MAX_TOKENS) return AFFQMM_E_ARG;
     if (heads_q < 1 || heads_q > 4096 || heads_q % c->heads) return AFFQMM_E_SHAPE;
@@ -317,6 +319,7 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     p.page_shift = page_shift_of(cache->page);
     p.window = window;
     p.row_tiles = (rows + shape.rows - 1) / shape.rows;
+    p.m_group = reciprocal(p.group), p.m_row_tiles = reciprocal(p.row_tiles);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.user_status = status;
     uint8_t* base = static_cast<uint8_t*>(workspace);
@@ -328,7 +331,7 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     int64_t keys = row_keys;
     // a window's keys, from a multiple of a tile on
     if (window > 0 && keys > (int64_t)window + tokens + shape.keys) keys = (int64_t)window + tokens + shape.keys;
-    const int64_t tiles = batch * cache->heads * p.row_tiles * (keys < shape.keys ? 1 : (keys + shape.keys - 1) / shape.keys);
+    const int64_t tiles = batch * cache->heads * p.row_tiles * ((keys < shape.keys ? 1 : (keys + shape.keys - 1) / shape.keys) + 1);
     if (tiles >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
     const int64_t most = (int64_t)sms * shape.ctas_per_sm;
     const int grid = (int)(tiles < most ? tiles : most);

@@ -145,6 +145,20 @@ __device__ __forceinline__ uint32_t count_part(uint32_t* counter) {
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
     return before;
 }
+// n / d by m = ceil(2^32 / d), exact for n < 2^32 / d (n up to 4096 heads x 64 tokens, d up to 4096)
+__device__ __forceinline__ int over(int n, int d, uint32_t m) { return d == 1 ? n : (int)__umulhi((uint32_t)n, m); }
+// Whether one of the values in a word (two bf16, or four e4m3) is an infinity or NaN.
+template <bool E4M3>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+    if constexpr (E4M3) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= ((w >> (8 * i)) & 0x7fu) == 0x7fu;
+        return any;
+    } else {
+        return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    }
+}
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -197,6 +211,9 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int b) {
 }
 
 // The CTA's run, segment by segment: unit (request b, u = key head * row tiles + row tile), tiles t0 .. t1 - 1.
+// A unit's end takes the time of about a tile (3400 cycles against 3000 for a tile of e4m3, dim 128), so in the
+// numbering that the runs are cut by, each unit has one tile more than there is to read: a run of many short
+// requests gets fewer of them.
 template <int KEYS>
 struct Walk {
     int b, u, t, t0, t1;
@@ -204,21 +221,26 @@ struct Walk {
     uint32_t unit0;    // number of the unit's first tile
     Span s;
     __device__ __forceinline__ bool next(const AttnParams& p, int units) {
-        if (left <= 0) return false;
-        if (t >= s.tiles) {
-            unit0 += s.tiles;
-            t = 0;
-            if (++u == units) {
-                u = 0;
-                ++b;
-                s = span_of<KEYS>(p, b);
+        while (left > 0) {
+            if (t > s.tiles) {
+                unit0 += s.tiles + 1;
+                t = 0;
+                if (++u == units) {
+                    u = 0;
+                    ++b;
+                    s = span_of<KEYS>(p, b);
+                }
+            }
+            const int from = t, n = min(s.tiles + 1 - t, left);
+            left -= n;
+            t += n;
+            if (from < s.tiles) {
+                t0 = from;
+                t1 = min(t, s.tiles);
+                return true;
             }
         }
-        t0 = t;
-        t1 = min(s.tiles, t0 + left);
-        left -= t1 - t0;
-        t = t1;
-        return true;
+        return false;
     }
 };
 
@@ -240,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     uint8_t* pbuf = qbuf + C::QBUF * C::QBYTES;
     float* red = reinterpret_cast<float*>(pbuf + 2 * C::PBYTES);      // [W][ROWS] maxima
     float* lred = red + W * C::ROWS;                                  // [W][ROWS] sums
-    float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: what undoes q's power of two
+    float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: scale of the row's scores
     int* row_token = reinterpret_cast<int*>(qscale + C::QBUF * C::ROWS);   // [QBUF][ROWS] token of a row, -1: none
     int* row_head = row_token + C::QBUF * C::ROWS;                    // [QBUF][ROWS] and its query head
     float* weight = reinterpret_cast<float*>(row_head + C::QBUF * C::ROWS);                       // [JOIN][ROWS] of a join's parts
@@ -256,6 +278,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     const uint32_t joined = stored + 32u;                        // parts of other runs are in the ring
     const uint32_t decided = stored + 24u;                       // whether the other parts of its unit are there
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
+    __shared__ float vscale[2];
     __shared__ int found_b;
     __shared__ uint32_t last_flag, late_join, others_in;
 
@@ -274,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         mbar_init(counted, 1);
         mbar_init(finished, W);
         mbar_init(decided, 1);
-        mbar_init(joined, 1);
+        mbar_init(joined, W);
         fence_mbar_init();
     }
     if (wid == W && lane == 0) {
@@ -295,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         const int b0 = min(me * each, p.batch), b1 = min(b0 + each, p.batch);
         uint32_t mine = 0;
 #pragma unroll 1
-        for (int b = b0; b < b1; ++b) mine += (uint32_t)(span_of<KEYS>(p, b).tiles * units);
+        for (int b = b0; b < b1; ++b) mine += (uint32_t)((span_of<KEYS>(p, b).tiles + 1) * units);
         uint32_t x = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         if (here)
 #pragma unroll 1
             for (;; ++b) {
-                const uint32_t n = (uint32_t)(span_of<KEYS>(p, b).tiles * units);
+                const uint32_t n = (uint32_t)((span_of<KEYS>(p, b).tiles + 1) * units);
                 if (r0 - before < n) break;
                 before += n;
             }
@@ -348,9 +371,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     Walk<KEYS> walk;
     walk.b = run_b;
     walk.s = span_of<KEYS>(p, walk.b);
-    walk.u = (int)(run_at / (uint32_t)walk.s.tiles);
-    walk.t = (int)run_at - walk.u * walk.s.tiles;
-    walk.unit0 = run_unit0 + (uint32_t)(walk.u * walk.s.tiles);
+    walk.u = (int)(run_at / (uint32_t)(walk.s.tiles + 1));
+    walk.t = (int)run_at - walk.u * (walk.s.tiles + 1);
+    walk.unit0 = run_unit0 + (uint32_t)(walk.u * (walk.s.tiles + 1));
+    walk.t0 = 1, walk.t1 = 0;
     walk.left = (int)run_tiles;
     bool ok = true;                       // no bounded wait has given up; after one, no wait is made
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         while (ok && walk.next(p, units)) {
             const Span s = walk.s;
             const int32_t* table = p.table + (int64_t)walk.b * p.table_stride;
-            const int head = walk.u / p.row_tiles;
+            const int head = over(walk.u, p.row_tiles, p.m_row_tiles);
             // 32 entries of the table in the lanes' registers and the next 32 on their way, so that no tile
             // waits for its entries; one that is no page becomes a page beyond the tensor, which reads as zeros
             auto entries = [&](int e) {
@@ -459,13 +483,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         while (walk.next(p, units)) {
             wait(qempty(qs), phase ^ 1u);
             uint8_t* dst = qbuf + qs * C::QBYTES;
-            const int hk = walk.u / p.row_tiles, r0 = (walk.u % p.row_tiles) * C::ROWS;
+            const int hk = over(walk.u, p.row_tiles, p.m_row_tiles), r0 = (walk.u - hk * p.row_tiles) * C::ROWS;
             constexpr int QCH = DP / 8;                             // 16-byte chunks of a row
             const uint16_t* base = p.q + (int64_t)walk.b * p.q_bs;
             // which token and query head each row is, for the consumers too
 #pragma unroll 1
             for (int r = lane; r < C::ROWS; r += 32) {
-                const int at = r0 + r, j = at / p.group;
+                const int at = r0 + r, j = over(at, p.group, p.m_group);
                 const bool in = at < rows;
                 row_token[qs * C::ROWS + r] = in ? j : -1;
                 row_head[qs * C::ROWS + r] = hk * p.group + (at - j * p.group);
@@ -487,6 +511,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 asm volatile("cp.async.wait_all;" ::: "memory");
             } else {
                 constexpr int PER = QCH > 32 ? QCH / 32 : 1, GO = 4;   // rows in flight
+                const float k_scale = p.scale_log2 * (p.k_scale ? p.k_scale[hk] : 1.f);
+                if (lane == 0) vscale[qs] = p.v_scale ? p.v_scale[hk] : 1.f;
 #pragma unroll 1
                 for (int g0 = 0; g0 < C::ROWS; g0 += GO) {
                     uint4 w[GO][PER];
@@ -512,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                         if (big >= 0x7f80u) up = 0;                 // an infinity or NaN stays one
                         up = min(up, 126);
                         const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                        if (lane == 0) qscale[qs * C::ROWS + g0 + r] = __uint_as_float((uint32_t)(127 - up) << 23);
+                        if (lane == 0) qscale[qs * C::ROWS + g0 + r] = __uint_as_float((uint32_t)(127 - up) << 23) * k_scale;
 #pragma unroll
                         for (int c = 0; c < PER; ++c) {
                             const int ch = lane + 32 * c;
@@ -625,17 +651,20 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll 1
         for (int c0 = 0; c0 < x.count; c0 += ROOM) {
             const int n = min(ROOM, x.count - c0), i0 = own && c0 == 0 ? 1 : 0;
-            if (tid == 0 && ok) {
+            if (lane == 0 && ok) {
                 asm volatile("fence.proxy.async;" ::: "memory");   // others' stores, before the copies read them
-                mbar_arrive_expect_tx(joined, (n - i0) * BYTES);
+                uint32_t mine = 0;
 #pragma unroll 1
-                for (int i = i0; i < n; ++i) bulk_g2s(ring_u + i * BYTES, slot_of(x, c0 + i), BYTES, joined);
+                for (int i = i0 + wid; i < n; i += W) mine += BYTES;
+                mbar_arrive_expect_tx(joined, mine);
+#pragma unroll 1
+                for (int i = i0 + wid; i < n; i += W) bulk_g2s(ring_u + i * BYTES, slot_of(x, c0 + i), BYTES, joined);
             }
             wait(joined, join_round++ & 1);
             const float* parts = reinterpret_cast<const float*>(ring);
             const float* stats = parts + C::STATS + 2 * row;
             float high = top;
-#pragma unroll 1
+#pragma unroll 4
             for (int i = i0; i < n; ++i) high = fmaxf(high, stats[i * C::SLOT_FLOATS]);
             const float f = top == high ? 1.f : exp2_approx(top - high);
             sum *= f;
@@ -656,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int mt = 0; mt < MT; ++mt)
                     acc[mt][nt][0] *= k.x, acc[mt][nt][1] *= k.y, acc[mt][nt][2] *= k.x, acc[mt][nt][3] *= k.y;
             }
-#pragma unroll 1
+#pragma unroll (MT * NT <= 4 ? 4 : 1)
             for (int i = i0; i < n; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -716,10 +745,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 }
             }
         consumer_sync();
-        const int hk = u / p.row_tiles, r0 = (u - hk * p.row_tiles) * C::ROWS;
+        const int hk = over(u, p.row_tiles, p.m_row_tiles), r0 = (u - hk * p.row_tiles) * C::ROWS;
 #pragma unroll 1
         for (int i = tid; i < C::ROWS * QCH; i += CONSUMERS) {
-            const int r = i / QCH, ch = i % QCH, j = (r0 + r) / p.group, hq = hk * p.group + r0 + r - j * p.group;
+            const int r = i / QCH, ch = i % QCH, j = over(r0 + r, p.group, p.m_group), hq = hk * p.group + r0 + r - j * p.group;
             if (!ok || j >= p.tokens) continue;
             if (ch * 8 < p.dim)
                 *reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs + ch * 8) =
@@ -750,9 +779,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             b = early_b, u = early_u, v_scale = early_scale, parts = early_parts, part = true;
         } else {
         const Span s = walk.s;
-        const int hk = walk.u / p.row_tiles, r0 = (walk.u % p.row_tiles) * C::ROWS;
-        const float k_scale = p.k_scale ? p.k_scale[hk] : 1.f;
-        v_scale = p.v_scale ? p.v_scale[hk] : 1.f;
         const bool end_of_run = walk.left <= 0;
         b = walk.b, u = walk.u;
         part = walk.t0 > 0 || walk.t1 < s.tiles;
@@ -764,12 +790,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             l[nt][0] = l[nt][1] = 0.f;
         }
         wait(qfull(qs), qphase);
-        const float sc_all = p.scale_log2 * k_scale;
-        float sc[NT][2];
+        v_scale = E4M3 ? vscale[qs] : 1.f;
+        float sc[NT][2];                     // of the scores: softmax scale, log2(e), k's scale, q's power of two
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? sc_all * qscale[qs * C::ROWS + 8 * nt + t2 + e] : sc_all;
+            for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? qscale[qs * C::ROWS + 8 * nt + t2 + e] : p.scale_log2;
         const uint32_t q_u = qbuf_u + qs * C::QBYTES;
 
 #pragma unroll 1
@@ -916,19 +942,32 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             wait(full(slot), phase);
             {
                 const uint32_t vt = ring_u + (uint32_t)slot * C::TILE;
+                // Keys that some tokens see and others do not meet P = 0 in the others' columns, where an
+                // infinity or NaN must not become one of the output: with such values among them the tokens
+                // are added one by one, each with the keys that it sees and in the same order.
+                bool apart = false;
                 if (!whole) {
-                    // Rows outside the visible keys are not the cache's (a box reads whole pages, and skips
-                    // those that nobody sees): zeros, so that P = 0 meets a number there.
                     constexpr int PCH = C::PITCH / 16;
                     uint8_t* v = ring + (size_t)slot * C::TILE;
+                    // Rows outside the visible keys are not the cache's (a box reads whole pages, and skips
+                    // those that nobody sees): zeros, so that P = 0 meets a number there.
                     const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
 #pragma unroll 1
                     for (int i = tid; i < (z0 + KEYS - z1) * PCH; i += CONSUMERS) {
                         const int r = i / PCH, row = r < z0 ? r : z1 + r - z0;
                         *reinterpret_cast<uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH)) = make_uint4(0, 0, 0, 0);
                     }
+                    // and the rows that not every token sees: the last tokens - 1 keys, and the first of a window
+                    const int a1 = p.window > 0 ? min(z1, max(z0, s.len - p.window - key0)) : z0;
+                    const int b0 = max(a1, min(z1, s.len - p.tokens + 1 - key0)), n = a1 - z0 + z1 - b0;
+#pragma unroll 1
+                    for (int i = tid; i < n * PCH; i += CONSUMERS) {
+                        const int r = i / PCH, row = r < a1 - z0 ? z0 + r : b0 + r - (a1 - z0);
+                        const uint4 w = *reinterpret_cast<const uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH));
+                        apart |= not_finite<E4M3>(w.x) || not_finite<E4M3>(w.y) || not_finite<E4M3>(w.z) || not_finite<E4M3>(w.w);
+                    }
                     fence_proxy_async_smem();        // before TMA writes the slot again
-                    consumer_sync();
+                    apart = consumer_any(apart);
                 }
                 // V^T fragments of 16-dim tile mt: keys 32 kp .. 32 kp + 31, two k-steps
                 auto v_frags = [&](int kp, int mt, uint32_t (&f)[2][4]) {
@@ -955,26 +994,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                         for (int nt = 0; nt < NT; ++nt)
                             ldsm4t(p_u + n * C::LOW + (nt * KEYS + 32 * kp + lane) * 16, b[n][nt]);
                 };
-                // Keys that some tokens see and others do not meet P = 0 in the others' columns, where an
-                // infinity or NaN must not become one of the output: with such values among them the tokens
-                // are added one by one, each with the keys that it sees and in the same order.
-                bool apart = false;
-                if (!whole && p.tokens > 1) {
-                    constexpr uint32_t EXP = E4M3 ? 0x7c00u : 0x7f80u;
-#pragma unroll 1
-                    for (int kp = 0; kp < KEYS / 32; ++kp)
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t f[2][4];
-                            v_frags(kp, mt, f);
-#pragma unroll
-                            for (int h = 0; h < 8; ++h) {
-                                const uint32_t x = f[h >> 2][h & 3];
-                                apart |= (x & EXP) == EXP || ((x >> 16) & EXP) == EXP;
-                            }
-                        }
-                    apart = __any_sync(~0u, apart);
-                }
                 if (!apart) {
 #pragma unroll 1
                     for (int kp = 0; kp < KEYS / 32; ++kp) {
