@@ -86,7 +86,7 @@ struct Cfg {
     static constexpr int PBYTES = PN * LOW;            // [PN][NT][keys][8 rows] of 16 bits
     static constexpr int MT = DP / (16 * W);           // 16-dim tiles of a consumer warp
     static constexpr int JOIN = NT <= 2 ? 32 : 64 / NT;         // parts whose weights a join holds at a time
-    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + 3 * QBUF * ROWS * 4 +
+    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
                                     JOIN * ROWS * 4 + 512;
     static constexpr bool LIGHT = MT * NT * 4 + NT * 8 <= 32;   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
@@ -265,18 +265,19 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: scale of the row's scores
     int* row_token = reinterpret_cast<int*>(qscale + C::QBUF * C::ROWS);   // [QBUF][ROWS] token of a row, -1: none
     int* row_head = row_token + C::QBUF * C::ROWS;                    // [QBUF][ROWS] and its query head
-    float* weight = reinterpret_cast<float*>(row_head + C::QBUF * C::ROWS);                       // [JOIN][ROWS] of a join's parts
+    float* stats = reinterpret_cast<float*>(row_head + C::QBUF * C::ROWS);   // [QBUF][ROWS]{m, l} of staged rows
+    float* weight = stats + 2 * C::QBUF * C::ROWS;                       // [JOIN][ROWS] of a join's parts
     uint64_t* bars = reinterpret_cast<uint64_t*>(weight + C::JOIN * C::ROWS);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (MAX_SLOTS + s); };
     auto qfull = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + s); };
-    auto qempty = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + 2 + s); };
-    const uint32_t stored = bar0 + 8u * (2 * MAX_SLOTS + 4);     // the run's first part is in its slot
-    const uint32_t counted = stored + 8u;                        // and has been counted in
-    const uint32_t finished = stored + 16u;                      // the run's last tile has been added
-    const uint32_t joined = stored + 32u;                        // parts of other runs are in the ring
-    const uint32_t decided = stored + 24u;                       // whether the other parts of its unit are there
+    auto stored = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + 2 + s); };   // a segment's rows, or the run's first part, are there
+    const uint32_t counted = bar0 + 8u * (2 * MAX_SLOTS + 4);    // the run's first part has been counted in
+    const uint32_t finished = counted + 8u;                      // the run's last tile has been added
+    const uint32_t decided = counted + 16u;                      // whether the other parts of its unit are there
+    const uint32_t joined = counted + 24u;                       // parts of other runs are in the ring
+    const uint32_t drained = counted + 32u;                      // the q warp has written every row
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
     __shared__ float vscale[2];
     __shared__ int found_b;
@@ -291,13 +292,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         }
         for (int s = 0; s < C::QBUF; ++s) {
             mbar_init(qfull(s), 32);
-            mbar_init(qempty(s), W);
+            mbar_init(stored(s), W);
         }
-        mbar_init(stored, W);
         mbar_init(counted, 1);
         mbar_init(finished, W);
         mbar_init(decided, 1);
         mbar_init(joined, W);
+        mbar_init(drained, 1);
         fence_mbar_init();
     }
     if (wid == W && lane == 0) {
@@ -445,6 +446,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 if (slot >= C::NS) slot -= C::NS, phase ^= 1u;
             }
         }
+        // The next kernel's CTAs may come as this one's end: what this kernel waited for is complete.
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // no copy is in flight when the CTA ends, whatever its consumers did
 #pragma unroll 1
         for (int64_t i = turn - 2; i >= 0 && i >= turn - C::NS; i -= 2)
@@ -463,25 +466,35 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         x.count = (int)(run_of(unit0 + tiles - 1, all_tiles, ctas) - x.first) + 1;
         return x;
     };
-    if (wid == W + 2) {
-        // ================= q of each segment, rows (token, head of the group), in the matrix type; and the
-        // counting in of parts, so that consumers do not wait for it: their own counter of a unit's parts is
-        // the first run's
-        int qs = 0, segment = 0;
-        uint32_t phase = 0;
-        const int rows = p.tokens * p.group;
-        bool early = false;                  // the run's first segment is a part, and not the run's last
-        Parts parts = {};
-        auto count_in = [&] {                // the first segment's part, once its consumers have stored it
-            wait(stored, 0);
-            if (lane == 0) {
-                late_join = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
-                mbar_arrive(counted);
+    // Rows that are staged in q buffer `buf`, with their maxima and sums, to the output: 16 bytes a thread.
+    auto copy_rows = [&](int b, int u, int buf, int first, int step) {
+        constexpr int QCH = DP / 8;
+        const uint8_t* stage = qbuf + buf * C::QBYTES;
+        const float* stat = stats + buf * 2 * C::ROWS;
+        const int hk = over(u, p.row_tiles, p.m_row_tiles), r0 = (u - hk * p.row_tiles) * C::ROWS;
+#pragma unroll 1
+        for (int i = first; i < C::ROWS * QCH; i += step) {
+            const int r = i / QCH, ch = i % QCH, j = over(r0 + r, p.group, p.m_group), hq = hk * p.group + r0 + r - j * p.group;
+            if (!ok || j >= p.tokens) continue;
+            if (ch * 8 < p.dim)
+                *reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs + ch * 8) =
+                    *reinterpret_cast<const uint4*>(stage + qchunk_at<QCH>(r, ch));
+            if (p.lse && ch == 0) {
+                const float top = stat[2 * r], sum = stat[2 * r + 1];
+                p.lse[((int64_t)b * p.tokens + j) * p.heads_q + hq] =
+                    ((top == __int_as_float(0xff800000) ? 0.f : top) + __log2f(sum)) * 0.69314718055994531f;
             }
-            early = false;
-        };
-        while (walk.next(p, units)) {
-            wait(qempty(qs), phase ^ 1u);
+        }
+    };
+    if (wid == W + 2) {
+        // ================= q of each segment, rows (token, head of the group), in the matrix type; and what is
+        // left of a segment's end beside the stream: rows to the output, the run's first part counted in (the
+        // counter of a unit's parts is the first run's)
+        const int rows = p.tokens * p.group;
+        Walk<KEYS> ahead = walk;             // whose q is loaded next; `walk` follows the consumers
+        bool more = true;
+        auto load_q = [&](int qs) {
+            const Walk<KEYS>& walk = ahead;
             uint8_t* dst = qbuf + qs * C::QBYTES;
             const int hk = over(walk.u, p.row_tiles, p.m_row_tiles), r0 = (walk.u - hk * p.row_tiles) * C::ROWS;
             constexpr int QCH = DP / 8;                             // 16-byte chunks of a row
@@ -560,12 +573,27 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 }
             }
             mbar_arrive(qfull(qs));
-            if (++qs == C::QBUF) qs = 0, phase ^= 1u;
-            if (early) count_in();
-            if (segment++ == 0 && walk.t0 > 0 && walk.left > 0) {
-                early = true;
-                parts = parts_of(walk.unit0, walk.s.tiles);
+        };
+#pragma unroll 1
+        for (int i = 0; more; ++i) {
+            // q buffers in turn: the first QBUF segments' at once, then each when its buffer is free again
+            if (i >= C::QBUF) {
+                walk.next(p, units);
+                const bool part = walk.t0 > 0 || walk.t1 < walk.s.tiles;
+                if (part && walk.left <= 0) break;          // the consumers end the run
+                wait(stored(i % C::QBUF), (i / C::QBUF - 1) & 1);
+                if (!part) {
+                    copy_rows(walk.b, walk.u, i % C::QBUF, lane, 32);
+                    __syncwarp();
+                } else if (lane == 0) {
+                    const Parts x = parts_of(walk.unit0, walk.s.tiles);
+                    late_join = count_part(p.counters + x.first) == (uint32_t)x.count - 1;
+                    mbar_arrive(counted);
+                }
+                if (walk.left <= 0) break;
             }
+            if (ahead.next(p, units)) load_q(i % C::QBUF);
+            else if (i == 0) more = false;                  // a run of nothing
         }
         if (walk.t0 == 0 && walk.t1 < walk.s.tiles) {
             // the run ends with its unit's first part: the other parts' runs mostly began with theirs, so
@@ -584,6 +612,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 mbar_arrive(decided);
             }
         }
+        if (lane == 0) mbar_arrive(drained);
         if (!ok && lane == 0) atomicOr(p.status, 1u);
         return;
     }
@@ -720,17 +749,18 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         consumer_sync();                                 // `weight` and `red` serve what follows
     };
 
-    // Rows out: normalised and rounded into the segment's q buffer (which has been read), then 16 bytes a thread.
-    // A row that sees no key (whose sum is zero) is zero.
-    auto write_out = [&](int b, int u, float v_scale, int buf) {
+    // Rows normalised and rounded into the segment's q buffer, which has been read.  A row that sees no key
+    // (whose sum is zero) is zero.
+    auto stage_out = [&](float v_scale, int buf) {
         uint8_t* stage = qbuf + buf * C::QBYTES;
+        float* stat = stats + buf * 2 * C::ROWS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * nt + t2 + e;
                 const float inv = l[nt][e] == 0.f ? 0.f : __fdividef(v_scale, l[nt][e]);
-                if (wid == 0 && g == 0) red[r] = m[nt][e], red[C::ROWS + r] = l[nt][e];
+                if (wid == 0 && g == 0) stat[2 * r] = m[nt][e], stat[2 * r + 1] = l[nt][e];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int d = (wid * MT + mt) * 16 + (E4M3 ? 2 * g : g);
@@ -744,21 +774,6 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     }
                 }
             }
-        consumer_sync();
-        const int hk = over(u, p.row_tiles, p.m_row_tiles), r0 = (u - hk * p.row_tiles) * C::ROWS;
-#pragma unroll 1
-        for (int i = tid; i < C::ROWS * QCH; i += CONSUMERS) {
-            const int r = i / QCH, ch = i % QCH, j = over(r0 + r, p.group, p.m_group), hq = hk * p.group + r0 + r - j * p.group;
-            if (!ok || j >= p.tokens) continue;
-            if (ch * 8 < p.dim)
-                *reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs + ch * 8) =
-                    *reinterpret_cast<const uint4*>(stage + qchunk_at<QCH>(r, ch));
-            if (p.lse && ch == 0) {
-                const float top = red[r], sum = red[C::ROWS + r];
-                p.lse[((int64_t)b * p.tokens + j) * p.heads_q + hq] = ((top == NINF ? 0.f : top) + __log2f(sum)) * 0.69314718055994531f;
-            }
-        }
-        consumer_sync();                                 // `red` serves the next segment
     };
 
     bool early = false;                      // the run's first segment is a part, and not the last
@@ -776,6 +791,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             early = false;
             wait(counted, 0);
             if (!ok || late_join == 0) break;
+            wait(drained, 0);                // its rows go through q buffer 0
             b = early_b, u = early_u, v_scale = early_scale, parts = early_parts, part = true;
         } else {
         const Span s = walk.s;
@@ -899,9 +915,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     }
                 }
             };
-            for (;;) {
-                make_p();
-                if (!consumer_any(need)) break;
+            for (bool fresh = t == walk.t0;; fresh = false) {
+                if (!fresh) {
+                    make_p();
+                    if (!consumer_any(need)) break;
+                }
                 // a new maximum for every row: the four warps' maxima meet in shared memory; then P again
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -1079,11 +1097,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         if (part && !end_of_run) {
             // the run's first part: to its slot, and on with the next segment; the q warp counts it in
             store_part(false);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(stored);
             early = true;
             early_b = b, early_u = u, early_scale = v_scale, early_parts = parts;
-            if (lane == 0) mbar_arrive(qempty(buf));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(stored(buf));
             continue;
         }
         if (part) {
@@ -1101,9 +1118,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         }
         }
         if (part) join(parts, direct);
-        write_out(b, u, v_scale, buf);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qempty(buf));
+        stage_out(v_scale, buf);
+        if (!part) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(stored(buf));             // the q warp writes the rows
+        } else {
+            consumer_sync();
+            copy_rows(b, u, buf, tid, CONSUMERS);
+            consumer_sync();                                // before the buffer is staged again
+        }
     }
     if (!ok && lane == 0) atomicOr(p.status, 1u);
 }
