@@ -59,43 +59,48 @@ namespace affqmm {
 namespace attn {
 
 constexpr int W = 4;                       // consumer warps
-constexpr int CONSUMERS = 32 * W;
-constexpr int THREADS = 32 * (W + 3);
+constexpr int GROUP = 32 * W;             // threads of a group of consumers
 constexpr float LAZY = 8.f;                // log2 of how far a score may exceed the running maximum
 constexpr size_t SM_SMEM = 233472;         // shared memory of an SM, 1 KB of it taken by each CTA
 constexpr size_t CTA_SMEM = 232448;        // and what one CTA may have of it
 constexpr size_t STATIC_SMEM = 1024;       // the kernel's few static variables, and the ring's alignment
 constexpr int MAX_SLOTS = 16;
 
-template <int DP, int NT, bool E4M3>
+template <int DP, int NA, bool E4M3>
 struct Cfg {
     static constexpr int ES = E4M3 ? 1 : 2;
-    static constexpr int ROWS = 8 * NT;
+    static constexpr int ROWS = 8 * NA;
     static constexpr int PITCH = DP * ES;              // bytes of a cache row in shared memory
     static constexpr int PW = PITCH < 128 ? PITCH : 128;   // bytes of a row in one panel
     static constexpr int PANELS = PITCH / PW;
     // Rows of 128 bytes or less: two blocks of 16 keys to a warp, so that two chains of matrix
     // instructions overlap and the barrier comes half as often (e4m3, dim 128).
-    static constexpr int KB = PITCH <= 128 && NT <= 2 ? 2 : 1;
+    static constexpr int KB = PITCH <= 128 && NA <= 2 ? 2 : 1;
     static constexpr int KEYS = 16 * W * KB;
     static constexpr int TILE = KEYS * PITCH;
     static constexpr int QBYTES = ROWS * DP * 2;
-    static constexpr int QBUF = (DP == 512 && NT > 1) ? 1 : 2;
+    static constexpr int QBUF = (DP == 512 && NA > 1) ? 1 : 2;
     static constexpr int PN = E4M3 ? 1 : 2;            // numbers that make one P
-    static constexpr int LOW = NT * KEYS * 16;         // from the first numbers to the second
-    static constexpr int PBYTES = PN * LOW;            // [PN][NT][keys][8 rows] of 16 bits
     static constexpr int MT = DP / (16 * W);           // 16-dim tiles of a consumer warp
-    static constexpr int JOIN = NT <= 2 ? 32 : 64 / NT;         // parts whose weights a join holds at a time
-    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PBYTES + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
+    static constexpr int JOIN = 32;                    // most parts that a join takes at once
+    static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PN * NA * KEYS * 16 + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
                                     JOIN * ROWS * 4 + 512;
-    static constexpr bool LIGHT = MT * NT * 4 + NT * 8 <= 32;   // registers allow two CTAs an SM
+    static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= 32;   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
     static constexpr int CPS = (LIGHT && FIXED + 3 * TILE <= HALF) ? 2 : 1;
+    // With one CTA an SM, the rows go to two groups of consumer warps (where there are two row tiles), which share
+    // the ring and q and nothing else: two warps to a scheduler, whose latencies overlap.
+    static constexpr int NG = CPS == 1 && NA >= 2 ? 2 : 1;
+    static constexpr int NT = NA / NG, GROWS = 8 * NT;           // row tiles, rows of a group
+    static constexpr int CONSUMERS = 32 * W * NG, THREADS = CONSUMERS + 96;
+    static constexpr int LOW = NT * KEYS * 16;         // from P's first numbers to the second
+    static constexpr int PBYTES = PN * LOW;            // of a group: [PN][NT][keys][8 rows] of 16 bits
     static constexpr size_t ROOM = (CPS == 2 ? HALF : CTA_SMEM - STATIC_SMEM) - FIXED;
     static constexpr int NS = ROOM / TILE > MAX_SLOTS ? MAX_SLOTS : (int)(ROOM / TILE);
     static constexpr size_t SMEM = FIXED + (size_t)NS * TILE;
-    static constexpr size_t STATS = (size_t)W * MT * NT * 128;  // of a partial slot: the accumulators, then [row]{m, l}
-    static constexpr size_t SLOT_FLOATS = STATS + 2 * ROWS;
+    static constexpr size_t STATS = (size_t)W * MT * NT * 128;  // of a group's part: the accumulators, then [row]{m, l}
+    static constexpr size_t PART_FLOATS = STATS + 2 * GROWS;
+    static constexpr size_t SLOT_FLOATS = NG * PART_FLOATS;
     static_assert(NS >= 3, "ring too short");
 };
 
@@ -170,14 +175,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool consumer_any(bool v) {
+__device__ __forceinline__ void group_sync(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+__device__ __forceinline__ bool group_any(int group, bool v) {
     uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r) : "r"((uint32_t)v) : "memory");
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r) : "r"((uint32_t)v), "r"(1 + group) : "memory");
     return r != 0;
 }
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(THREADS) : "memory"); }
 // 16-byte chunk `c` of row `row` of a tile: panels of PW bytes of every row,
 // swizzled as TMA swizzles rows of 128 (64) bytes, so that the eight rows that
 // one fragment load reads fall into eight bank groups.
@@ -251,22 +258,22 @@ __device__ __forceinline__ uint32_t run_of(uint32_t x, uint32_t total, uint32_t 
     return (uint32_t)(top / total);
 }
 
-template <int DP, int NT, bool E4M3>
-__global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_kernel(
+template <int DP, int NA, bool E4M3>
+__global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>::CPS) paged_attn_kernel(
     const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = Cfg<DP, NT, E4M3>;
-    constexpr int KEYS = C::KEYS;
+    using C = Cfg<DP, NA, E4M3>;
+    constexpr int KEYS = C::KEYS, THREADS = C::THREADS, PRODUCER = C::NG * W;   // the first warp that is no consumer
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
     uint8_t* qbuf = ring + (size_t)C::NS * C::TILE;
     uint8_t* pbuf = qbuf + C::QBUF * C::QBYTES;
-    float* red = reinterpret_cast<float*>(pbuf + 2 * C::PBYTES);      // [W][ROWS] maxima
-    float* lred = red + W * C::ROWS;                                  // [W][ROWS] sums
+    float* red = reinterpret_cast<float*>(pbuf + 2 * C::NG * C::PBYTES);      // of each group: [W][rows] maxima
+    float* lred = red + W * C::ROWS;                                  // of each group: [W][rows] sums
     float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: scale of the row's scores
     int* row_token = reinterpret_cast<int*>(qscale + C::QBUF * C::ROWS);   // [QBUF][ROWS] token of a row, -1: none
     int* row_head = row_token + C::QBUF * C::ROWS;                    // [QBUF][ROWS] and its query head
     float* stats = reinterpret_cast<float*>(row_head + C::QBUF * C::ROWS);   // [QBUF][ROWS]{m, l} of staged rows
-    float* weight = stats + 2 * C::QBUF * C::ROWS;                       // [JOIN][ROWS] of a join's parts
+    float* weight = stats + 2 * C::QBUF * C::ROWS;                       // of each group: [JOIN][rows] of a join's parts
     uint64_t* bars = reinterpret_cast<uint64_t*>(weight + C::JOIN * C::ROWS);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -276,8 +283,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     const uint32_t counted = bar0 + 8u * (2 * MAX_SLOTS + 4);    // the run's first part has been counted in
     const uint32_t finished = counted + 8u;                      // the run's last tile has been added
     const uint32_t decided = counted + 16u;                      // whether the other parts of its unit are there
-    const uint32_t joined = counted + 24u;                       // parts of other runs are in the ring
-    const uint32_t drained = counted + 32u;                      // the q warp has written every row
+    auto joined = [&](int s) { return counted + 24u + 8u * s; };  // parts of other runs are in the group's share of the ring
+    const uint32_t drained = counted + 40u;                      // the q warp has written every row
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
     __shared__ float vscale[2];
     __shared__ int found_b;
@@ -288,20 +295,20 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll 1
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), W);
+            mbar_init(empty(s), PRODUCER);
         }
         for (int s = 0; s < C::QBUF; ++s) {
             mbar_init(qfull(s), 32);
-            mbar_init(stored(s), W);
+            mbar_init(stored(s), PRODUCER);
         }
         mbar_init(counted, 1);
-        mbar_init(finished, W);
+        mbar_init(finished, PRODUCER);
         mbar_init(decided, 1);
-        mbar_init(joined, W);
+        for (int s = 0; s < C::NG; ++s) mbar_init(joined(s), W);
         mbar_init(drained, 1);
         fence_mbar_init();
     }
-    if (wid == W && lane == 0) {
+    if (wid == PRODUCER && lane == 0) {
         prefetch_tmap(&k_map);
         prefetch_tmap(&v_map);
     }
@@ -382,9 +389,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         if (ok) ok = mbar_wait(bar, parity);
     };
 
-    if (wid == W || wid == W + 1) {
+    if (wid == PRODUCER || wid == PRODUCER + 1) {
         // ================= producers: K tiles take the ring's even turns, V tiles the odd ones
-        const bool is_v = wid == W + 1;
+        const bool is_v = wid == PRODUCER + 1;
         const CUtensorMap* map = is_v ? &v_map : &k_map;
         const int box_shift = min(p.page_shift, KEYS == 128 ? 7 : 6), box = 1 << box_shift;
         const uint32_t page_mask = (1u << p.page_shift) - 1u;
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             }
         }
     };
-    if (wid == W + 2) {
+    if (wid == PRODUCER + 2) {
         // ================= q of each segment, rows (token, head of the group), in the matrix type; and what is
         // left of a segment's end beside the stream: rows to the output, the run's first part counted in (the
         // counter of a unit's parts is the first run's)
@@ -619,10 +626,17 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 
     // ===================== consumers
     const int g = lane >> 2, t2 = (lane & 3) * 2;
-    constexpr int MT = C::MT, QCH = DP / 8, KB = C::KB;
+    constexpr int MT = C::MT, NT = C::NT, QCH = DP / 8, KB = C::KB, GROWS = C::GROWS;
+    const int group = C::NG == 1 ? 0 : wid / W, cw = C::NG == 1 ? wid : wid % W, ct = C::NG == 1 ? tid : tid % GROUP;   // warp and thread of the group
+    const int rb = group * GROWS;            // the group's first row
+    red += group * W * GROWS;
+    lred += group * W * GROWS;
+    weight += group * C::JOIN * GROWS;
+    auto consumer_sync = [&] { group_sync(group); };
+    auto consumer_any = [&](bool v) { return group_any(group, v); };
     int slot = 0, qs = 0;
     uint32_t phase = 0, qphase = 0;
-    const uint32_t ring_u = smem_u32(ring), qbuf_u = smem_u32(qbuf), pbuf_u = smem_u32(pbuf);
+    const uint32_t ring_u = smem_u32(ring), qbuf_u = smem_u32(qbuf), pbuf_u = smem_u32(pbuf) + group * 2 * C::PBYTES;
     uint32_t turn = 0;                       // which half of pbuf
     float acc[MT][NT][4], m[NT][2], l[NT][2];
     const float NINF = __int_as_float(0xff800000);
@@ -639,19 +653,19 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
     };
-    auto slot_of = [&](const Parts& x, int i) { return p.slots + (size_t)(2 * (x.first + i) + (i == 0 ? 1 : 0)) * C::SLOT_FLOATS; };
+    auto slot_of = [&](const Parts& x, int i) { return p.slots + (size_t)(2 * (x.first + i) + (i == 0 ? 1 : 0)) * C::SLOT_FLOATS + group * C::PART_FLOATS; };
     int join_round = 0;                      // of `joined`
 
     // this run's part of a unit, to its slot
     auto store_part = [&](bool first) {
-        float4* part = reinterpret_cast<float4*>(p.slots + (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * C::SLOT_FLOATS);
+        float4* part = reinterpret_cast<float4*>(p.slots + (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * C::SLOT_FLOATS + group * C::PART_FLOATS);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                __stcg(part + ((wid * MT + mt) * NT + nt) * 32 + lane,
+                __stcg(part + ((cw * MT + mt) * NT + nt) * 32 + lane,
                        make_float4(acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]));
-        if (wid == 0 && g == 0)
+        if (cw == 0 && g == 0)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 __stcg(reinterpret_cast<float4*>(reinterpret_cast<float*>(part) + C::STATS + 2 * (8 * nt + t2)),
@@ -662,18 +676,19 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
     // in registers; the same sums come out as if it were read from its slot.  The ring is free by now, so the
     // other parts come by bulk copies, as many at once as it holds: one round trip for them all.
     auto join = [&](const Parts& x, bool own) {
-        constexpr uint32_t BYTES = C::SLOT_FLOATS * sizeof(float);
-        constexpr int ROOM = C::NS * C::TILE / BYTES < C::JOIN ? C::NS * C::TILE / BYTES : C::JOIN;
-        constexpr int TPR = CONSUMERS / C::ROWS;         // threads of a row
-        const int row = tid % C::ROWS, p0 = tid / C::ROWS;
-        if (own && wid == 0 && g == 0)
+        constexpr uint32_t BYTES = C::PART_FLOATS * sizeof(float), SHARE = C::NS * C::TILE / C::NG;
+        constexpr int ROOM = SHARE / BYTES < C::JOIN ? SHARE / BYTES : C::JOIN;
+        static_assert(ROOM >= 1, "a part is larger than its share of the ring");
+        constexpr int TPR = GROUP / GROWS;         // threads of a row
+        const int row = ct % GROWS, p0 = ct / GROWS;
+        if (own && cw == 0 && g == 0)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) red[8 * nt + t2 + e] = m[nt][e], red[C::ROWS + 8 * nt + t2 + e] = l[nt][e];
+                for (int e = 0; e < 2; ++e) red[8 * nt + t2 + e] = m[nt][e], red[GROWS + 8 * nt + t2 + e] = l[nt][e];
         consumer_sync();
         float top = NINF, sum = 0.f;
-        if (own) top = red[row], sum = red[C::ROWS + row];
+        if (own) top = red[row], sum = red[GROWS + row];
         else clear();
         consumer_sync();                                 // `red` has been read
         if (p0 > 0) sum = 0.f;                           // a row's sum is kept by its threads in pieces
@@ -684,26 +699,26 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 asm volatile("fence.proxy.async;" ::: "memory");   // others' stores, before the copies read them
                 uint32_t mine = 0;
 #pragma unroll 1
-                for (int i = i0 + wid; i < n; i += W) mine += BYTES;
-                mbar_arrive_expect_tx(joined, mine);
+                for (int i = i0 + cw; i < n; i += W) mine += BYTES;
+                mbar_arrive_expect_tx(joined(group), mine);
 #pragma unroll 1
-                for (int i = i0 + wid; i < n; i += W) bulk_g2s(ring_u + i * BYTES, slot_of(x, c0 + i), BYTES, joined);
+                for (int i = i0 + cw; i < n; i += W) bulk_g2s(ring_u + group * SHARE + i * BYTES, slot_of(x, c0 + i), BYTES, joined(group));
             }
-            wait(joined, join_round++ & 1);
-            const float* parts = reinterpret_cast<const float*>(ring);
+            wait(joined(group), join_round++ & 1);
+            const float* parts = reinterpret_cast<const float*>(ring + group * SHARE);
             const float* stats = parts + C::STATS + 2 * row;
             float high = top;
 #pragma unroll 4
-            for (int i = i0; i < n; ++i) high = fmaxf(high, stats[i * C::SLOT_FLOATS]);
+            for (int i = i0; i < n; ++i) high = fmaxf(high, stats[i * C::PART_FLOATS]);
             const float f = top == high ? 1.f : exp2_approx(top - high);
             sum *= f;
             top = high;
             if (p0 == 0) red[row] = f;
 #pragma unroll 1
             for (int i = p0 < i0 ? p0 + TPR : p0; i < n; i += TPR) {
-                const float2 st = *reinterpret_cast<const float2*>(stats + i * C::SLOT_FLOATS);
+                const float2 st = *reinterpret_cast<const float2*>(stats + i * C::PART_FLOATS);
                 const float w = st.x == top ? 1.f : exp2_approx(st.x - top);
-                weight[i * C::ROWS + row] = w;
+                weight[i * GROWS + row] = w;
                 sum = fmaf(w, st.y, sum);
             }
             consumer_sync();
@@ -718,11 +733,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             for (int i = i0; i < n; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float2 w = *reinterpret_cast<const float2*>(weight + i * C::ROWS + 8 * nt + t2);
+                    const float2 w = *reinterpret_cast<const float2*>(weight + i * GROWS + 8 * nt + t2);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        const float4 a = *(reinterpret_cast<const float4*>(parts + i * C::SLOT_FLOATS) +
-                                           ((wid * MT + mt) * NT + nt) * 32 + lane);
+                        const float4 a = *(reinterpret_cast<const float4*>(parts + i * C::PART_FLOATS) +
+                                           ((cw * MT + mt) * NT + nt) * 32 + lane);
                         acc[mt][nt][0] = fmaf(w.x, a.x, acc[mt][nt][0]);
                         acc[mt][nt][1] = fmaf(w.y, a.y, acc[mt][nt][1]);
                         acc[mt][nt][2] = fmaf(w.x, a.z, acc[mt][nt][2]);
@@ -731,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 }
             consumer_sync();                             // the ring, `weight` and `red` serve the next parts
         }
-        weight[tid] = sum;
+        weight[ct] = sum;
         if (p0 == 0) red[row] = top;
         consumer_sync();
 #pragma unroll
@@ -742,7 +757,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 m[nt][e] = red[r];
                 float z = 0.f;
 #pragma unroll
-                for (int i = 0; i < TPR; ++i) z += weight[i * C::ROWS + r];
+                for (int i = 0; i < TPR; ++i) z += weight[i * GROWS + r];
                 l[nt][e] = z;
             }
         if (tid == 0) p.counters[x.first] = 0;           // every part has counted in: zero for the next call
@@ -758,12 +773,12 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nt + t2 + e;
+                const int r = rb + 8 * nt + t2 + e;
                 const float inv = l[nt][e] == 0.f ? 0.f : __fdividef(v_scale, l[nt][e]);
-                if (wid == 0 && g == 0) stat[2 * r] = m[nt][e], stat[2 * r + 1] = l[nt][e];
+                if (cw == 0 && g == 0) stat[2 * r] = m[nt][e], stat[2 * r + 1] = l[nt][e];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const int d = (wid * MT + mt) * 16 + (E4M3 ? 2 * g : g);
+                    const int d = (cw * MT + mt) * 16 + (E4M3 ? 2 * g : g);
                     uint8_t* to = stage + qchunk_at<QCH>(r, d >> 3) + (d & 7) * 2;
                     if constexpr (E4M3) {
                         *reinterpret_cast<uint32_t*>(to) = pack2<false>(acc[mt][nt][e] * inv, acc[mt][nt][e + 2] * inv);
@@ -811,7 +826,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? qscale[qs * C::ROWS + 8 * nt + t2 + e] : p.scale_log2;
+            for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? qscale[qs * C::ROWS + rb + 8 * nt + t2 + e] : p.scale_log2;
         const uint32_t q_u = qbuf_u + qs * C::QBYTES;
 
 #pragma unroll 1
@@ -833,7 +848,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     uint32_t a0[KB][4], a1[KB][4];
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
-                        const int krow = 16 * (wid + W * kb) + (lane & 15);
+                        const int krow = 16 * (cw + W * kb) + (lane & 15);
                         if constexpr (E4M3) {
                             uint32_t r[4];
                             ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 2 * s2 + (lane >> 4)), r);
@@ -849,7 +864,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint32_t b[4];
-                        ldsm4(q_u + qchunk_at<QCH>(8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
+                        ldsm4(q_u + qchunk_at<QCH>(rb + 8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a0[kb], b[0], b[1]);
 #pragma unroll
@@ -873,11 +888,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int end = min(s.len - p.tokens + row_token[qs * C::ROWS + 8 * nt + t2 + e] + 1, s.hi);
+                        const int end = min(s.len - p.tokens + row_token[qs * C::ROWS + rb + 8 * nt + t2 + e] + 1, s.hi);
                         const int begin = p.window > 0 ? end - p.window : 0;
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
-                            const int key = key0 + 16 * (wid + W * kb) + g;
+                            const int key = key0 + 16 * (cw + W * kb) + g;
                             if (key >= end || key < begin) sT[kb][nt][e] = NINF;
                             if (key + 8 >= end || key + 8 < begin) sT[kb][nt][e + 2] = NINF;
                         }
@@ -902,7 +917,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) pT[kb][nt][e] = exp2_approx(sT[kb][nt][e] - (e & 1 ? m1 : m0));
-                        const uint32_t at = p_u + (nt * KEYS + 16 * (wid + W * kb) + g) * 16 + t2 * 2;
+                        const uint32_t at = p_u + (nt * KEYS + 16 * (cw + W * kb) + g) * 16 + t2 * 2;
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             const uint32_t hi = pack2<E4M3>(pT[kb][nt][e], pT[kb][nt][e + 1]);
@@ -931,7 +946,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                        if (g == 0) red[wid * C::ROWS + 8 * nt + t2 + e] = x;
+                        if (g == 0) red[cw * GROWS + 8 * nt + t2 + e] = x;
                     }
                 consumer_sync();
 #pragma unroll
@@ -940,7 +955,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     for (int e = 0; e < 2; ++e) {
                         float x = m[nt][e];
 #pragma unroll
-                        for (int w = 0; w < W; ++w) x = fmaxf(x, red[w * C::ROWS + 8 * nt + t2 + e]);
+                        for (int w = 0; w < W; ++w) x = fmaxf(x, red[w * GROWS + 8 * nt + t2 + e]);
                         const float f = m[nt][e] == x ? 1.f : exp2_approx(m[nt][e] - x);
                         m[nt][e] = x;
                         l[nt][e] *= f;
@@ -971,7 +986,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     // those that nobody sees): zeros, so that P = 0 meets a number there.
                     const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
 #pragma unroll 1
-                    for (int i = tid; i < (z0 + KEYS - z1) * PCH; i += CONSUMERS) {
+                    for (int i = ct; i < (z0 + KEYS - z1) * PCH; i += GROUP) {
                         const int r = i / PCH, row = r < z0 ? r : z1 + r - z0;
                         *reinterpret_cast<uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH)) = make_uint4(0, 0, 0, 0);
                     }
@@ -979,7 +994,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                     const int a1 = p.window > 0 ? min(z1, max(z0, s.len - p.window - key0)) : z0;
                     const int b0 = max(a1, min(z1, s.len - p.tokens + 1 - key0)), n = a1 - z0 + z1 - b0;
 #pragma unroll 1
-                    for (int i = tid; i < n * PCH; i += CONSUMERS) {
+                    for (int i = ct; i < n * PCH; i += GROUP) {
                         const int r = i / PCH, row = r < a1 - z0 ? z0 + r : b0 + r - (a1 - z0);
                         const uint4 w = *reinterpret_cast<const uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH));
                         apart |= not_finite<E4M3>(w.x) || not_finite<E4M3>(w.y) || not_finite<E4M3>(w.z) || not_finite<E4M3>(w.w);
@@ -991,7 +1006,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 auto v_frags = [&](int kp, int mt, uint32_t (&f)[2][4]) {
                     if constexpr (E4M3) {
                         uint32_t r[4];
-                        ldsm4t(vt + chunk_at<C::PW, KEYS>(32 * kp + lane, wid * MT + mt), r);
+                        ldsm4t(vt + chunk_at<C::PW, KEYS>(32 * kp + lane, cw * MT + mt), r);
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const uint32_t x = __byte_perm(r[h], 0, 0x3120);   // (key, key + 1) of dim 2g, then of 2g + 1
@@ -1000,7 +1015,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                         }
                     } else {
                         const int key = 32 * kp + (lane & 7) + ((lane >> 4) << 3);
-                        const int c = 2 * (wid * MT + mt) + ((lane >> 3) & 1);
+                        const int c = 2 * (cw * MT + mt) + ((lane >> 3) & 1);
                         ldsm4t(vt + chunk_at<C::PW, KEYS>(key, c), f[0]);
                         ldsm4t(vt + chunk_at<C::PW, KEYS>(key + 16, c), f[1]);
                     }
@@ -1058,7 +1073,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                                     }
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
-                                        if (row_token[qs * C::ROWS + 8 * nt + t2 + (e & 1)] == j) acc[mt][nt][e] = d[e];
+                                        if (row_token[qs * C::ROWS + rb + 8 * nt + t2 + (e & 1)] == j) acc[mt][nt][e] = d[e];
                                 }
                             }
                         }
@@ -1082,7 +1097,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
                 x += __shfl_xor_sync(~0u, x, 4);
                 x += __shfl_xor_sync(~0u, x, 8);
                 x += __shfl_xor_sync(~0u, x, 16);
-                if (g == 0) lred[wid * C::ROWS + 8 * nt + t2 + e] = x;
+                if (g == 0) lred[cw * GROWS + 8 * nt + t2 + e] = x;
             }
         consumer_sync();
 #pragma unroll
@@ -1091,7 +1106,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             for (int e = 0; e < 2; ++e) {
                 float x = 0.f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) x += lred[w * C::ROWS + 8 * nt + t2 + e];
+                for (int w = 0; w < W; ++w) x += lred[w * GROWS + 8 * nt + t2 + e];
                 l[nt][e] = x;
             }
         if (part && !end_of_run) {
@@ -1110,9 +1125,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             }
             if (!direct) {
                 store_part(walk.t0 == 0);
-                consumer_sync();
+                consumers_sync<C::CONSUMERS>();
                 if (tid == 0) last_flag = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
-                consumer_sync();
+                consumers_sync<C::CONSUMERS>();
                 if (last_flag == 0) continue;
             }
         }
@@ -1123,9 +1138,9 @@ __global__ void __launch_bounds__(THREADS, Cfg<DP, NT, E4M3>::CPS) paged_attn_ke
             __syncwarp();
             if (lane == 0) mbar_arrive(stored(buf));             // the q warp writes the rows
         } else {
-            consumer_sync();
-            copy_rows(b, u, buf, tid, CONSUMERS);
-            consumer_sync();                                // before the buffer is staged again
+            consumers_sync<C::CONSUMERS>();
+            copy_rows(b, u, buf, tid, C::CONSUMERS);
+            consumers_sync<C::CONSUMERS>();                                // before the buffer is staged again
         }
     }
     if (!ok && lane == 0) atomicOr(p.status, 1u);
@@ -1148,7 +1163,7 @@ AttnShape shape() {
 }
 template <int DP, int NT, bool E4M3>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
-    return launch_pdl(paged_attn_kernel<DP, NT, E4M3>, dim3((unsigned)grid), THREADS, Cfg<DP, NT, E4M3>::SMEM, st, p,
+    return launch_pdl(paged_attn_kernel<DP, NT, E4M3>, dim3((unsigned)grid), Cfg<DP, NT, E4M3>::THREADS, Cfg<DP, NT, E4M3>::SMEM, st, p,
                       k, v);
 }
 
