@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
     auto joined = [&](int s) { return counted + 24u + 8u * s; };  // parts of other runs are in the group's share of the ring
     const uint32_t drained = counted + 40u;                      // the q warp has written every row
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
-    __shared__ float vscale[2];
+    __shared__ float kscale[2], vscale[2];
     __shared__ int found_b;
     __shared__ uint32_t last_flag, late_join, others_in;
 
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
         }
     };
     if (wid == PRODUCER + 2) {
-        // ================= q of each segment, rows (token, head of the group), in the matrix type; and what is
+        // ================= q of each segment, rows (token, head of the group), and what is
         // left of a segment's end beside the stream: rows to the output, the run's first part counted in (the
         // counter of a unit's parts is the first run's)
         const int rows = p.tokens * p.group;
@@ -520,65 +520,19 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
                 return (j >= 0 && ch * 8 < p.dim) ? base + (int64_t)j * p.q_ts + (int64_t)row_head[qs * C::ROWS + r] * p.q_hs + ch * 8
                                                   : nullptr;
             };
-            if constexpr (!E4M3) {
-                const uint32_t to = smem_u32(dst);
+            const uint32_t to = smem_u32(dst);
 #pragma unroll 1
-                for (int i = lane; i < C::ROWS * QCH; i += 32) {    // in flight together
-                    const uint16_t* src = source(i / QCH, i % QCH);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + qchunk_at<QCH>(i / QCH, i % QCH)),
-                                 "l"(src ? src : p.q), "r"(src ? 16u : 0u) : "memory");
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-            } else {
-                constexpr int PER = QCH > 32 ? QCH / 32 : 1, GO = 4;   // rows in flight
-                const float k_scale = p.scale_log2 * (p.k_scale ? p.k_scale[hk] : 1.f);
-                if (lane == 0) vscale[qs] = p.v_scale ? p.v_scale[hk] : 1.f;
-#pragma unroll 1
-                for (int g0 = 0; g0 < C::ROWS; g0 += GO) {
-                    uint4 w[GO][PER];
-#pragma unroll
-                    for (int r = 0; r < GO; ++r)
-#pragma unroll
-                        for (int c = 0; c < PER; ++c) {
-                            const uint16_t* src = lane + 32 * c < QCH ? source(g0 + r, lane + 32 * c) : nullptr;
-                            w[r][c] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                    for (int r = 0; r < GO; ++r) {
-                        // a power of two that brings the row's largest magnitude into [2^13, 2^14)
-                        uint32_t big = 0;
-#pragma unroll
-                        for (int c = 0; c < PER; ++c) {
-                            const uint32_t v[4] = {w[r][c].x, w[r][c].y, w[r][c].z, w[r][c].w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) big = max(big, max(v[e] & 0x7fffu, (v[e] >> 16) & 0x7fffu));
-                        }
-                        big = __reduce_max_sync(~0u, big);
-                        int up = 13 - ((int)(big >> 7) - 127);
-                        if (big >= 0x7f80u) up = 0;                 // an infinity or NaN stays one
-                        up = min(up, 126);
-                        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                        if (lane == 0) qscale[qs * C::ROWS + g0 + r] = __uint_as_float((uint32_t)(127 - up) << 23) * k_scale;
-#pragma unroll
-                        for (int c = 0; c < PER; ++c) {
-                            const int ch = lane + 32 * c;
-                            const uint32_t v[4] = {w[r][c].x, w[r][c].y, w[r][c].z, w[r][c].w};
-                            if (ch < QCH) {
-                                // within 16 dims, the order in which an 8-bit K fragment holds them: a thread's
-                                // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
-                                const int step = ch >> 1, h = ch & 1;   // dims 16 step + 8 h ..
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int pair = 4 * h + e;         // dims 2 pair, 2 pair + 1 of the 16
-                                    const int k = (pair >> 1) * 2 + (pair & 1) * 8;
-                                    *reinterpret_cast<uint32_t*>(dst + qchunk_at<QCH>(g0 + r, 2 * step + (k >> 3)) + (k & 7) * 2) =
-                                        pack2<true>(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
-                                }
-                            }
-                        }
-                    }
-                }
+            for (int i = lane; i < C::ROWS * QCH; i += 32) {        // in flight together
+                const uint16_t* src = source(i / QCH, i % QCH);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + qchunk_at<QCH>(i / QCH, i % QCH)),
+                             "l"(src ? src : p.q), "r"(src ? 16u : 0u) : "memory");
             }
+            if constexpr (E4M3)
+                if (lane == 0) {
+                    kscale[qs] = p.k_scale ? p.k_scale[hk] : 1.f;
+                    vscale[qs] = p.v_scale ? p.v_scale[hk] : 1.f;
+                }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             mbar_arrive(qfull(qs));
         };
 #pragma unroll 1
@@ -821,6 +775,37 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
             l[nt][0] = l[nt][1] = 0.f;
         }
         wait(qfull(qs), qphase);
+        if constexpr (E4M3) {
+            // q to f16, a warp to a row: times a power of two that brings the row's largest magnitude into
+            // [2^13, 2^14), and within 16 dims in the order in which an 8-bit K fragment holds them: a thread's
+            // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
+            constexpr int PAIRS = DP / 64;   // of dims, of a lane
+            uint8_t* rows = qbuf + qs * C::QBYTES;
+            const float k_scale = p.scale_log2 * kscale[qs];
+#pragma unroll 1
+            for (int r = rb + cw; r < rb + GROWS; r += W) {
+                uint32_t w[PAIRS], big = 0;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    const int pair = lane * PAIRS + i;
+                    w[i] = *reinterpret_cast<const uint32_t*>(rows + qchunk_at<QCH>(r, pair >> 2) + (pair & 3) * 4);
+                    big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                }
+                big = __reduce_max_sync(~0u, big);       // and every lane has read
+                int up = 13 - ((int)(big >> 7) - 127);
+                if (big >= 0x7f80u) up = 0;              // an infinity or NaN stays one
+                up = min(up, 126);
+                const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+                if (lane == 0) qscale[qs * C::ROWS + r] = __uint_as_float((uint32_t)(127 - up) << 23) * k_scale;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    const int pair = lane * PAIRS + i, in16 = pair & 7, k = (in16 >> 1) * 2 + (in16 & 1) * 8;
+                    *reinterpret_cast<uint32_t*>(rows + qchunk_at<QCH>(r, 2 * (pair >> 3) + (k >> 3)) + (k & 7) * 2) =
+                        pack2<true>(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+                }
+            }
+            consumer_sync();
+        }
         v_scale = E4M3 ? vscale[qs] : 1.f;
         float sc[NT][2];                     // of the scores: softmax scale, log2(e), k's scale, q's power of two
 #pragma unroll
