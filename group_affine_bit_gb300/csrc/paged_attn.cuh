@@ -75,7 +75,7 @@ struct Cfg {
     static constexpr int PANELS = PITCH / PW;
     // Rows of 128 bytes or less: two blocks of 16 keys to a warp, so that two chains of matrix
     // instructions overlap and the barrier comes half as often (e4m3, dim 128).
-    static constexpr int KB = PITCH <= 128 && NA <= 2 ? 2 : 1;
+    static constexpr int KB = PITCH <= 128 || (PITCH == 256 && NA >= 4) ? 2 : 1;
     static constexpr int KEYS = 16 * W * KB;
     static constexpr int TILE = KEYS * PITCH;
     static constexpr int QBYTES = ROWS * DP * 2;
@@ -893,24 +893,25 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
 
             // ---- P^T = 2^(s - m), to [nt][key][row]
             const uint32_t p_u = pbuf_u + turn * C::PBYTES;
-            float pT[KB][NT][4];
+            float sum[NT][2];                // of this lane's P, before it is rounded
             auto make_p = [&] {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float m0 = m[nt][0] == NINF ? 0.f : m[nt][0], m1 = m[nt][1] == NINF ? 0.f : m[nt][1];
+                    sum[nt][0] = sum[nt][1] = 0.f;
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) pT[kb][nt][e] = exp2_approx(sT[kb][nt][e] - (e & 1 ? m1 : m0));
                         const uint32_t at = p_u + (nt * KEYS + 16 * (cw + W * kb) + g) * 16 + t2 * 2;
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
-                            const uint32_t hi = pack2<E4M3>(pT[kb][nt][e], pT[kb][nt][e + 1]);
+                            const float x = exp2_approx(sT[kb][nt][e] - m0), y = exp2_approx(sT[kb][nt][e + 1] - m1);
+                            sum[nt][0] += x;
+                            sum[nt][1] += y;
+                            const uint32_t hi = pack2<E4M3>(x, y);
                             st_shared(at + e * 64, hi);
                             if constexpr (!E4M3)
                                 st_shared(at + e * 64 + C::LOW,
-                                          pack2<false>(pT[kb][nt][e] - __uint_as_float(hi << 16),
-                                                       pT[kb][nt][e + 1] - __uint_as_float(hi & 0xffff0000u)));
+                                          pack2<false>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
                         }
                     }
                 }
@@ -950,11 +951,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
                 need = false;
             }
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) l[nt][e & 1] += pT[kb][nt][e];
+            for (int nt = 0; nt < NT; ++nt) l[nt][0] += sum[nt][0], l[nt][1] += sum[nt][1];
 
             // ---- O^T += V^T P^T: this warp's dims, all keys of the tile
             wait(full(slot), phase);
