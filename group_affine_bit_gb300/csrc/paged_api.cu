@@ -132,13 +132,13 @@ int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, C
     return AFFQMM_OK;
 }
 
-AttnShape attn_shape(const affqmm_kv_cache* c, int rows) {
+AttnShape attn_shape(const affqmm_kv_cache* c, int rows, bool lasting) {
     const bool e4m3 = c->type == AFFQMM_KV_E4M3;
     switch (which_dim(c)) {
-        case 0: return attn_shape_64(e4m3, rows);
-        case 1: return attn_shape_128(e4m3, rows);
-        case 2: return attn_shape_256(e4m3, rows);
-        default: return attn_shape_512(e4m3, rows);
+        case 0: return attn_shape_64(e4m3, lasting, rows);
+        case 1: return attn_shape_128(e4m3, lasting, rows);
+        case 2: return attn_shape_256(e4m3, lasting, rows);
+        default: return attn_shape_512(e4m3, lasting, rows);
     }
 }
 
@@ -150,8 +150,21 @@ int check_heads(const affqmm_kv_cache* c, int tokens, int heads_q) {
     return AFFQMM_OK;
 }
 
-size_t attn_workspace(const AttnShape& s, int sms) {
-    return kSlotsOffset + (size_t)2 * s.ctas_per_sm * sms * s.slot_floats * sizeof(float);
+// Two partial slots for each CTA that the SMs hold, of whichever kernel a call may take.
+size_t attn_workspace(const affqmm_kv_cache* c, int rows, int sms) {
+    size_t most = 0;
+    for (const bool lasting : {false, true}) {
+        const AttnShape s = attn_shape(c, rows, lasting);
+        const size_t floats = (size_t)2 * s.ctas_per_sm * sms * s.slot_floats;
+        if (floats > most) most = floats;
+    }
+    return kSlotsOffset + most * sizeof(float);
+}
+
+// Whether the tables have room for eight tiles of 128 keys to a CTA (two CTAs an SM): only then does a coarser cut
+// cost nothing.
+bool lasting_tiles(const affqmm_kv_cache* c, int64_t batch, int64_t keys, int sms) {
+    return batch * c->heads * ((keys + 127) / 128) >= (int64_t)8 * 2 * sms;
 }
 
 }  // namespace
@@ -265,7 +278,7 @@ int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cache, int tok
     if ((rc = check_heads(cache, tokens, heads_q))) return rc;
     int sms = 0;
     if ((rc = device_sms(&sms))) return rc;
-    *bytes = attn_workspace(attn_shape(cache, tokens * (heads_q / cache->heads)), sms);
+    *bytes = attn_workspace(cache, tokens * (heads_q / cache->heads), sms);
     return AFFQMM_OK;
 }
 
@@ -288,8 +301,11 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     int sms = 0;
     if ((rc = device_sms(&sms))) return rc;
     const int group = heads_q / cache->heads, rows = tokens * group;
-    const AttnShape shape = attn_shape(cache, rows);
-    if (!workspace || ws_bytes < attn_workspace(shape, sms)) return AFFQMM_E_WORKSPACE;
+    int64_t keys = wide * cache->page;       // that a request can have, and a window sees
+    if (window > 0 && keys > (int64_t)window + tokens) keys = (int64_t)window + tokens;
+    const bool lasting = lasting_tiles(cache, batch, keys, sms);
+    const AttnShape shape = attn_shape(cache, rows, lasting);
+    if (!workspace || ws_bytes < attn_workspace(cache, rows, sms)) return AFFQMM_E_WORKSPACE;
     if (!aligned(workspace, 256)) return AFFQMM_E_ALIGN;
     const int which = which_dim(cache);
     if ((rc = allow_attn(which))) return rc;
@@ -327,21 +343,18 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     p.counters = reinterpret_cast<uint32_t*>(base + kStatusBytes);
     p.slots = reinterpret_cast<float*>(base + kSlotsOffset);
     // one CTA for each that the SMs hold, or for each tile that the tables have room for
-    const int64_t row_keys = wide * cache->page;
-    int64_t keys = row_keys;
-    // a window's keys, from a multiple of a tile on
-    if (window > 0 && keys > (int64_t)window + tokens + shape.keys) keys = (int64_t)window + tokens + shape.keys;
-    const int64_t tiles = batch * cache->heads * p.row_tiles * ((keys < shape.keys ? 1 : (keys + shape.keys - 1) / shape.keys) + 1);
+    keys += shape.keys;                      // counted from a multiple of a tile on
+    const int64_t tiles = batch * cache->heads * p.row_tiles * ((keys + shape.keys - 1) / shape.keys + 1);
     if (tiles >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
     const int64_t most = (int64_t)sms * shape.ctas_per_sm;
     const int grid = (int)(tiles < most ? tiles : most);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (which) {
-        case 0: e = launch_attn_64(e4m3, rows, p, k_map, v_map, grid, st); break;
-        case 1: e = launch_attn_128(e4m3, rows, p, k_map, v_map, grid, st); break;
-        case 2: e = launch_attn_256(e4m3, rows, p, k_map, v_map, grid, st); break;
-        default: e = launch_attn_512(e4m3, rows, p, k_map, v_map, grid, st); break;
+        case 0: e = launch_attn_64(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
+        case 1: e = launch_attn_128(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
+        case 2: e = launch_attn_256(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
+        default: e = launch_attn_512(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
     }
     return e == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
 }

@@ -50,6 +50,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "affqmm_async.cuh"
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
@@ -66,16 +68,20 @@ constexpr size_t CTA_SMEM = 232448;        // and what one CTA may have of it
 constexpr size_t STATIC_SMEM = 1024;       // the kernel's few static variables, and the ring's alignment
 constexpr int MAX_SLOTS = 16;
 
-template <int DP, int NA, bool E4M3>
+// Blocks of 16 keys to a consumer warp: with two, two chains of matrix instructions overlap and the barrier comes
+// half as often, but a tile has 128 keys and the cut is coarser.  Two for rows of 128 bytes or less, and for rows of
+// 256 bytes with four row tiles or more (204.8 -> 170.2 us for 64 rows of dim 128), or where the tables have room for
+// `lasting` tiles (dim 128: 678 -> 657 us for 64 requests of up to 32768 keys; 7.6 -> 8.2 for one of 577).
+constexpr int key_blocks(int pitch, int na, bool lasting) { return pitch <= 128 || (pitch == 256 && (na >= 4 || lasting)) ? 2 : 1; }
+
+template <int DP, int NA, bool E4M3, int KBLOCKS>
 struct Cfg {
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int ROWS = 8 * NA;
     static constexpr int PITCH = DP * ES;              // bytes of a cache row in shared memory
     static constexpr int PW = PITCH < 128 ? PITCH : 128;   // bytes of a row in one panel
     static constexpr int PANELS = PITCH / PW;
-    // Rows of 128 bytes or less: two blocks of 16 keys to a warp, so that two chains of matrix
-    // instructions overlap and the barrier comes half as often (e4m3, dim 128).
-    static constexpr int KB = PITCH <= 128 || (PITCH == 256 && NA >= 4) ? 2 : 1;
+    static constexpr int KB = KBLOCKS;
     static constexpr int KEYS = 16 * W * KB;
     static constexpr int TILE = KEYS * PITCH;
     static constexpr int QBYTES = ROWS * DP * 2;
@@ -258,10 +264,10 @@ __device__ __forceinline__ uint32_t run_of(uint32_t x, uint32_t total, uint32_t 
     return (uint32_t)(top / total);
 }
 
-template <int DP, int NA, bool E4M3>
-__global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>::CPS) paged_attn_kernel(
+template <int DP, int NA, bool E4M3, int KBLOCKS>
+__global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, NA, E4M3, KBLOCKS>::CPS) paged_attn_kernel(
     const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = Cfg<DP, NA, E4M3>;
+    using C = Cfg<DP, NA, E4M3, KBLOCKS>;
     constexpr int KEYS = C::KEYS, THREADS = C::THREADS, PRODUCER = C::NG * W;   // the first warp that is no consumer
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
@@ -1128,64 +1134,71 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3>::THREADS, Cfg<DP, NA, E4M3>:
     if (!ok && lane == 0) atomicOr(p.status, 1u);
 }
 
-template <int DP, int NT, bool E4M3>
-cudaError_t allow() {
-    return cudaFuncSetAttribute(paged_attn_kernel<DP, NT, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Cfg<DP, NT, E4M3>::SMEM);
-}
-template <int DP, int NT, bool E4M3>
-AttnShape shape() {
-    using C = Cfg<DP, NT, E4M3>;
-    AttnShape s;
-    s.ctas_per_sm = C::CPS;
-    s.rows = C::ROWS;
-    s.keys = C::KEYS;
-    s.slot_floats = C::SLOT_FLOATS;
-    return s;
-}
-template <int DP, int NT, bool E4M3>
-cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
-    return launch_pdl(paged_attn_kernel<DP, NT, E4M3>, dim3((unsigned)grid), Cfg<DP, NT, E4M3>::THREADS, Cfg<DP, NT, E4M3>::SMEM, st, p,
-                      k, v);
-}
+template <int DP, int NA, bool E4M3, bool LASTING>
+struct Launch {
+    static constexpr int KB = key_blocks(DP * (E4M3 ? 1 : 2), NA, LASTING);
+    using C = Cfg<DP, NA, E4M3, KB>;
+    static AttnShape shape() {
+        AttnShape s;
+        s.ctas_per_sm = C::CPS;
+        s.rows = C::ROWS;
+        s.keys = C::KEYS;
+        s.slot_floats = C::SLOT_FLOATS;
+        return s;
+    }
+    static cudaError_t allow() {
+        return cudaFuncSetAttribute(paged_attn_kernel<DP, NA, E4M3, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    }
+    static cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
+        return launch_pdl(paged_attn_kernel<DP, NA, E4M3, KB>, dim3((unsigned)grid), C::THREADS, C::SMEM, st, p, k, v);
+    }
+};
 
-// Row tiles hold 8 NT rows, the fewest that take all rows at once, up to 64
+// Row tiles hold 8 NA rows, the fewest that take all rows at once, up to 64
 // (32 at dim 256, whose accumulators fill the registers, and 16 at dim 512,
 // whose tiles fill shared memory); more rows go to several tiles, each of
 // which reads the keys again, the later ones mostly from L2.
-constexpr int most_nt(int dp) { return dp <= 128 ? 8 : dp == 256 ? 4 : 2; }
-#define AFFQMM_ATTN_SWITCH(DP, rows, CALL)                                          \
-    if ((rows) <= 8) { CALL(DP, 1); }                                               \
-    if ((rows) <= 16 || attn::most_nt(DP) == 2) { CALL(DP, 2); }                    \
-    if constexpr (attn::most_nt(DP) >= 4)                                           \
-        if ((rows) <= 32 || attn::most_nt(DP) == 4) { CALL(DP, 4); }                \
-    if constexpr (attn::most_nt(DP) >= 8) { CALL(DP, 8); }
-#define AFFQMM_ATTN_SHAPE(DP, NT) return e4m3 ? attn::shape<(DP), NT, true>() : attn::shape<(DP), NT, false>()
-#define AFFQMM_ATTN_LAUNCH(DP, NT) \
-    return e4m3 ? attn::launch<DP, NT, true>(p, k, v, grid, st) : attn::launch<DP, NT, false>(p, k, v, grid, st)
-#define AFFQMM_ATTN_ALLOW(DP, NT)                                           \
-    if (cudaError_t e = attn::allow<DP, NT, true>(); e != cudaSuccess) return e; \
-    if (cudaError_t e = attn::allow<DP, NT, false>(); e != cudaSuccess) return e
+template <int DP, typename Then>
+auto with_rows(bool e4m3, bool lasting, int rows, Then then) {
+    constexpr int MOST = DP <= 128 ? 8 : DP == 256 ? 4 : 2;
+    auto typed = [&](auto na) {
+        constexpr int NA = decltype(na)::value;
+        if (e4m3) return lasting ? then(Launch<DP, NA, true, true>{}) : then(Launch<DP, NA, true, false>{});
+        return lasting ? then(Launch<DP, NA, false, true>{}) : then(Launch<DP, NA, false, false>{});
+    };
+    if (rows <= 8) return typed(std::integral_constant<int, 1>{});
+    if (rows <= 16 || MOST == 2) return typed(std::integral_constant<int, 2>{});
+    if (rows <= 32 || MOST == 4) return typed(std::integral_constant<int, MOST < 4 ? 2 : 4>{});
+    return typed(std::integral_constant<int, MOST < 8 ? 2 : 8>{});
+}
+
+template <int DP>
+AttnShape shape(bool e4m3, bool lasting, int rows) {
+    return with_rows<DP>(e4m3, lasting, rows, [](auto l) { return l.shape(); });
+}
+template <int DP>
+cudaError_t allow_all() {
+    for (int i = 0; i < 16; ++i) {
+        const cudaError_t e = with_rows<DP>(i & 1, i & 2, 8 << (i >> 2), [](auto l) { return l.allow(); });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+template <int DP>
+cudaError_t launch(bool e4m3, bool lasting, int rows, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid,
+                   cudaStream_t st) {
+    return with_rows<DP>(e4m3, lasting, rows, [&](auto l) { return l.launch(p, k, v, grid, st); });
+}
 
 }  // namespace attn
 }  // namespace affqmm
 
-#define AFFQMM_ATTN_DEFINE(DP)                                                                            \
-    namespace affqmm {                                                                                    \
-    AttnShape attn_shape_##DP(bool e4m3, int rows) {                                                      \
-        AFFQMM_ATTN_SWITCH(DP, rows, AFFQMM_ATTN_SHAPE)                                                   \
-        return {};                                                                                        \
-    }                                                                                                     \
-    cudaError_t attn_allow_smem_##DP() {                                                                  \
-        AFFQMM_ATTN_ALLOW(DP, 1);                                                                         \
-        AFFQMM_ATTN_ALLOW(DP, 2);                                                                         \
-        if constexpr (attn::most_nt(DP) >= 4) { AFFQMM_ATTN_ALLOW((DP <= 256 ? DP : 64), 4); }            \
-        if constexpr (attn::most_nt(DP) >= 8) { AFFQMM_ATTN_ALLOW((DP <= 128 ? DP : 64), 8); }            \
-        return cudaSuccess;                                                                               \
-    }                                                                                                     \
-    cudaError_t launch_attn_##DP(bool e4m3, int rows, const AttnParams& p, const CUtensorMap& k,          \
-                                 const CUtensorMap& v, int grid, cudaStream_t st) {                       \
-        AFFQMM_ATTN_SWITCH(DP, rows, AFFQMM_ATTN_LAUNCH)                                                  \
-        return cudaErrorInvalidValue;                                                                     \
-    }                                                                                                     \
+#define AFFQMM_ATTN_DEFINE(DP)                                                                                              \
+    namespace affqmm {                                                                                                      \
+    AttnShape attn_shape_##DP(bool e4m3, bool lasting, int rows) { return attn::shape<DP>(e4m3, lasting, rows); }           \
+    cudaError_t attn_allow_smem_##DP() { return attn::allow_all<DP>(); }                                                    \
+    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, int rows, const AttnParams& p, const CUtensorMap& k,              \
+                                 const CUtensorMap& v, int grid, cudaStream_t st) {                                         \
+        return attn::launch<DP>(e4m3, lasting, rows, p, k, v, grid, st);                                                    \
+    }                                                                                                                       \
     }

@@ -285,3 +285,20 @@ def test_the_workspace_serves_projections_and_attention():
         assert torch.equal(api.run(w, x.cuda()).cpu(), y0) and torch.equal(attend(s)[0], a0)
     ws = api.default_workspace(torch.device("cuda", 0))
     assert bool((ws.buf[: api.WORKSPACE_ZEROED] == 0).all())
+
+
+@pytest.mark.parametrize("hq,hk,tokens,dim,kv", [(8, 2, 1, 128, "bf16"), (6, 2, 3, 128, "bf16"), (4, 2, 1, 80, "bf16"), (8, 2, 1, 256, "e4m3"),
+                                                 (8, 2, 4, 192, "e4m3")])
+def test_tables_with_room_for_much_more(hq, hk, tokens, dim, kv):
+    """The same requests in rows of a table that could hold half a million tokens: a coarser cut of the work."""
+    for page, window in ((16, 0), (4, 40)):
+        s = scene(EDGES, hq, hk, dim, page, kv, tokens=tokens, seed=dim)
+        wide = torch.full((len(EDGES), (1 << 19) // page), -1, dtype=torch.int32)
+        wide[:, : s["table"].shape[1]] = s["table"]
+        s["table"] = wide
+        check(s, window=window)
+    long = scene([5003, 17, 9000], hq, hk, dim, 32, kv, tokens=tokens, seed=1)
+    wide = torch.full((3, 40000), -1, dtype=torch.int32)
+    wide[:, : long["table"].shape[1]] = long["table"]
+    long["table"] = wide
+    check(long)
