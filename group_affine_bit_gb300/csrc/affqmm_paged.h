@@ -43,6 +43,7 @@ struct RopeParams {
     int64_t page_bytes, token_bytes, head_bytes, pages;
     const float *k_scale, *v_scale;
     uint32_t* status;
+    int32_t stream;              // more is written than L2 keeps
 };
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t st);
 

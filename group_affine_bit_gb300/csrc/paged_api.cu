@@ -268,6 +268,7 @@ int affqmm_rope_append(const affqmm_kv_cache* cache, const affqmm_rope* rope, co
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
     p.status = status;
+    p.stream = tokens * (heads_q * 2 + (int64_t)cache->heads * 2 * es) * cache->dim > (int64_t)63 << 20;
     return launch_rope_append(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
 }
 
