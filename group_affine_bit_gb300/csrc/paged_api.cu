@@ -292,7 +292,7 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     if ((rc = check_heads(cache, tokens, heads_q))) return rc;
     if (!q || !out) return AFFQMM_E_NULL;
     if (batch < 0 || batch > AFFQMM_PAGED_MAX_BATCH || wide < 0 || table_stride < 0) return AFFQMM_E_SHAPE;
-    if (wide * cache->page >= (int64_t)1 << 31 || wide >= kMost) return AFFQMM_E_SHAPE;
+    if (wide * cache->page >= ((int64_t)1 << 31) - 1024 || wide >= kMost) return AFFQMM_E_SHAPE;   // room to count tiles past the end
     if (!std::isfinite(scale) || window < 0) return AFFQMM_E_ARG;
     if (batch == 0) return AFFQMM_OK;
     if (!lens || (wide > 0 && !table)) return AFFQMM_E_NULL;

@@ -523,15 +523,17 @@ AFFQMM_API int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cac
  *   table     device, int32 [batch, wide], rows table_stride apart; batch x key
  *             heads x wide x page below 2^37
  *   lens      device, int32 [batch]: tokens in the cache, the step's own
- *             included; nothing behind them is read
+ *             included
  *   scale     of the scores; finite
  *   status    device uint32 or NULL: bit 1 is set for a length below 0 or beyond
  *             the table's row (taken as 0, as the row's end) and for a visible
  *             entry of the table that is no page (its keys and values are zeros)
  *   workspace as affqmm_run: its first AFFQMM_WORKSPACE_ZEROED bytes zero before
  *             the first use, shared with the other calls of a stream
- * A token that sees no key gets zeros, and lse -infinity.  What the cache holds
- * outside the visible keys (NaN, say) does not matter.  Sums are fp32; the
+ * A token that sees no key, or whose scores are all -infinity, gets zeros, and
+ * lse -infinity.  What the cache holds outside the visible keys (NaN, say) does
+ * not matter; the rest of a page with a visible key may be read.  A bounded wait
+ * that gave up is reported by affqmm_workspace_status.  Sums are fp32; the
  * probabilities keep 16 bits beside a bf16 cache, 11 beside an e4m3 one.  The same inputs give the same bits on a device.
  * Errors: E_NULL, E_SHAPE, E_ALIGN, E_ARG, E_WORKSPACE, E_DEVICE, E_CUDA. */
 AFFQMM_API int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, const affqmm_lanes* out,

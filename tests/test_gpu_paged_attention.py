@@ -302,3 +302,48 @@ def test_tables_with_room_for_much_more(hq, hk, tokens, dim, kv):
     wide[:, : long["table"].shape[1]] = long["table"]
     long["table"] = wide
     check(long)
+
+
+@pytest.mark.parametrize("page", [1, 2, 4, 512])
+@pytest.mark.parametrize("dim", [32, 64])
+def test_short_rows_in_small_and_large_pages(page, dim):
+    """Rows of 64 bytes and less (e4m3), page by page of one token."""
+    for kv in ("e4m3", "bf16"):
+        check(scene([1, 70, 129, 5, 257], 6, 2, dim, page, kv, tokens=2, seed=page))
+
+
+@pytest.mark.parametrize("hq,tokens,dim,kv", [(16, 9, 64, "bf16"), (16, 9, 128, "e4m3"), (24, 3, 256, "bf16"), (24, 2, 512, "bf16"), (33, 4, 512, "e4m3")])
+def test_row_tiles_of_long_requests(hq, tokens, dim, kv):
+    """More rows than a tile holds, over requests that several runs share."""
+    check(scene([3000, 1, 777], hq, 1, dim, 16, kv, tokens=tokens, seed=dim))
+
+
+def test_more_requests_than_a_warp_scans():
+    """Beyond 256 requests the threads of a CTA share the prefix sum; some of the requests are long enough to be split."""
+    lens = [(i * 7919) % 300 for i in range(290)]
+    lens[5], lens[100], lens[289] = 6000, 4001, 5000
+    check(scene(lens, 2, 1, 64, 16, seed=9))
+
+
+def test_a_pool_whose_axes_lie_apart():
+    """K and V in one allocation, pages padded, key heads a slice of more."""
+    s = scene([100, 37], 4, 2, 64, 16, seed=19, fill=0.125)
+    pages = s["k"].shape[0]
+    big = torch.zeros(pages, 2, 16, 5, 96, dtype=torch.bfloat16, device="cuda")
+    k, v = big[:, 0, :, 1:3, :64], big[:, 1, :, 1:3, :64]
+    k.copy_(s["k"])
+    v.copy_(s["v"])
+    want, _, _ = attend(s)
+    out = api.paged_attention(s["q"].cuda(), api.KVCache(k, v), s["table"].cuda(), s["lens"].cuda())
+    assert torch.equal(out.cpu(), want)
+
+
+def test_empty_batches_and_tables():
+    cache = api.KVCache.empty(2, 16, 2, 64)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    out = api.paged_attention(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), cache, none.view(0, 3), none)
+    assert out.shape == (0, 4, 64)
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    lse = torch.empty(2, 4, device="cuda")
+    out = api.paged_attention(q, cache, none.view(2, 0), torch.tensor([0, 0], dtype=torch.int32, device="cuda"), lse=lse)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
