@@ -9,33 +9,37 @@
 // read once, and the matrix work beside it is small (rows that share a key
 // head: query heads of the group x tokens, 1 .. 64 to a tile).
 //
-// Roles.  A CTA has four consumer warps, two producer warps and one for q.  A
-// tile is 64 or 128 keys.  The producers (one for K, one for V) gather it through the
-// block table with TMA, a box to a page's rows of the tile, in 128-byte panels
-// whose swizzle keeps the fragment loads free of bank conflicts; K and V tiles
-// take turns in one ring.  Rows of pages that no
-// query may see are not read, an entry that is no page reads as zeros, and
-// what lies in a tile beyond the visible keys is masked out by the consumers.
-// The producers run ahead across the borders of requests, so the memory
-// pipeline does not drain there.  (Gathering with 16-byte cp.async copies, two
-// producer warps, cost 54-97 cycles of a warp for each 512 bytes: 58 % of the
-// copy rate for e4m3 pages, 71 % at dim 256.)
+// Roles.  A CTA has four consumer warps (or two groups of four, below), two
+// producer warps and one for q.  A tile is 64 or 128 keys.  The producers (one
+// for K, one for V) gather it through the block table with TMA, a box to a
+// page's rows of the tile, in 128-byte panels whose swizzle keeps the fragment
+// loads free of bank conflicts; K and V tiles take turns in one ring.  Rows of
+// pages that no query may see are not read, an entry that is no page reads as
+// zeros, and what lies in a tile beyond the visible keys is zeroed by the
+// consumers.  The producers run ahead across the borders of requests, so the
+// memory pipeline does not drain there.  (Gathering with 16-byte cp.async
+// copies cost a producer warp 54-97 cycles for each 512 bytes: 559 MB at dim
+// 256 in 117 us instead of 90, 659 MB of e4m3 in 165 us instead of 114-128.)
 //
 // Arithmetic.  Keys are the M side of the matrix instruction (m16n8k16) and
 // query rows its N side, so that one to eight rows cost one instruction per 16
-// x 16 keys x dims: S^T = K Q^T, a warp to 16 keys; then O^T = V^T P^T, a warp
-// to a quarter of the dims, P^T through shared memory.  The running maximum is
-// shared by the CTA and lazy: a tile is rescaled only if a score exceeds it by
-// more than 2^8 (an OR over the barrier that P^T needs anyway), so most tiles
-// cost one barrier and no shuffles.  Scores, maxima, sums and outputs are
-// fp32.  P meets V in the matrix type.  Beside a bf16 cache it is the sum of two
-// bf16 numbers, what the first leaves being in the second, each with its own
-// matrix instruction: 16 bits of P instead of 8, so that the output's own
-// rounding is what is left of the error (2-norm against 64 bits 0.0017; with
-// one bf16 number 0.0023), for instructions that a memory-bound kernel has to
-// spare.  Beside an e4m3 one it is one f16 (11 bits); f16 holds the cache's
-// values exactly, and q is brought to f16 with a power of two per row, so that
-// it keeps its eight bits.  The sum of P is taken before these roundings.
+// keys x 16 dims: S^T = K Q^T, a warp to 16 (or 2 x 16) keys; then O^T = V^T
+// P^T, a warp to a quarter of the dims, P^T through shared memory.  The running
+// maximum is shared by the group and lazy: a tile is rescaled only if a score
+// exceeds it by more than 2^8 (an OR over the barrier that P^T needs anyway),
+// so most tiles cost one barrier and no shuffles.  Scores, maxima, sums and
+// outputs are fp32.  P meets V in the matrix type.  Beside a bf16 cache it is
+// the sum of two bf16 numbers, what the first leaves being in the second, each
+// with its own matrix instruction: 16 bits of P instead of 8, so that the
+// output's own rounding is what is left of the error (2-norm against 64 bits
+// 0.0017; with one bf16 number 0.0023), for instructions that a memory-bound
+// kernel has to spare.  Beside an e4m3 one it is one f16 (11 bits); f16 holds
+// the cache's values exactly, and q is brought to f16 with a power of two per
+// row, so that it keeps its eight bits.  The sum of P is taken before these
+// roundings.  The warp-level matrix instruction, not tcgen05: with few rows the
+// pipe is far from busy, and from 32 rows on it is what bounds the kernel (64
+// rows at dim 128: 192 instructions of 16 cycles a tile, 168 us of the measured
+// 170).
 //
 // Split.  All tiles of all (request, key head, row tile) units, in order, are
 // cut into equal runs, one per CTA, so a batch of ragged lengths loads every
@@ -46,6 +50,13 @@
 // warp while the consumers go on; a run that ends with a unit's first part
 // keeps it in registers if the others are in by then, as they mostly are;
 // else the last to count in joins.
+//
+// Measured (GB300, device time): 64 requests of up to 32768 keys, dim 128, 4.47
+// GB: 656 us, the measured copy rate; one request of 262143 keys 165 us, 96 % of
+// it; 32 requests of up to 4096 keys, dim 256, 559 MB: 90-93 us, 89-91 %; e4m3,
+// 659 MB: 114-128 us (two boards), 76-85 %, its 128-byte rows being what DRAM
+// reads less well; one request of 577 keys 8.6 us, of which 0.7 is the launch,
+// 3 lead to the first tile and 4 are the join of its parts.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -769,274 +780,253 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
             wait(drained, 0);                // its rows go through q buffer 0
             b = early_b, u = early_u, v_scale = early_scale, parts = early_parts, part = true;
         } else {
-        const Span s = walk.s;
-        const bool end_of_run = walk.left <= 0;
-        b = walk.b, u = walk.u;
-        part = walk.t0 > 0 || walk.t1 < s.tiles;
-        if (part) parts = parts_of(walk.unit0, s.tiles);
-        clear();
+            const Span s = walk.s;
+            const bool end_of_run = walk.left <= 0;
+            b = walk.b, u = walk.u;
+            part = walk.t0 > 0 || walk.t1 < s.tiles;
+            if (part) parts = parts_of(walk.unit0, s.tiles);
+            clear();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = NINF;
-            l[nt][0] = l[nt][1] = 0.f;
-        }
-        wait(qfull(qs), qphase);
-        if constexpr (E4M3) {
-            // q to f16, a warp to a row: times a power of two that brings the row's largest magnitude into
-            // [2^13, 2^14), and within 16 dims in the order in which an 8-bit K fragment holds them: a thread's
-            // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
-            constexpr int PAIRS = DP / 64;   // of dims, of a lane
-            uint8_t* rows = qbuf + qs * C::QBYTES;
-            const float k_scale = p.scale_log2 * kscale[qs];
-#pragma unroll 1
-            for (int r = rb + cw; r < rb + GROWS; r += W) {
-                uint32_t w[PAIRS], big = 0;
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) {
-                    const int pair = lane * PAIRS + i;
-                    w[i] = *reinterpret_cast<const uint32_t*>(rows + qchunk_at<QCH>(r, pair >> 2) + (pair & 3) * 4);
-                    big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-                }
-                big = __reduce_max_sync(~0u, big);       // and every lane has read
-                int up = 13 - ((int)(big >> 7) - 127);
-                if (big >= 0x7f80u) up = 0;              // an infinity or NaN stays one
-                up = min(up, 126);
-                const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-                if (lane == 0) qscale[qs * C::ROWS + r] = __uint_as_float((uint32_t)(127 - up) << 23) * k_scale;
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) {
-                    const int pair = lane * PAIRS + i, in16 = pair & 7, k = (in16 >> 1) * 2 + (in16 & 1) * 8;
-                    *reinterpret_cast<uint32_t*>(rows + qchunk_at<QCH>(r, 2 * (pair >> 3) + (k >> 3)) + (k & 7) * 2) =
-                        pack2<true>(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                m[nt][0] = m[nt][1] = NINF;
+                l[nt][0] = l[nt][1] = 0.f;
             }
-            consumer_sync();
-        }
-        v_scale = E4M3 ? vscale[qs] : 1.f;
-        float sc[NT][2];                     // of the scores: softmax scale, log2(e), k's scale, q's power of two
+            wait(qfull(qs), qphase);
+            if constexpr (E4M3) {
+                // q to f16, a warp to a row: times a power of two that brings the row's largest magnitude into
+                // [2^13, 2^14), and within 16 dims in the order in which an 8-bit K fragment holds them: a thread's
+                // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
+                constexpr int PAIRS = DP / 64;   // of dims, of a lane
+                uint8_t* rows = qbuf + qs * C::QBYTES;
+                const float k_scale = p.scale_log2 * kscale[qs];
+#pragma unroll 1
+                for (int r = rb + cw; r < rb + GROWS; r += W) {
+                    uint32_t w[PAIRS], big = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                    for (int i = 0; i < PAIRS; ++i) {
+                        const int pair = lane * PAIRS + i;
+                        w[i] = *reinterpret_cast<const uint32_t*>(rows + qchunk_at<QCH>(r, pair >> 2) + (pair & 3) * 4);
+                        big = max(big, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                    }
+                    big = __reduce_max_sync(~0u, big);       // and every lane has read
+                    int up = 13 - ((int)(big >> 7) - 127);
+                    if (big >= 0x7f80u) up = 0;              // an infinity or NaN stays one
+                    up = min(up, 126);
+                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+                    if (lane == 0) qscale[qs * C::ROWS + r] = __uint_as_float((uint32_t)(127 - up) << 23) * k_scale;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? qscale[qs * C::ROWS + rb + 8 * nt + t2 + e] : p.scale_log2;
-        const uint32_t q_u = qbuf_u + qs * C::QBYTES;
+                    for (int i = 0; i < PAIRS; ++i) {
+                        const int pair = lane * PAIRS + i, in16 = pair & 7, k = (in16 >> 1) * 2 + (in16 & 1) * 8;
+                        *reinterpret_cast<uint32_t*>(rows + qchunk_at<QCH>(r, 2 * (pair >> 3) + (k >> 3)) + (k & 7) * 2) =
+                            pack2<true>(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+                    }
+                }
+                consumer_sync();
+            }
+            v_scale = E4M3 ? vscale[qs] : 1.f;
+            float sc[NT][2];                     // of the scores: softmax scale, log2(e), k's scale, q's power of two
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? qscale[qs * C::ROWS + rb + 8 * nt + t2 + e] : p.scale_log2;
+            const uint32_t q_u = qbuf_u + qs * C::QBYTES;
 
 #pragma unroll 1
-        for (int t = walk.t0; t < walk.t1; ++t) {
-            const int key0 = s.base + t * KEYS;
-            // ---- S^T: this warp's 16 KB keys x all rows
-            float sT[KB][NT][4];
+            for (int t = walk.t0; t < walk.t1; ++t) {
+                const int key0 = s.base + t * KEYS;
+                // ---- S^T: this warp's 16 KB keys x all rows
+                float sT[KB][NT][4];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sT[kb][nt][e] = 0.f;
-            wait(full(slot), phase);
-            {
-                const uint32_t kt = ring_u + (uint32_t)slot * C::TILE;
+                        for (int e = 0; e < 4; ++e) sT[kb][nt][e] = 0.f;
+                wait(full(slot), phase);
+                {
+                    const uint32_t kt = ring_u + (uint32_t)slot * C::TILE;
 #pragma unroll 2
-                for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
-                    uint32_t a0[KB][4], a1[KB][4];
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        const int krow = 16 * (cw + W * kb) + (lane & 15);
-                        if constexpr (E4M3) {
-                            uint32_t r[4];
-                            ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 2 * s2 + (lane >> 4)), r);
-                            a0[kb][0] = e4m3_f16x2(r[0]), a0[kb][2] = e4m3_f16x2(r[0] >> 16);
-                            a0[kb][1] = e4m3_f16x2(r[1]), a0[kb][3] = e4m3_f16x2(r[1] >> 16);
-                            a1[kb][0] = e4m3_f16x2(r[2]), a1[kb][2] = e4m3_f16x2(r[2] >> 16);
-                            a1[kb][1] = e4m3_f16x2(r[3]), a1[kb][3] = e4m3_f16x2(r[3] >> 16);
-                        } else {
-                            ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + (lane >> 4)), a0[kb]);
-                            ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + 2 + (lane >> 4)), a1[kb]);
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t b[4];
-                        ldsm4(q_u + qchunk_at<QCH>(rb + 8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a0[kb], b[0], b[1]);
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a1[kb], b[2], b[3]);
-                    }
-                }
-            }
-            advance();   // the K tile has been read
-
-            // ---- scores in log2 units; what a row may not see is -inf
-            // every key of the tile visible to every row?
-            const bool whole = key0 + KEYS <= s.len - p.tokens + 1 && (p.window <= 0 || key0 >= s.len - p.window);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sT[kb][nt][e] *= sc[nt][e & 1];
-            if (!whole) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int end = min(s.len - p.tokens + row_token[qs * C::ROWS + rb + 8 * nt + t2 + e] + 1, s.hi);
-                        const int begin = p.window > 0 ? end - p.window : 0;
+                    for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
+                        uint32_t a0[KB][4], a1[KB][4];
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
-                            const int key = key0 + 16 * (cw + W * kb) + g;
-                            if (key >= end || key < begin) sT[kb][nt][e] = NINF;
-                            if (key + 8 >= end || key + 8 < begin) sT[kb][nt][e + 2] = NINF;
+                            const int krow = 16 * (cw + W * kb) + (lane & 15);
+                            if constexpr (E4M3) {
+                                uint32_t r[4];
+                                ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 2 * s2 + (lane >> 4)), r);
+                                a0[kb][0] = e4m3_f16x2(r[0]), a0[kb][2] = e4m3_f16x2(r[0] >> 16);
+                                a0[kb][1] = e4m3_f16x2(r[1]), a0[kb][3] = e4m3_f16x2(r[1] >> 16);
+                                a1[kb][0] = e4m3_f16x2(r[2]), a1[kb][2] = e4m3_f16x2(r[2] >> 16);
+                                a1[kb][1] = e4m3_f16x2(r[3]), a1[kb][3] = e4m3_f16x2(r[3] >> 16);
+                            } else {
+                                ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + (lane >> 4)), a0[kb]);
+                                ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + 2 + (lane >> 4)), a1[kb]);
+                            }
                         }
-                    }
-            }
-            bool need = false;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint32_t b[4];
+                            ldsm4(q_u + qchunk_at<QCH>(rb + 8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                            for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a0[kb], b[0], b[1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + LAZY;
-
-            // ---- P^T = 2^(s - m), to [nt][key][row]
-            const uint32_t p_u = pbuf_u + turn * C::PBYTES;
-            float sum[NT][2];                // of this lane's P, before it is rounded
-            auto make_p = [&] {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float m0 = m[nt][0] == NINF ? 0.f : m[nt][0], m1 = m[nt][1] == NINF ? 0.f : m[nt][1];
-                    sum[nt][0] = sum[nt][1] = 0.f;
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        const uint32_t at = p_u + (nt * KEYS + 16 * (cw + W * kb) + g) * 16 + t2 * 2;
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const float x = exp2_approx(sT[kb][nt][e] - m0), y = exp2_approx(sT[kb][nt][e + 1] - m1);
-                            sum[nt][0] += x;
-                            sum[nt][1] += y;
-                            const uint32_t hi = pack2<E4M3>(x, y);
-                            st_shared(at + e * 64, hi);
-                            if constexpr (!E4M3)
-                                st_shared(at + e * 64 + C::LOW,
-                                          pack2<false>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+                            for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a1[kb], b[2], b[3]);
                         }
                     }
                 }
-            };
-            for (bool fresh = t == walk.t0;; fresh = false) {
-                if (!fresh) {
-                    make_p();
-                    if (!consumer_any(need)) break;
-                }
-                // a new maximum for every row: the four warps' maxima meet in shared memory; then P again
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = NINF;
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) x = fmaxf(x, fmaxf(sT[kb][nt][e], sT[kb][nt][e + 2]));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                        if (g == 0) red[cw * GROWS + 8 * nt + t2 + e] = x;
-                    }
-                consumer_sync();
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = m[nt][e];
-#pragma unroll
-                        for (int w = 0; w < W; ++w) x = fmaxf(x, red[w * GROWS + 8 * nt + t2 + e]);
-                        const float f = m[nt][e] == x ? 1.f : exp2_approx(m[nt][e] - x);
-                        m[nt][e] = x;
-                        l[nt][e] *= f;
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] *= f, acc[mt][nt][e + 2] *= f;
-                    }
-                need = false;
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) l[nt][0] += sum[nt][0], l[nt][1] += sum[nt][1];
+                advance();   // the K tile has been read
 
-            // ---- O^T += V^T P^T: this warp's dims, all keys of the tile
-            wait(full(slot), phase);
-            {
-                const uint32_t vt = ring_u + (uint32_t)slot * C::TILE;
-                // Keys that some tokens see and others do not meet P = 0 in the others' columns, where an
-                // infinity or NaN must not become one of the output: with such values among them the tokens
-                // are added one by one, each with the keys that it sees and in the same order.
-                bool apart = false;
+                // ---- scores in log2 units; what a row may not see is -inf
+                // every key of the tile visible to every row?
+                const bool whole = key0 + KEYS <= s.len - p.tokens + 1 && (p.window <= 0 || key0 >= s.len - p.window);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sT[kb][nt][e] *= sc[nt][e & 1];
                 if (!whole) {
-                    constexpr int PCH = C::PITCH / 16;
-                    uint8_t* v = ring + (size_t)slot * C::TILE;
-                    // Rows outside the visible keys are not the cache's (a box reads whole pages, and skips
-                    // those that nobody sees): zeros, so that P = 0 meets a number there.
-                    const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
-#pragma unroll 1
-                    for (int i = ct; i < (z0 + KEYS - z1) * PCH; i += GROUP) {
-                        const int r = i / PCH, row = r < z0 ? r : z1 + r - z0;
-                        *reinterpret_cast<uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH)) = make_uint4(0, 0, 0, 0);
-                    }
-                    // and the rows that not every token sees: the last tokens - 1 keys, and the first of a window
-                    const int a1 = p.window > 0 ? min(z1, max(z0, s.len - p.window - key0)) : z0;
-                    const int b0 = max(a1, min(z1, s.len - p.tokens + 1 - key0)), n = a1 - z0 + z1 - b0;
-#pragma unroll 1
-                    for (int i = ct; i < n * PCH; i += GROUP) {
-                        const int r = i / PCH, row = r < a1 - z0 ? z0 + r : b0 + r - (a1 - z0);
-                        const uint4 w = *reinterpret_cast<const uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH));
-                        apart |= not_finite<E4M3>(w.x) || not_finite<E4M3>(w.y) || not_finite<E4M3>(w.z) || not_finite<E4M3>(w.w);
-                    }
-                    fence_proxy_async_smem();        // before TMA writes the slot again
-                    apart = consumer_any(apart);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int end = min(s.len - p.tokens + row_token[qs * C::ROWS + rb + 8 * nt + t2 + e] + 1, s.hi);
+                            const int begin = p.window > 0 ? end - p.window : 0;
+#pragma unroll
+                            for (int kb = 0; kb < KB; ++kb) {
+                                const int key = key0 + 16 * (cw + W * kb) + g;
+                                if (key >= end || key < begin) sT[kb][nt][e] = NINF;
+                                if (key + 8 >= end || key + 8 < begin) sT[kb][nt][e + 2] = NINF;
+                            }
+                        }
                 }
-                // V^T fragments of 16-dim tile mt: keys 32 kp .. 32 kp + 31, two k-steps
-                auto v_frags = [&](int kp, int mt, uint32_t (&f)[2][4]) {
-                    if constexpr (E4M3) {
-                        uint32_t r[4];
-                        ldsm4t(vt + chunk_at<C::PW, KEYS>(32 * kp + lane, cw * MT + mt), r);
+                bool need = false;
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const uint32_t x = __byte_perm(r[h], 0, 0x3120);   // (key, key + 1) of dim 2g, then of 2g + 1
-                            f[h >> 1][(h & 1) * 2] = e4m3_f16x2(x);
-                            f[h >> 1][(h & 1) * 2 + 1] = e4m3_f16x2(x >> 16);
-                        }
-                    } else {
-                        const int key = 32 * kp + (lane & 7) + ((lane >> 4) << 3);
-                        const int c = 2 * (cw * MT + mt) + ((lane >> 3) & 1);
-                        ldsm4t(vt + chunk_at<C::PW, KEYS>(key, c), f[0]);
-                        ldsm4t(vt + chunk_at<C::PW, KEYS>(key + 16, c), f[1]);
-                    }
-                };
-                auto p_frags = [&](int kp, uint32_t (&b)[C::PN][NT][4]) {
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                    for (int n = 0; n < C::PN; ++n)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            ldsm4t(p_u + n * C::LOW + (nt * KEYS + 32 * kp + lane) * 16, b[n][nt]);
-                };
-                if (!apart) {
-#pragma unroll 1
-                    for (int kp = 0; kp < KEYS / 32; ++kp) {
-                        uint32_t b[C::PN][NT][4];
-                        p_frags(kp, b);
+                        for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + LAZY;
+
+                // ---- P^T = 2^(s - m), to [nt][key][row]
+                const uint32_t p_u = pbuf_u + turn * C::PBYTES;
+                float sum[NT][2];                // of this lane's P, before it is rounded
+                auto make_p = [&] {
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t f[2][4];
-                            v_frags(kp, mt, f);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float m0 = m[nt][0] == NINF ? 0.f : m[nt][0], m1 = m[nt][1] == NINF ? 0.f : m[nt][1];
+                        sum[nt][0] = sum[nt][1] = 0.f;
 #pragma unroll
-                            for (int n = 0; n < C::PN; ++n)
+                        for (int kb = 0; kb < KB; ++kb) {
+                            const uint32_t at = p_u + (nt * KEYS + 16 * (cw + W * kb) + g) * 16 + t2 * 2;
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma<E4M3>(acc[mt][nt], f[0], b[n][nt][0], b[n][nt][1]);
-                                    mma<E4M3>(acc[mt][nt], f[1], b[n][nt][2], b[n][nt][3]);
-                                }
+                            for (int e = 0; e < 4; e += 2) {
+                                const float x = exp2_approx(sT[kb][nt][e] - m0), y = exp2_approx(sT[kb][nt][e + 1] - m1);
+                                sum[nt][0] += x;
+                                sum[nt][1] += y;
+                                const uint32_t hi = pack2<E4M3>(x, y);
+                                st_shared(at + e * 64, hi);
+                                if constexpr (!E4M3)
+                                    st_shared(at + e * 64 + C::LOW,
+                                              pack2<false>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+                            }
                         }
                     }
-                } else {
+                };
+                for (bool fresh = t == walk.t0;; fresh = false) {
+                    if (!fresh) {
+                        make_p();
+                        if (!consumer_any(need)) break;
+                    }
+                    // a new maximum for every row: the four warps' maxima meet in shared memory; then P again
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = NINF;
+#pragma unroll
+                            for (int kb = 0; kb < KB; ++kb) x = fmaxf(x, fmaxf(sT[kb][nt][e], sT[kb][nt][e + 2]));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                            if (g == 0) red[cw * GROWS + 8 * nt + t2 + e] = x;
+                        }
+                    consumer_sync();
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = m[nt][e];
+#pragma unroll
+                            for (int w = 0; w < W; ++w) x = fmaxf(x, red[w * GROWS + 8 * nt + t2 + e]);
+                            const float f = m[nt][e] == x ? 1.f : exp2_approx(m[nt][e] - x);
+                            m[nt][e] = x;
+                            l[nt][e] *= f;
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) acc[mt][nt][e] *= f, acc[mt][nt][e + 2] *= f;
+                        }
+                    need = false;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) l[nt][0] += sum[nt][0], l[nt][1] += sum[nt][1];
+
+                // ---- O^T += V^T P^T: this warp's dims, all keys of the tile
+                wait(full(slot), phase);
+                {
+                    const uint32_t vt = ring_u + (uint32_t)slot * C::TILE;
+                    // Keys that some tokens see and others do not meet P = 0 in the others' columns, where an
+                    // infinity or NaN must not become one of the output: with such values among them the tokens
+                    // are added one by one, each with the keys that it sees and in the same order.
+                    bool apart = false;
+                    if (!whole) {
+                        constexpr int PCH = C::PITCH / 16;
+                        uint8_t* v = ring + (size_t)slot * C::TILE;
+                        // Rows outside the visible keys are not the cache's (a box reads whole pages, and skips
+                        // those that nobody sees): zeros, so that P = 0 meets a number there.
+                        const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
 #pragma unroll 1
-                    for (int j = 0; j < p.tokens; ++j) {
-                        const int end = s.len - p.tokens + j + 1, begin = p.window > 0 ? max(0, end - p.window) : 0;
+                        for (int i = ct; i < (z0 + KEYS - z1) * PCH; i += GROUP) {
+                            const int r = i / PCH, row = r < z0 ? r : z1 + r - z0;
+                            *reinterpret_cast<uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH)) = make_uint4(0, 0, 0, 0);
+                        }
+                        // and the rows that not every token sees: the last tokens - 1 keys, and the first of a window
+                        const int a1 = p.window > 0 ? min(z1, max(z0, s.len - p.window - key0)) : z0;
+                        const int b0 = max(a1, min(z1, s.len - p.tokens + 1 - key0)), n = a1 - z0 + z1 - b0;
+#pragma unroll 1
+                        for (int i = ct; i < n * PCH; i += GROUP) {
+                            const int r = i / PCH, row = r < a1 - z0 ? z0 + r : b0 + r - (a1 - z0);
+                            const uint4 w = *reinterpret_cast<const uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH));
+                            apart |= not_finite<E4M3>(w.x) || not_finite<E4M3>(w.y) || not_finite<E4M3>(w.z) || not_finite<E4M3>(w.w);
+                        }
+                        fence_proxy_async_smem();        // before TMA writes the slot again
+                        apart = consumer_any(apart);
+                    }
+                    // V^T fragments of 16-dim tile mt: keys 32 kp .. 32 kp + 31, two k-steps
+                    auto v_frags = [&](int kp, int mt, uint32_t (&f)[2][4]) {
+                        if constexpr (E4M3) {
+                            uint32_t r[4];
+                            ldsm4t(vt + chunk_at<C::PW, KEYS>(32 * kp + lane, cw * MT + mt), r);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const uint32_t x = __byte_perm(r[h], 0, 0x3120);   // (key, key + 1) of dim 2g, then of 2g + 1
+                                f[h >> 1][(h & 1) * 2] = e4m3_f16x2(x);
+                                f[h >> 1][(h & 1) * 2 + 1] = e4m3_f16x2(x >> 16);
+                            }
+                        } else {
+                            const int key = 32 * kp + (lane & 7) + ((lane >> 4) << 3);
+                            const int c = 2 * (cw * MT + mt) + ((lane >> 3) & 1);
+                            ldsm4t(vt + chunk_at<C::PW, KEYS>(key, c), f[0]);
+                            ldsm4t(vt + chunk_at<C::PW, KEYS>(key + 16, c), f[1]);
+                        }
+                    };
+                    auto p_frags = [&](int kp, uint32_t (&b)[C::PN][NT][4]) {
+#pragma unroll
+                        for (int n = 0; n < C::PN; ++n)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                ldsm4t(p_u + n * C::LOW + (nt * KEYS + 32 * kp + lane) * 16, b[n][nt]);
+                    };
+                    if (!apart) {
 #pragma unroll 1
                         for (int kp = 0; kp < KEYS / 32; ++kp) {
                             uint32_t b[C::PN][NT][4];
@@ -1046,79 +1036,100 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                                 uint32_t f[2][4];
                                 v_frags(kp, mt, f);
 #pragma unroll
-                                for (int h = 0; h < 8; ++h) {       // keys 2t, 2t + 1 (+ 8 for registers 2 and 3)
-                                    const int key = key0 + 32 * kp + 16 * (h >> 2) + t2 + ((h & 2) ? 8 : 0);
-                                    if (key < begin || key >= end) f[h >> 2][h & 3] &= 0xffff0000u;
-                                    if (key + 1 < begin || key + 1 >= end) f[h >> 2][h & 3] &= 0x0000ffffu;
-                                }
+                                for (int n = 0; n < C::PN; ++n)
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    float d[4] = {acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]};
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        mma<E4M3>(acc[mt][nt], f[0], b[n][nt][0], b[n][nt][1]);
+                                        mma<E4M3>(acc[mt][nt], f[1], b[n][nt][2], b[n][nt][3]);
+                                    }
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < p.tokens; ++j) {
+                            const int end = s.len - p.tokens + j + 1, begin = p.window > 0 ? max(0, end - p.window) : 0;
+#pragma unroll 1
+                            for (int kp = 0; kp < KEYS / 32; ++kp) {
+                                uint32_t b[C::PN][NT][4];
+                                p_frags(kp, b);
 #pragma unroll
-                                    for (int n = 0; n < C::PN; ++n) {
-                                        mma<E4M3>(d, f[0], b[n][nt][0], b[n][nt][1]);
-                                        mma<E4M3>(d, f[1], b[n][nt][2], b[n][nt][3]);
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    uint32_t f[2][4];
+                                    v_frags(kp, mt, f);
+#pragma unroll
+                                    for (int h = 0; h < 8; ++h) {       // keys 2t, 2t + 1 (+ 8 for registers 2 and 3)
+                                        const int key = key0 + 32 * kp + 16 * (h >> 2) + t2 + ((h & 2) ? 8 : 0);
+                                        if (key < begin || key >= end) f[h >> 2][h & 3] &= 0xffff0000u;
+                                        if (key + 1 < begin || key + 1 >= end) f[h >> 2][h & 3] &= 0x0000ffffu;
                                     }
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (row_token[qs * C::ROWS + rb + 8 * nt + t2 + (e & 1)] == j) acc[mt][nt][e] = d[e];
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        float d[4] = {acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]};
+#pragma unroll
+                                        for (int n = 0; n < C::PN; ++n) {
+                                            mma<E4M3>(d, f[0], b[n][nt][0], b[n][nt][1]);
+                                            mma<E4M3>(d, f[1], b[n][nt][2], b[n][nt][3]);
+                                        }
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if (row_token[qs * C::ROWS + rb + 8 * nt + t2 + (e & 1)] == j) acc[mt][nt][e] = d[e];
+                                    }
                                 }
                             }
                         }
                     }
                 }
+                advance();   // the V tile has been read
+                turn ^= 1u;
             }
-            advance();   // the V tile has been read
-            turn ^= 1u;
-        }
 
-        // ---- the end of a segment
-        buf = qs;
-        if (++qs == C::QBUF) qs = 0, qphase ^= 1u;
-        __syncwarp();
-        if (lane == 0 && end_of_run) mbar_arrive(finished);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[nt][e];
-                x += __shfl_xor_sync(~0u, x, 4);
-                x += __shfl_xor_sync(~0u, x, 8);
-                x += __shfl_xor_sync(~0u, x, 16);
-                if (g == 0) lred[cw * GROWS + 8 * nt + t2 + e] = x;
-            }
-        consumer_sync();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = 0.f;
-#pragma unroll
-                for (int w = 0; w < W; ++w) x += lred[w * GROWS + 8 * nt + t2 + e];
-                l[nt][e] = x;
-            }
-        if (part && !end_of_run) {
-            // the run's first part: to its slot, and on with the next segment; the q warp counts it in
-            store_part(false);
-            early = true;
-            early_b = b, early_u = u, early_scale = v_scale, early_parts = parts;
+            // ---- the end of a segment
+            buf = qs;
+            if (++qs == C::QBUF) qs = 0, qphase ^= 1u;
             __syncwarp();
-            if (lane == 0) mbar_arrive(stored(buf));
-            continue;
-        }
-        if (part) {
-            if (walk.t0 == 0) {
-                wait(decided, 0);
-                direct = ok && others_in != 0;
+            if (lane == 0 && end_of_run) mbar_arrive(finished);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[nt][e];
+                    x += __shfl_xor_sync(~0u, x, 4);
+                    x += __shfl_xor_sync(~0u, x, 8);
+                    x += __shfl_xor_sync(~0u, x, 16);
+                    if (g == 0) lred[cw * GROWS + 8 * nt + t2 + e] = x;
+                }
+            consumer_sync();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) x += lred[w * GROWS + 8 * nt + t2 + e];
+                    l[nt][e] = x;
+                }
+            if (part && !end_of_run) {
+                // the run's first part: to its slot, and on with the next segment; the q warp counts it in
+                store_part(false);
+                early = true;
+                early_b = b, early_u = u, early_scale = v_scale, early_parts = parts;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(stored(buf));
+                continue;
             }
-            if (!direct) {
-                store_part(walk.t0 == 0);
-                consumers_sync<C::CONSUMERS>();
-                if (tid == 0) last_flag = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
-                consumers_sync<C::CONSUMERS>();
-                if (last_flag == 0) continue;
+            if (part) {
+                if (walk.t0 == 0) {
+                    wait(decided, 0);
+                    direct = ok && others_in != 0;
+                }
+                if (!direct) {
+                    store_part(walk.t0 == 0);
+                    consumers_sync<C::CONSUMERS>();
+                    if (tid == 0) last_flag = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
+                    consumers_sync<C::CONSUMERS>();
+                    if (last_flag == 0) continue;
+                }
             }
-        }
         }
         if (part) join(parts, direct);
         stage_out(v_scale, buf);
