@@ -26,6 +26,31 @@ int page_shift_of(int64_t page) {
     return -1;
 }
 
+// The cache's axes (0 token, 1 head, 2 page) in the order of their strides, those that are stepped along first.
+struct Axes {
+    int order[3];
+    int64_t stride[3];   // elements; of an axis of one, which is never stepped along, the one before it
+};
+Axes axes_of(const affqmm_kv_cache* c) {
+    const int64_t size[3] = {c->page, c->heads, c->pages}, stride[3] = {c->token_stride, c->head_stride, c->page_stride};
+    Axes a;
+    int n = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (size[i] == 1) continue;
+        int j = n++;
+        for (; j > 0 && stride[i] < stride[a.order[j - 1]]; --j) a.order[j] = a.order[j - 1];
+        a.order[j] = i;
+    }
+    for (int j = 0; j < n; ++j) a.stride[j] = stride[a.order[j]];
+    for (int i = 0; i < 3; ++i)
+        if (size[i] == 1) {
+            a.order[n] = i;
+            a.stride[n] = n ? a.stride[n - 1] : c->dim;
+            ++n;
+        }
+    return a;
+}
+
 int check_cache(const affqmm_kv_cache* c, bool memory) {
     if (!c) return AFFQMM_E_NULL;
     if (c->type != AFFQMM_KV_BF16 && c->type != AFFQMM_KV_E4M3) return AFFQMM_E_ARG;
@@ -43,6 +68,9 @@ int check_cache(const affqmm_kv_cache* c, bool memory) {
         return AFFQMM_E_ALIGN;
     for (int i = 0; i < 3; ++i)
         if (size[i] > 1 && stride[i] % each) return AFFQMM_E_ALIGN;
+    const Axes a = axes_of(c);
+    for (int i = 1; i < 3; ++i)
+        if (a.stride[i] % a.stride[i - 1]) return AFFQMM_E_ALIGN;
     return AFFQMM_OK;
 }
 
@@ -103,25 +131,15 @@ int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, C
     const bool e4m3 = c->type == AFFQMM_KV_E4M3;
     const int es = e4m3 ? 1 : 2, panel = padded * es < 128 ? padded * es : 128;
     const int box = c->page < keys ? c->page : keys;
-    int64_t size[3] = {c->page, c->heads, c->pages};
-    int64_t stride[3] = {c->token_stride * es, c->head_stride * es, c->page_stride * es};
-    // an axis of one is never stepped along, whatever its stride says
-    for (int i = 0; i < 3; ++i)
-        if (size[i] == 1) stride[i] = (int64_t)1 << 36;
-    int order[3] = {0, 1, 2};
-    for (int i = 1; i < 3; ++i)
-        for (int j = i; j > 0 && stride[order[j]] < stride[order[j - 1]]; --j) {
-            const int t = order[j];
-            order[j] = order[j - 1];
-            order[j - 1] = t;
-        }
+    const int64_t size[3] = {c->page, c->heads, c->pages};
+    const Axes a = axes_of(c);
     cuuint64_t dims[4] = {(cuuint64_t)c->dim}, strides[3];
     cuuint32_t boxes[4] = {(cuuint32_t)(panel / es)}, steps[4] = {1, 1, 1, 1};
     for (int i = 0; i < 3; ++i) {
-        axis[i] = order[i];
-        dims[i + 1] = (cuuint64_t)size[order[i]];
-        strides[i] = (cuuint64_t)stride[order[i]];
-        boxes[i + 1] = order[i] == 0 ? (cuuint32_t)box : 1u;
+        axis[i] = a.order[i];
+        dims[i + 1] = (cuuint64_t)size[a.order[i]];
+        strides[i] = (cuuint64_t)(a.stride[i] * es);
+        boxes[i + 1] = a.order[i] == 0 ? (cuuint32_t)box : 1u;
     }
     for (int kv = 0; kv < 2; ++kv)
         if (enc(kv ? v : k, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv ? c->v : c->k, dims,

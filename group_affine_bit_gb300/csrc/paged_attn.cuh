@@ -331,16 +331,13 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this CTA's run of tiles: a prefix sum over the requests' tiles.  Up to 256 requests, every warp makes it
-    // for itself, eight requests to a lane, without a barrier; beyond, the CTA's threads share the requests.
+    // ---- this CTA's run of tiles: a prefix sum over the requests' tiles, which the CTA's threads share
     const int units = p.heads_kv * p.row_tiles;
-    uint32_t all_tiles, ctas, run_tiles, run_unit0, run_at;
+    uint32_t all_tiles = 0, ctas, run_tiles, run_unit0, run_at;
     int run_b;
     {
-        const bool alone = p.batch <= 256;
-        const int sharers = alone ? 32 : THREADS, me = alone ? lane : tid;
-        const int each = (p.batch + sharers - 1) / sharers;
-        const int b0 = min(me * each, p.batch), b1 = min(b0 + each, p.batch);
+        const int each = (p.batch + THREADS - 1) / THREADS;
+        const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
         uint32_t mine = 0;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) mine += (uint32_t)((span_of<KEYS>(p, b).tiles + 1) * units);
@@ -351,47 +348,36 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
             if (lane >= d) x += y;
         }
         uint32_t before = x - mine;
-        all_tiles = __shfl_sync(~0u, x, 31);
-        if (!alone) {
-            if (lane == 31) sums[wid] = x;
-            __syncthreads();
-            all_tiles = 0;
-            for (int w = 0; w < THREADS / 32; ++w) {
-                if (w < wid) before += sums[w];
-                all_tiles += sums[w];
-            }
+        if (lane == 31) sums[wid] = x;
+        __syncthreads();
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < wid) before += sums[w];
+            all_tiles += sums[w];
         }
         // no run is empty: with fewer tiles than CTAs, the first `all_tiles` CTAs take one each
         ctas = min(gridDim.x, all_tiles);
         const uint32_t c = min(blockIdx.x, ctas), per = all_tiles / ctas, over = all_tiles - per * ctas;
         const uint32_t r0 = c * per + c * over / ctas;
         run_tiles = c < ctas ? (c + 1) * per + (c + 1) * over / ctas - r0 : 0;
-        const bool here = run_tiles > 0 && before <= r0 && r0 - before < mine;
-        int b = b0;
-        if (here)
+        if (run_tiles > 0 && before <= r0 && r0 - before < mine) {
+            int b = b0;
 #pragma unroll 1
             for (;; ++b) {
                 const uint32_t n = (uint32_t)((span_of<KEYS>(p, b).tiles + 1) * units);
                 if (r0 - before < n) break;
                 before += n;
             }
-        if (alone) {
-            const int src = __ffs(__ballot_sync(~0u, here)) - 1;
-            run_b = __shfl_sync(~0u, b, src & 31);
-            run_unit0 = __shfl_sync(~0u, before, src & 31);
-        } else {
-            if (here) found_b = b, found_unit0 = before;
-            __syncthreads();
-            run_b = found_b;
-            run_unit0 = found_unit0;
+            found_b = b, found_unit0 = before;
         }
+        __syncthreads();
+        run_b = found_b;
+        run_unit0 = found_unit0;
         run_at = r0 - run_unit0;
     }
     if (blockIdx.x == 0 && p.user_status)
 #pragma unroll 1
         for (int b = tid; b < p.batch; b += THREADS)
             if (p.lens[b] < 0 || p.lens[b] > ((int64_t)p.wide << p.page_shift)) atomicOr(p.user_status, 2u);
-    __syncthreads();                         // the barriers are set up
     if (run_tiles == 0) return;
     Walk<KEYS> walk;
     walk.b = run_b;

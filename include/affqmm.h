@@ -386,8 +386,8 @@ AFFQMM_API int affqmm_run_noalloc(const affqmm_weight* w, const uint16_t* x, int
  *   pages         pages of the pool, at least one; pages * page < 2^31
  *   *_stride      elements between pages, tokens and heads (any order in
  *                 memory; the values of a head are contiguous), each a multiple
- *                 of 16 bytes and at least dim (that of an axis of one does not
- *                 matter)
+ *                 of 16 bytes, at least dim, and a multiple of the next smaller
+ *                 one (that of an axis of one does not matter)
  *   k, v          device, 16-byte aligned
  *   k_scale, v_scale  device, fp32 [heads] or NULL (1): with AFFQMM_KV_E4M3, a
  *                 value is the stored one times its head's scale; NULL with

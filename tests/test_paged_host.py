@@ -29,7 +29,7 @@ CACHE_REFUSALS = [
     (dict(ks=0x1000), "AFFQMM_E_ARG"), (dict(heads=0), "AFFQMM_E_SHAPE"), (dict(dim=0), "AFFQMM_E_SHAPE"), (dict(dim=72), "AFFQMM_E_SHAPE"),
     (dict(dim=528), "AFFQMM_E_SHAPE"), (dict(pages=-1), "AFFQMM_E_SHAPE"), (dict(pages=1 << 27), "AFFQMM_E_SHAPE"), (dict(ps=-8), "AFFQMM_E_SHAPE"),
     (dict(k=None), "AFFQMM_E_NULL"), (dict(v=None), "AFFQMM_E_NULL"), (dict(k=0x100008), "AFFQMM_E_ALIGN"), (dict(ts=252), "AFFQMM_E_ALIGN"),
-    (dict(type=1, hs=136), "AFFQMM_E_ALIGN"), (dict(type=1, vs=0x1002), "AFFQMM_E_ALIGN")]
+    (dict(type=1, hs=136), "AFFQMM_E_ALIGN"), (dict(ps=4104), "AFFQMM_E_ALIGN"), (dict(hs=384), "AFFQMM_E_ALIGN"), (dict(ts=64), "AFFQMM_E_SHAPE"), (dict(type=1, vs=0x1002), "AFFQMM_E_ALIGN")]
 
 
 def attend(L, c, batch=1, tokens=1, hq=8, q=0x300000, out=0x400000, qs=1024, table=0x500000, stride=8, wide=8, lens=0x600000,
