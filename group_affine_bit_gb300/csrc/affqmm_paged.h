@@ -77,11 +77,11 @@ struct AttnShape {
     size_t slot_floats = 0;
 };
 // DP: head dim padded to 64, 128, 256 or 512; rows: (token, head) rows that share a key head; lasting: the tables
-// have room for many tiles.
+// have room for many tiles; pair: two key heads to a CTA.
 #define AFFQMM_ATTN_DECL(DP)                                                                            \
-    AttnShape attn_shape_##DP(bool e4m3, bool lasting, int rows);                                       \
+    AttnShape attn_shape_##DP(bool e4m3, bool lasting, bool pair, int rows);                            \
     cudaError_t attn_allow_smem_##DP();                                                                 \
-    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, int rows, const AttnParams& p, const CUtensorMap& k, \
+    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, \
                                  const CUtensorMap& v, int grid, cudaStream_t st);
 AFFQMM_ATTN_DECL(64)
 AFFQMM_ATTN_DECL(128)

@@ -150,13 +150,13 @@ int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, C
     return AFFQMM_OK;
 }
 
-AttnShape attn_shape(const affqmm_kv_cache* c, int rows, bool lasting) {
+AttnShape attn_shape(const affqmm_kv_cache* c, int rows, bool lasting, bool pair) {
     const bool e4m3 = c->type == AFFQMM_KV_E4M3;
     switch (which_dim(c)) {
-        case 0: return attn_shape_64(e4m3, lasting, rows);
-        case 1: return attn_shape_128(e4m3, lasting, rows);
-        case 2: return attn_shape_256(e4m3, lasting, rows);
-        default: return attn_shape_512(e4m3, lasting, rows);
+        case 0: return attn_shape_64(e4m3, lasting, pair, rows);
+        case 1: return attn_shape_128(e4m3, lasting, pair, rows);
+        case 2: return attn_shape_256(e4m3, lasting, pair, rows);
+        default: return attn_shape_512(e4m3, lasting, pair, rows);
     }
 }
 
@@ -168,14 +168,23 @@ int check_heads(const affqmm_kv_cache* c, int tokens, int heads_q) {
     return AFFQMM_OK;
 }
 
+// Whether a CTA may take two key heads: their rows of 128 bytes or less lie side by side in the pool, and DRAM reads
+// both at once better than either (e4m3, dim 128, 659 MB: see the kernel).
+bool pairable(const affqmm_kv_cache* c, int rows) {
+    const int row_bytes = (64 << which_dim(c)) * (c->type == AFFQMM_KV_E4M3 ? 1 : 2);
+    return rows <= 8 && c->heads % 2 == 0 && row_bytes <= 128 && (c->page == 1 || c->head_stride < c->token_stride);
+}
+
 // Two partial slots for each CTA that the SMs hold, of whichever kernel a call may take.
 size_t attn_workspace(const affqmm_kv_cache* c, int rows, int sms) {
     size_t most = 0;
-    for (const bool lasting : {false, true}) {
-        const AttnShape s = attn_shape(c, rows, lasting);
-        const size_t floats = (size_t)2 * s.ctas_per_sm * sms * s.slot_floats;
-        if (floats > most) most = floats;
-    }
+    for (const bool lasting : {false, true})
+        for (const bool pair : {false, true}) {
+            if (pair && !(lasting && pairable(c, rows))) continue;
+            const AttnShape s = attn_shape(c, rows, lasting, pair);
+            const size_t floats = (size_t)2 * s.ctas_per_sm * sms * s.slot_floats;
+            if (floats > most) most = floats;
+        }
     return kSlotsOffset + most * sizeof(float);
 }
 
@@ -323,7 +332,8 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     int64_t keys = wide * cache->page;       // that a request can have, and a window sees
     if (window > 0 && keys > (int64_t)window + tokens) keys = (int64_t)window + tokens;
     const bool lasting = lasting_tiles(cache, batch, keys, sms);
-    const AttnShape shape = attn_shape(cache, rows, lasting);
+    const bool pair = lasting && pairable(cache, rows);
+    const AttnShape shape = attn_shape(cache, rows, lasting, pair);
     if (!workspace || ws_bytes < attn_workspace(cache, rows, sms)) return AFFQMM_E_WORKSPACE;
     if (!aligned(workspace, 256)) return AFFQMM_E_ALIGN;
     const int which = which_dim(cache);
@@ -370,10 +380,10 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (which) {
-        case 0: e = launch_attn_64(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
-        case 1: e = launch_attn_128(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
-        case 2: e = launch_attn_256(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
-        default: e = launch_attn_512(e4m3, lasting, rows, p, k_map, v_map, grid, st); break;
+        case 0: e = launch_attn_64(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
+        case 1: e = launch_attn_128(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
+        case 2: e = launch_attn_256(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
+        default: e = launch_attn_512(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
     }
     return e == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
 }

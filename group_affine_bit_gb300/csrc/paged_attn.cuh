@@ -85,8 +85,12 @@ constexpr int MAX_SLOTS = 16;
 // `lasting` tiles (dim 128: 678 -> 657 us for 64 requests of up to 32768 keys; 7.6 -> 8.2 for one of 577).
 constexpr int key_blocks(int pitch, int na, bool lasting) { return pitch <= 128 || (pitch == 256 && (na >= 4 || lasting)) ? 2 : 1; }
 
-template <int DP, int NA, bool E4M3, int KBLOCKS>
+template <int DP, int NA, bool E4M3, int KBLOCKS, bool PAIRED>
 struct Cfg {
+    // PAIR: the two groups of consumer warps take two neighbouring key heads, whose rows lie side by side in the
+    // pool, and a tile holds the keys of both.
+    static constexpr bool PAIR = PAIRED;
+    static constexpr int HEADS = PAIR ? 2 : 1;
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int ROWS = 8 * NA;
     static constexpr int PITCH = DP * ES;              // bytes of a cache row in shared memory
@@ -94,7 +98,7 @@ struct Cfg {
     static constexpr int PANELS = PITCH / PW;
     static constexpr int KB = KBLOCKS;
     static constexpr int KEYS = 16 * W * KB;
-    static constexpr int TILE = KEYS * PITCH;
+    static constexpr int HEAD_TILE = KEYS * PITCH, TILE = HEADS * HEAD_TILE;
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int QBUF = (DP == 512 && NA > 1) ? 1 : 2;
     static constexpr int PN = E4M3 ? 1 : 2;            // numbers that make one P
@@ -104,7 +108,7 @@ struct Cfg {
                                     JOIN * ROWS * 4 + 512;
     static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= 32;   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
-    static constexpr int CPS = (LIGHT && FIXED + 3 * TILE <= HALF) ? 2 : 1;
+    static constexpr int CPS = (!PAIR && LIGHT && FIXED + 3 * TILE <= HALF) ? 2 : 1;
     // With one CTA an SM, the rows go to two groups of consumer warps (where there are two row tiles), which share
     // the ring and q and nothing else: two warps to a scheduler, whose latencies overlap.
     static constexpr int NG = CPS == 1 && NA >= 2 ? 2 : 1;
@@ -275,10 +279,10 @@ __device__ __forceinline__ uint32_t run_of(uint32_t x, uint32_t total, uint32_t 
     return (uint32_t)(top / total);
 }
 
-template <int DP, int NA, bool E4M3, int KBLOCKS>
-__global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, NA, E4M3, KBLOCKS>::CPS) paged_attn_kernel(
+template <int DP, int NA, bool E4M3, int KBLOCKS, bool PAIRED>
+__global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::CPS) paged_attn_kernel(
     const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = Cfg<DP, NA, E4M3, KBLOCKS>;
+    using C = Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>;
     constexpr int KEYS = C::KEYS, THREADS = C::THREADS, PRODUCER = C::NG * W;   // the first warp that is no consumer
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
     auto joined = [&](int s) { return counted + 24u + 8u * s; };  // parts of other runs are in the group's share of the ring
     const uint32_t drained = counted + 40u;                      // the q warp has written every row
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
-    __shared__ float kscale[2], vscale[2];
+    __shared__ float kscale[4], vscale[4];   // of each q buffer, of each key head of the unit
     __shared__ int found_b;
     __shared__ uint32_t last_flag, late_join, others_in;
 
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- this CTA's run of tiles: a prefix sum over the requests' tiles, which the CTA's threads share
-    const int units = p.heads_kv * p.row_tiles;
+    const int units = C::PAIR ? p.heads_kv >> 1 : p.heads_kv * p.row_tiles;
     uint32_t all_tiles = 0, ctas, run_tiles, run_unit0, run_at;
     int run_b;
     {
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
         while (ok && walk.next(p, units)) {
             const Span s = walk.s;
             const int32_t* table = p.table + (int64_t)walk.b * p.table_stride;
-            const int head = over(walk.u, p.row_tiles, p.m_row_tiles);
+            const int head0 = C::PAIR ? 2 * walk.u : over(walk.u, p.row_tiles, p.m_row_tiles);
             // 32 entries of the table in the lanes' registers and the next 32 on their way, so that no tile
             // waits for its entries; one that is no page becomes a page beyond the tensor, which reads as zeros
             auto entries = [&](int e) {
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                 wait(empty(slot), phase ^ 1u);
                 if (!ok) break;
                 const uint32_t dst = ring_u + (uint32_t)slot * C::TILE, bar = full(slot);
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::PANELS * box_bytes);
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::HEADS * C::PANELS * box_bytes);
                 __syncwarp();
 #pragma unroll 1
                 for (int i = i0; i < i1; ++i) {
@@ -444,12 +448,16 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                     }
                     const int page = __shfl_sync(~0u, cur, e);
                     const int token = (int)((uint32_t)(key0 + row) & page_mask);
-                    auto at = [&](int axis) { return axis == 0 ? token : axis == 1 ? head : page; };
-                    const int c1 = at(p.axis1), c2 = at(p.axis2), c3 = at(p.axis3);
-                    if (lane == 0)
 #pragma unroll
-                        for (int n = 0; n < C::PANELS; ++n)
-                            tma_load_4d(dst + n * KEYS * C::PW + row * C::PW, map, n * (C::PW / C::ES), c1, c2, c3, bar);
+                    for (int h = 0; h < C::HEADS; ++h) {
+                        auto at = [&](int axis) { return axis == 0 ? token : axis == 1 ? head0 + h : page; };
+                        const int c1 = at(p.axis1), c2 = at(p.axis2), c3 = at(p.axis3);
+                        if (lane == 0)
+#pragma unroll
+                            for (int n = 0; n < C::PANELS; ++n)
+                                tma_load_4d(dst + h * C::HEAD_TILE + n * KEYS * C::PW + row * C::PW, map, n * (C::PW / C::ES), c1, c2, c3,
+                                            bar);
+                    }
                 }
                 turn += 2;
                 slot += 2;
@@ -476,22 +484,32 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
         x.count = (int)(run_of(unit0 + tiles - 1, all_tiles, ctas) - x.first) + 1;
         return x;
     };
+    // Which token and query head row r of unit u is; token >= tokens (or rows beyond the last): none.
+    struct Place {
+        int token, head;
+    };
+    auto place_of = [&](int u, int r) {
+        const int hk = C::PAIR ? 2 * u + r / C::GROWS : over(u, p.row_tiles, p.m_row_tiles);
+        const int at = C::PAIR ? r % C::GROWS : (u - hk * p.row_tiles) * C::ROWS + r;
+        const int j = over(at, p.group, p.m_group);
+        return Place{j, hk * p.group + at - j * p.group};
+    };
     // Rows that are staged in q buffer `buf`, with their maxima and sums, to the output: 16 bytes a thread.
     auto copy_rows = [&](int b, int u, int buf, int first, int step) {
         constexpr int QCH = DP / 8;
         const uint8_t* stage = qbuf + buf * C::QBYTES;
         const float* stat = stats + buf * 2 * C::ROWS;
-        const int hk = over(u, p.row_tiles, p.m_row_tiles), r0 = (u - hk * p.row_tiles) * C::ROWS;
 #pragma unroll 1
         for (int i = first; i < C::ROWS * QCH; i += step) {
-            const int r = i / QCH, ch = i % QCH, j = over(r0 + r, p.group, p.m_group), hq = hk * p.group + r0 + r - j * p.group;
-            if (!ok || j >= p.tokens) continue;
+            const int r = i / QCH, ch = i % QCH;
+            const Place at = place_of(u, r);
+            if (!ok || at.token >= p.tokens) continue;
             if (ch * 8 < p.dim)
-                *reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_bs + (int64_t)j * p.o_ts + (int64_t)hq * p.o_hs + ch * 8) =
+                *reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_bs + (int64_t)at.token * p.o_ts + (int64_t)at.head * p.o_hs + ch * 8) =
                     *reinterpret_cast<const uint4*>(stage + qchunk_at<QCH>(r, ch));
             if (p.lse && ch == 0) {
                 const float top = stat[2 * r], sum = stat[2 * r + 1];
-                p.lse[((int64_t)b * p.tokens + j) * p.heads_q + hq] =
+                p.lse[((int64_t)b * p.tokens + at.token) * p.heads_q + at.head] =
                     ((top == __int_as_float(0xff800000) ? 0.f : top) + __log2f(sum)) * 0.69314718055994531f;
             }
         }
@@ -500,22 +518,20 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
         // ================= q of each segment, rows (token, head of the group), and what is
         // left of a segment's end beside the stream: rows to the output, the run's first part counted in (the
         // counter of a unit's parts is the first run's)
-        const int rows = p.tokens * p.group;
         Walk<KEYS> ahead = walk;             // whose q is loaded next; `walk` follows the consumers
         bool more = true;
         auto load_q = [&](int qs) {
             const Walk<KEYS>& walk = ahead;
             uint8_t* dst = qbuf + qs * C::QBYTES;
-            const int hk = over(walk.u, p.row_tiles, p.m_row_tiles), r0 = (walk.u - hk * p.row_tiles) * C::ROWS;
+            const int hk = C::PAIR ? 2 * walk.u : over(walk.u, p.row_tiles, p.m_row_tiles);
             constexpr int QCH = DP / 8;                             // 16-byte chunks of a row
             const uint16_t* base = p.q + (int64_t)walk.b * p.q_bs;
             // which token and query head each row is, for the consumers too
 #pragma unroll 1
             for (int r = lane; r < C::ROWS; r += 32) {
-                const int at = r0 + r, j = over(at, p.group, p.m_group);
-                const bool in = at < rows;
-                row_token[qs * C::ROWS + r] = in ? j : -1;
-                row_head[qs * C::ROWS + r] = hk * p.group + (at - j * p.group);
+                const Place at = place_of(walk.u, r);
+                row_token[qs * C::ROWS + r] = at.token < p.tokens ? at.token : -1;
+                row_head[qs * C::ROWS + r] = at.head;
             }
             __syncwarp();
             auto source = [&](int r, int ch) {
@@ -531,9 +547,9 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                              "l"(src ? src : p.q), "r"(src ? 16u : 0u) : "memory");
             }
             if constexpr (E4M3)
-                if (lane == 0) {
-                    kscale[qs] = p.k_scale ? p.k_scale[hk] : 1.f;
-                    vscale[qs] = p.v_scale ? p.v_scale[hk] : 1.f;
+                if (lane < C::HEADS) {
+                    kscale[2 * qs + lane] = p.k_scale ? p.k_scale[hk + lane] : 1.f;
+                    vscale[2 * qs + lane] = p.v_scale ? p.v_scale[hk + lane] : 1.f;
                 }
             asm volatile("cp.async.wait_all;" ::: "memory");
             mbar_arrive(qfull(qs));
@@ -586,6 +602,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
     constexpr int MT = C::MT, NT = C::NT, QCH = DP / 8, KB = C::KB, GROWS = C::GROWS;
     const int group = C::NG == 1 ? 0 : wid / W, cw = C::NG == 1 ? wid : wid % W, ct = C::NG == 1 ? tid : tid % GROUP;   // warp and thread of the group
     const int rb = group * GROWS;            // the group's first row
+    const int own_head = C::PAIR ? group * C::HEAD_TILE : 0;   // where a tile holds the group's key head
     red += group * W * GROWS;
     lred += group * W * GROWS;
     weight += group * C::JOIN * GROWS;
@@ -784,7 +801,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                 // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
                 constexpr int PAIRS = DP / 64;   // of dims, of a lane
                 uint8_t* rows = qbuf + qs * C::QBYTES;
-                const float k_scale = p.scale_log2 * kscale[qs];
+                const float k_scale = p.scale_log2 * kscale[2 * qs + (C::PAIR ? group : 0)];
 #pragma unroll 1
                 for (int r = rb + cw; r < rb + GROWS; r += W) {
                     uint32_t w[PAIRS], big = 0;
@@ -809,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                 }
                 consumer_sync();
             }
-            v_scale = E4M3 ? vscale[qs] : 1.f;
+            v_scale = E4M3 ? vscale[2 * qs + (C::PAIR ? group : 0)] : 1.f;
             float sc[NT][2];                     // of the scores: softmax scale, log2(e), k's scale, q's power of two
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -830,7 +847,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                         for (int e = 0; e < 4; ++e) sT[kb][nt][e] = 0.f;
                 wait(full(slot), phase);
                 {
-                    const uint32_t kt = ring_u + (uint32_t)slot * C::TILE;
+                    const uint32_t kt = ring_u + (uint32_t)slot * C::TILE + own_head;
 #pragma unroll 2
                     for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
                         uint32_t a0[KB][4], a1[KB][4];
@@ -959,14 +976,14 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
                 // ---- O^T += V^T P^T: this warp's dims, all keys of the tile
                 wait(full(slot), phase);
                 {
-                    const uint32_t vt = ring_u + (uint32_t)slot * C::TILE;
+                    const uint32_t vt = ring_u + (uint32_t)slot * C::TILE + own_head;
                     // Keys that some tokens see and others do not meet P = 0 in the others' columns, where an
                     // infinity or NaN must not become one of the output: with such values among them the tokens
                     // are added one by one, each with the keys that it sees and in the same order.
                     bool apart = false;
                     if (!whole) {
                         constexpr int PCH = C::PITCH / 16;
-                        uint8_t* v = ring + (size_t)slot * C::TILE;
+                        uint8_t* v = ring + (size_t)slot * C::TILE + own_head;
                         // Rows outside the visible keys are not the cache's (a box reads whole pages, and skips
                         // those that nobody sees): zeros, so that P = 0 meets a number there.
                         const int z0 = max(0, min(KEYS, s.lo - key0)), z1 = max(0, min(KEYS, s.hi - key0));
@@ -1131,10 +1148,10 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS>::THREADS, Cfg<DP, N
     if (!ok && lane == 0) atomicOr(p.status, 1u);
 }
 
-template <int DP, int NA, bool E4M3, bool LASTING>
+template <int DP, int NA, bool E4M3, bool LASTING, bool PAIR>
 struct Launch {
     static constexpr int KB = key_blocks(DP * (E4M3 ? 1 : 2), NA, LASTING);
-    using C = Cfg<DP, NA, E4M3, KB>;
+    using C = Cfg<DP, NA, E4M3, KB, PAIR>;
     static AttnShape shape() {
         AttnShape s;
         s.ctas_per_sm = C::CPS;
@@ -1144,10 +1161,10 @@ struct Launch {
         return s;
     }
     static cudaError_t allow() {
-        return cudaFuncSetAttribute(paged_attn_kernel<DP, NA, E4M3, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        return cudaFuncSetAttribute(paged_attn_kernel<DP, NA, E4M3, KB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     }
     static cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
-        return launch_pdl(paged_attn_kernel<DP, NA, E4M3, KB>, dim3((unsigned)grid), C::THREADS, C::SMEM, st, p, k, v);
+        return launch_pdl(paged_attn_kernel<DP, NA, E4M3, KB, PAIR>, dim3((unsigned)grid), C::THREADS, C::SMEM, st, p, k, v);
     }
 };
 
@@ -1156,13 +1173,17 @@ struct Launch {
 // whose tiles fill shared memory); more rows go to several tiles, each of
 // which reads the keys again, the later ones mostly from L2.
 template <int DP, typename Then>
-auto with_rows(bool e4m3, bool lasting, int rows, Then then) {
+auto with_rows(bool e4m3, bool lasting, bool pair, int rows, Then then) {
     constexpr int MOST = DP <= 128 ? 8 : DP == 256 ? 4 : 2;
     auto typed = [&](auto na) {
         constexpr int NA = decltype(na)::value;
-        if (e4m3) return lasting ? then(Launch<DP, NA, true, true>{}) : then(Launch<DP, NA, true, false>{});
-        return lasting ? then(Launch<DP, NA, false, true>{}) : then(Launch<DP, NA, false, false>{});
+        if (e4m3) return lasting ? then(Launch<DP, NA, true, true, false>{}) : then(Launch<DP, NA, true, false, false>{});
+        return lasting ? then(Launch<DP, NA, false, true, false>{}) : then(Launch<DP, NA, false, false, false>{});
     };
+    if constexpr (DP <= 128)
+        if (pair && e4m3) return then(Launch<DP, 2, true, true, true>{});
+    if constexpr (DP <= 64)
+        if (pair) return then(Launch<DP, 2, false, true, true>{});
     if (rows <= 8) return typed(std::integral_constant<int, 1>{});
     if (rows <= 16 || MOST == 2) return typed(std::integral_constant<int, 2>{});
     if (rows <= 32 || MOST == 4) return typed(std::integral_constant<int, MOST < 4 ? 2 : 4>{});
@@ -1170,21 +1191,21 @@ auto with_rows(bool e4m3, bool lasting, int rows, Then then) {
 }
 
 template <int DP>
-AttnShape shape(bool e4m3, bool lasting, int rows) {
-    return with_rows<DP>(e4m3, lasting, rows, [](auto l) { return l.shape(); });
+AttnShape shape(bool e4m3, bool lasting, bool pair, int rows) {
+    return with_rows<DP>(e4m3, lasting, pair, rows, [](auto l) { return l.shape(); });
 }
 template <int DP>
 cudaError_t allow_all() {
-    for (int i = 0; i < 16; ++i) {
-        const cudaError_t e = with_rows<DP>(i & 1, i & 2, 8 << (i >> 2), [](auto l) { return l.allow(); });
+    for (int i = 0; i < 32; ++i) {
+        const cudaError_t e = with_rows<DP>(i & 1, i & 2, i & 4, 8 << (i >> 3), [](auto l) { return l.allow(); });
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 template <int DP>
-cudaError_t launch(bool e4m3, bool lasting, int rows, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid,
+cudaError_t launch(bool e4m3, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid,
                    cudaStream_t st) {
-    return with_rows<DP>(e4m3, lasting, rows, [&](auto l) { return l.launch(p, k, v, grid, st); });
+    return with_rows<DP>(e4m3, lasting, pair, rows, [&](auto l) { return l.launch(p, k, v, grid, st); });
 }
 
 }  // namespace attn
@@ -1192,10 +1213,12 @@ cudaError_t launch(bool e4m3, bool lasting, int rows, const AttnParams& p, const
 
 #define AFFQMM_ATTN_DEFINE(DP)                                                                                              \
     namespace affqmm {                                                                                                      \
-    AttnShape attn_shape_##DP(bool e4m3, bool lasting, int rows) { return attn::shape<DP>(e4m3, lasting, rows); }           \
+    AttnShape attn_shape_##DP(bool e4m3, bool lasting, bool pair, int rows) {                                               \
+        return attn::shape<DP>(e4m3, lasting, pair, rows);                                                                  \
+    }                                                                                                                       \
     cudaError_t attn_allow_smem_##DP() { return attn::allow_all<DP>(); }                                                    \
-    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, int rows, const AttnParams& p, const CUtensorMap& k,              \
+    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k,   \
                                  const CUtensorMap& v, int grid, cudaStream_t st) {                                         \
-        return attn::launch<DP>(e4m3, lasting, rows, p, k, v, grid, st);                                                    \
+        return attn::launch<DP>(e4m3, lasting, pair, rows, p, k, v, grid, st);                                              \
     }                                                                                                                       \
     }

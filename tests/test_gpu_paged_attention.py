@@ -288,7 +288,8 @@ def test_the_workspace_serves_projections_and_attention():
 
 
 @pytest.mark.parametrize("hq,hk,tokens,dim,kv", [(8, 2, 1, 128, "bf16"), (6, 2, 3, 128, "bf16"), (4, 2, 1, 80, "bf16"), (8, 2, 1, 256, "e4m3"),
-                                                 (8, 2, 4, 192, "e4m3")])
+                                                 (8, 2, 4, 192, "e4m3"), (8, 2, 1, 128, "e4m3"), (12, 6, 4, 96, "e4m3"), (8, 8, 1, 64, "bf16"),
+                                                 (6, 2, 2, 48, "e4m3"), (9, 3, 1, 64, "bf16"), (32, 4, 1, 64, "e4m3")])
 def test_tables_with_room_for_much_more(hq, hk, tokens, dim, kv):
     """The same requests in rows of a table that could hold half a million tokens: a coarser cut of the work."""
     for page, window in ((16, 0), (4, 40)):
