@@ -169,10 +169,12 @@ int check_heads(const affqmm_kv_cache* c, int tokens, int heads_q) {
 }
 
 // Whether a CTA may take two key heads: their rows of 128 bytes or less lie side by side in the pool, and DRAM reads
-// both at once better than either (e4m3, dim 128, 659 MB: see the kernel).
+// both at once better than either (e4m3, dim 128, 64 requests of up to 16384 keys, pages of 32: 202 -> 168 us; dim 64,
+// pages of 64: 173 -> 113).  Not for pages below 32 tokens, whose small boxes want the producers of two CTAs an SM
+// (pages of 16: 207 us with one head to a CTA, 262 with two).
 bool pairable(const affqmm_kv_cache* c, int rows) {
     const int row_bytes = (64 << which_dim(c)) * (c->type == AFFQMM_KV_E4M3 ? 1 : 2);
-    return rows <= 8 && c->heads % 2 == 0 && row_bytes <= 128 && (c->page == 1 || c->head_stride < c->token_stride);
+    return rows <= 8 && c->heads % 2 == 0 && row_bytes <= 128 && c->page >= 32 && c->head_stride < c->token_stride;
 }
 
 // Two partial slots for each CTA that the SMs hold, of whichever kernel a call may take.

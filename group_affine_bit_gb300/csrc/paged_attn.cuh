@@ -19,7 +19,7 @@
 // consumers.  The producers run ahead across the borders of requests, so the
 // memory pipeline does not drain there.  (Gathering with 16-byte cp.async
 // copies cost a producer warp 54-97 cycles for each 512 bytes: 559 MB at dim
-// 256 in 117 us instead of 90, 659 MB of e4m3 in 165 us instead of 114-128.)
+// 256 in 117 us instead of 90, 659 MB of e4m3 in 165 us instead of 108-129.)
 //
 // Arithmetic.  Keys are the M side of the matrix instruction (m16n8k16) and
 // query rows its N side, so that one to eight rows cost one instruction per 16
@@ -41,6 +41,12 @@
 // rows at dim 128: 192 instructions of 16 cycles a tile, 168 us of the measured
 // 170).
 //
+// Groups.  Where one CTA fills an SM and the rows fill two row tiles or more,
+// they go to two groups of four consumer warps that share the ring and q: two
+// warps to a scheduler, whose latencies overlap (64 rows at dim 128: 226 -> 204
+// us).  In long tables of short rows the two groups take two neighbouring key
+// heads instead (paged_api.cu says where).
+//
 // Split.  All tiles of all (request, key head, row tile) units, in order, are
 // cut into equal runs, one per CTA, so a batch of ragged lengths loads every
 // SM alike; each CTA finds its run by a prefix sum over the lengths.  The runs
@@ -54,9 +60,8 @@
 // Measured (GB300, device time): 64 requests of up to 32768 keys, dim 128, 4.47
 // GB: 656 us, the measured copy rate; one request of 262143 keys 165 us, 96 % of
 // it; 32 requests of up to 4096 keys, dim 256, 559 MB: 90-93 us, 89-91 %; e4m3,
-// 659 MB: 114-128 us (two boards), 76-85 %, its 128-byte rows being what DRAM
-// reads less well; one request of 577 keys 8.6 us, of which 0.7 is the launch,
-// 3 lead to the first tile and 4 are the join of its parts.
+// 659 MB: 108 us, 90 %; one request of 577 keys 8.6 us, of which 0.7 is the
+// launch, 3 lead to the first tile and 4 are the join of its parts.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -292,7 +292,7 @@ def test_the_workspace_serves_projections_and_attention():
                                                  (6, 2, 2, 48, "e4m3"), (9, 3, 1, 64, "bf16"), (32, 4, 1, 64, "e4m3")])
 def test_tables_with_room_for_much_more(hq, hk, tokens, dim, kv):
     """The same requests in rows of a table that could hold half a million tokens: a coarser cut of the work."""
-    for page, window in ((16, 0), (4, 40)):
+    for page, window in ((16, 0), (4, 40), (32, 0), (64, 100)):
         s = scene(EDGES, hq, hk, dim, page, kv, tokens=tokens, seed=dim)
         wide = torch.full((len(EDGES), (1 << 19) // page), -1, dtype=torch.int32)
         wide[:, : s["table"].shape[1]] = s["table"]
