@@ -371,6 +371,8 @@ AFFQMM_API int affqmm_run_noalloc(const affqmm_weight* w, const uint16_t* x, int
  * `page` tokens; request r's token i sits in page table[r][i / page], at
  * token i % page of it; a slot names a token of the pool, page number * page
  * + token.  The method's pages have no counterpart to these entry points.
+ * Their kernels wait for the kernel ahead of them in the stream before they
+ * read or write anything.
  */
 
 /* Most requests of a call, and most query tokens of a request. */
