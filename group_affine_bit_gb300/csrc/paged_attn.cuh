@@ -209,6 +209,15 @@ __device__ __forceinline__ bool group_any(int group, bool v) {
         : "=r"(r) : "r"((uint32_t)v), "r"(1 + group) : "memory");
     return r != 0;
 }
+// Whether `v` holds in every consumer thread: what branches around a barrier is decided by all of them alike.
+template <int THREADS>
+__device__ __forceinline__ bool consumers_all(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 3, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r) : "r"((uint32_t)v), "n"(THREADS) : "memory");
+    return r != 0;
+}
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(THREADS) : "memory"); }
 // 16-byte chunk `c` of row `row` of a tile: panels of PW bytes of every row,
@@ -436,6 +445,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 // the tile's boxes that hold a visible key
                 const int i0 = max(0, s.lo - key0) >> box_shift, i1 = (min(KEYS, s.hi - key0) + box - 1) >> box_shift;
                 wait(empty(slot), phase ^ 1u);
+                ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 const uint32_t dst = ring_u + (uint32_t)slot * C::TILE, bar = full(slot);
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::HEADS * C::PANELS * box_bytes);
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
         }
         if (walk.t0 == 0 && walk.t1 < walk.s.tiles) {
             // the run ends with its unit's first part: the other parts' runs mostly began with theirs, so
-            // look for them while the last tiles are added
+            // look for them as soon as the last tile is added, while the consumers add up their sums
             if (lane == 0) {
                 const Parts x = parts_of(walk.unit0, walk.s.tiles);
                 const uint32_t* counter = p.counters + x.first;
@@ -784,6 +794,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
             if (!early) break;
             early = false;
             wait(counted, 0);
+            ok = consumers_all<C::CONSUMERS>(ok);
             if (!ok || late_join == 0) break;
             wait(drained, 0);                // its rows go through q buffer 0
             b = early_b, u = early_u, v_scale = early_scale, parts = early_parts, part = true;
@@ -1128,6 +1139,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
             if (part) {
                 if (walk.t0 == 0) {
                     wait(decided, 0);
+                    ok = consumers_all<C::CONSUMERS>(ok);
                     direct = ok && others_in != 0;
                 }
                 if (!direct) {
