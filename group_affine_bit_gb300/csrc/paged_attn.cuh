@@ -26,16 +26,19 @@
 // keys x 16 dims: S^T = K Q^T, a warp to 16 (or 2 x 16) keys; then O^T = V^T
 // P^T, a warp to a quarter of the dims, P^T through shared memory.  The running
 // maximum is shared by the group and lazy: a tile is rescaled only if a score
-// exceeds it by more than 2^8 (an OR over the barrier that P^T needs anyway),
-// so most tiles cost one barrier and no shuffles.  Scores, maxima, sums and
+// exceeds it by more than 2^8 (e4m3: 2^2; an OR over the barrier that P^T needs
+// anyway), so most tiles cost one barrier and no shuffles.  Scores, maxima, sums and
 // outputs are fp32.  P meets V in the matrix type.  Beside a bf16 cache it is
 // the sum of two bf16 numbers, what the first leaves being in the second, each
 // with its own matrix instruction: 16 bits of P instead of 8, so that the
 // output's own rounding is what is left of the error (2-norm against 64 bits
 // 0.0017; with one bf16 number 0.0023), for instructions that a memory-bound
-// kernel has to spare.  Beside an e4m3 one it is one f16 (11 bits); f16 holds
-// the cache's values exactly, and q is brought to f16 with a power of two per
-// row, so that it keeps its eight bits.  The sum of P is taken before these
+// kernel has to spare.  Beside an e4m3 one it is one f16, 2^13 times P: f16 has
+// 11 bits from 2^-14 on and reaches 2^16, so that P keeps them down to 2^-27 of
+// the running maximum, and below that is off by 2^-38 at most (a tail 18 nats
+// below a key whose value is zero is the whole output; with P itself in f16 it
+// came out as zero).  f16 holds the cache's values exactly, and q is brought to
+// f16 with a power of two per row, so that it keeps its eight bits.  The sum of P is taken before these
 // roundings.  The warp-level matrix instruction, not tcgen05: with few rows the
 // pipe is far from busy, and from 32 rows on it is what bounds the kernel (64
 // rows at dim 128: 192 instructions of 16 cycles a tile, 168 us of the measured
@@ -78,7 +81,8 @@ namespace attn {
 
 constexpr int W = 4;                       // consumer warps
 constexpr int GROUP = 32 * W;             // threads of a group of consumers
-constexpr float LAZY = 8.f;                // log2 of how far a score may exceed the running maximum
+constexpr float lazy(bool e4m3) { return e4m3 ? 2.f : 8.f; }   // log2 of how far a score may exceed the running maximum
+constexpr float lift(bool e4m3) { return e4m3 ? 13.f : 0.f; }  // log2 of what P is multiplied by: with lazy() below f16's 16
 constexpr size_t SM_SMEM = 233472;         // shared memory of an SM, 1 KB of it taken by each CTA
 constexpr size_t CTA_SMEM = 232448;        // and what one CTA may have of it
 constexpr size_t STATIC_SMEM = 1024;       // the kernel's few static variables, and the ring's alignment
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
             if (p.lse && ch == 0) {
                 const float top = stat[2 * r], sum = stat[2 * r + 1];
                 p.lse[((int64_t)b * p.tokens + at.token) * p.heads_q + at.head] =
-                    ((top == __int_as_float(0xff800000) ? 0.f : top) + __log2f(sum)) * 0.69314718055994531f;
+                    ((top == __int_as_float(0xff800000) ? 0.f : top) + __log2f(sum) - lift(E4M3)) * 0.69314718055994531f;
             }
         }
     };
@@ -925,15 +929,15 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + LAZY;
+                        for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + lazy(E4M3);
 
-                // ---- P^T = 2^(s - m), to [nt][key][row]
+                // ---- P^T = 2^(s - m + lift), to [nt][key][row]
                 const uint32_t p_u = pbuf_u + turn * C::PBYTES;
                 float sum[NT][2];                // of this lane's P, before it is rounded
                 auto make_p = [&] {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float m0 = m[nt][0] == NINF ? 0.f : m[nt][0], m1 = m[nt][1] == NINF ? 0.f : m[nt][1];
+                        const float m0 = (m[nt][0] == NINF ? 0.f : m[nt][0]) - lift(E4M3), m1 = (m[nt][1] == NINF ? 0.f : m[nt][1]) - lift(E4M3);
                         sum[nt][0] = sum[nt][1] = 0.f;
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {

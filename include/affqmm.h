@@ -536,7 +536,9 @@ AFFQMM_API int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cac
  * lse -infinity.  What the cache holds outside the visible keys (NaN, say) does
  * not matter; the rest of a page with a visible key may be read.  A bounded wait
  * that gave up is reported by affqmm_workspace_status.  Sums are fp32; the
- * probabilities keep 16 bits beside a bf16 cache, 11 beside an e4m3 one.  The same inputs give the same bits on a device.
+ * probabilities keep 16 bits beside a bf16 cache; beside an e4m3 one 11 bits
+ * down to 2^-27 of a row's largest, and smaller ones are off by 2^-38 of it at
+ * most.  The same inputs give the same bits on a device.
  * Errors: E_NULL, E_SHAPE, E_ALIGN, E_ARG, E_WORKSPACE, E_DEVICE, E_CUDA. */
 AFFQMM_API int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, const affqmm_lanes* out,
                                       float* lse, int64_t batch, int tokens, int heads_q, const int32_t* table,

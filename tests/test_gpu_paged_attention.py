@@ -115,6 +115,27 @@ def test_rising_scores():
     check(s, scale=0.5)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,dim", [(8, 64), (24, 128), (128, 256)])
+@pytest.mark.parametrize("nats", [10, 15, 16, 17, 18])
+def test_small_probabilities_beside_a_large_one(nats, hq, dim, kv):
+    """One key `nats` above the others, whose value is zero: the others are the whole output, and all alike, so that
+    what their probabilities lose does not average out.  Requests enough that a run takes whole ones."""
+    s = scene([600] * 40, hq, 8, dim, 16, kv, seed=nats)
+    k, v = s["k"].float(), s["v"].float().abs()
+    k[torch.isfinite(k)] = 0
+    for b in range(40):
+        at = (0, 300, 599)[b % 3]
+        p, o = int(s["table"][b, at // 16]), at % 16
+        k[p, o, :, 0], v[p, o] = 1, 0
+    s["k"], s["v"] = k.to(s["k"].dtype), v.to(s["v"].dtype)
+    s["q"] = torch.zeros_like(s["q"])
+    s["q"][..., 0] = 1
+    if kv == "e4m3":
+        s["k_scale"] = torch.ones(8)
+    check(s, scale=float(nats))
+
+
 @pytest.mark.parametrize("hq,hk,dim,lens,kv", [(8, 1, 128, [20011], "bf16"), (32, 8, 256, [9000, 31], "bf16"), (2, 2, 64, [30000, 1, 64, 7000], "e4m3"),
                                               (16, 1, 512, [5000, 3001], "e4m3")])
 def test_long_caches_are_split_and_joined(hq, hk, dim, lens, kv):
