@@ -33,7 +33,9 @@
 // with its own matrix instruction: 16 bits of P instead of 8, so that the
 // output's own rounding is what is left of the error (2-norm against 64 bits
 // 0.0017; with one bf16 number 0.0023), for instructions that a memory-bound
-// kernel has to spare.  Beside an e4m3 one it is one f16, 2^13 times P: f16 has
+// kernel has to spare.  The first is cut off, not rounded, and the second is
+// never zero beside it: an infinite value meets two positive numbers, and stays
+// infinite.  Beside an e4m3 one it is one f16, 2^13 times P: f16 has
 // 11 bits from 2^-14 on and reaches 2^16, so that P keeps them down to 2^-27 of
 // the running maximum, and below that is off by 2^-38 at most (a tail 18 nats
 // below a key whose value is zero is the whole output; with P itself in f16 it
@@ -947,11 +949,14 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                                 const float x = exp2_approx(sT[kb][nt][e] - m0), y = exp2_approx(sT[kb][nt][e + 1] - m1);
                                 sum[nt][0] += x;
                                 sum[nt][1] += y;
-                                const uint32_t hi = pack2<E4M3>(x, y);
-                                st_shared(at + e * 64, hi);
-                                if constexpr (!E4M3)
-                                    st_shared(at + e * 64 + C::LOW,
-                                              pack2<false>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)));
+                                if constexpr (E4M3) {
+                                    st_shared(at + e * 64, pack2<true>(x, y));
+                                } else {         // the upper halves, and what they leave of P (1 + 2^-23)
+                                    const uint32_t bx = __float_as_uint(x), by = __float_as_uint(y);
+                                    st_shared(at + e * 64, __byte_perm(bx, by, 0x7632));
+                                    st_shared(at + e * 64 + C::LOW, pack2<false>(fmaf(x, 1.f + 0x1p-23f, -__uint_as_float(bx & 0xffff0000u)),
+                                                                                 fmaf(y, 1.f + 0x1p-23f, -__uint_as_float(by & 0xffff0000u))));
+                                }
                             }
                         }
                     }

@@ -198,6 +198,27 @@ def test_nan_and_infinite_scores():
     assert bool(torch.isfinite(out[1, 0, :3]).all()) and bool(torch.isnan(out[1, 0, 3]).all())
 
 
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("dim", [64, 128, 256, 512])
+def test_infinite_values_stay_infinite(dim, tokens):
+    """As the formula has them: a row that sees an infinite value has it in that place, and NaN where both signs meet;
+    other rows and places are as if it were zero."""
+    s = scene([100, 6000, 5], 4, 2, dim, 16, tokens=tokens, seed=dim)
+    clean = {**s, "v": s["v"].clone()}
+    hit = []                                     # (request, token from which it is seen, key head, value, what is there)
+    for b, n in enumerate(s["lens"].tolist()):
+        for key, h, d, x in ((0, 0, 3, math.inf), (n - 1, 1, 5, -math.inf), (n // 3, 1, 9, math.inf), (n // 2, 1, 9, -math.inf)):
+            p, o = int(s["table"][b, key // 16]), key % 16
+            s["v"][p, o, h, d], clean["v"][p, o, h, d] = x, 0
+            hit.append((b, max(0, key - (n - tokens)), h, d, x if d != 9 else math.nan))
+    out, lse, _ = attend(s)
+    want, wl, _ = attend(clean)
+    for b, j, h, d, x in hit:
+        want[b, j:, 2 * h: 2 * h + 2, d] = x
+    assert torch.equal(lse, wl)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out.nan_to_num(7), want.nan_to_num(7))
+
+
 def test_entries_that_are_no_page():
     """Read as zeros, and the status says so; beyond the length they are not looked at."""
     for entry in (-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1):
