@@ -673,6 +673,8 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
         (batch, heads, d), tokens = shape, 1
     else:
         raise ValueError("q must be [batch, query heads, dim] or [batch, tokens, query heads, dim]")
+    if not -1 << 31 <= window < 1 << 31:         # the ABI's int; ctypes would drop the upper bits
+        raise ValueError("window must fit 32 bits")
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=cache.device)
     sq, so, st, tshape = q.stride(), out.stride(), table.stride(), table.shape

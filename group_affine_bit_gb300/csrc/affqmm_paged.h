@@ -59,7 +59,8 @@ struct AttnParams {
     const int32_t* table;
     int64_t table_stride;
     const int32_t* lens;
-    int32_t batch, tokens, heads_q, heads_kv, group, dim, wide, page_shift, window;
+    int32_t batch, tokens, heads_q, heads_kv, group, dim, wide, page_shift;
+    int32_t window;              // 0, or less than wide << page_shift (which is below 2^31 - 1024)
     int32_t row_tiles;           // tiles of 8 NT (token, head) rows
     uint32_t m_group, m_row_tiles;   // ceil(2^32 / d) of the two
     float scale_log2;            // softmax scale times log2(e)

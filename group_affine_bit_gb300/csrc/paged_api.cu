@@ -332,6 +332,7 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     if ((rc = device_sms(&sms))) return rc;
     const int group = heads_q / cache->heads, rows = tokens * group;
     int64_t keys = wide * cache->page;       // that a request can have, and a window sees
+    if (window >= keys) window = 0;          // it hides nothing (and the kernel's sums of lengths and windows stay within 32 bits)
     if (window > 0 && keys > (int64_t)window + tokens) keys = (int64_t)window + tokens;
     const bool lasting = lasting_tiles(cache, batch, keys, sms);
     const bool pair = lasting && pairable(cache, rows);

@@ -99,6 +99,23 @@ def test_windows(window, tokens):
     check(scene([0, 1, 3, 16, 64, 65, 130, 700], 8, 2, 128, 8, tokens=tokens, seed=window), window=window)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 31 - 64])
+@pytest.mark.parametrize("tokens", [1, 5, 64])
+def test_windows_that_hide_nothing(window, tokens):
+    s = scene([0, 1, 2, 3, 4, 5, 6, 63, 64, 130], 2, 2, 64, 8, tokens=tokens, seed=tokens)
+    got, want = check(s, window=window), check(s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_window_beyond_32_bits_is_refused():
+    s = scene([5], 2, 2, 64, 8)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            attend(s, window=window)
+    with pytest.raises(api.AffqmmError):
+        attend(s, window=-1)
+
+
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.25, 30.0])
 def test_scales(scale):
     """Sharp, flat and negative scores; at 30 the running maximum moves many times."""
