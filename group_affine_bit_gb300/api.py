@@ -8,6 +8,7 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -138,6 +139,33 @@ def _stream_ptr(stream, device_index: int | None = None) -> int:
     return int(stream.cuda_stream)
 
 
+def _under(stream, device):
+    """Context in which torch allocates and fills for a call's stream: what is made there is ready when the call's
+    kernel runs, and goes back to that stream's memory."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _under(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _capture_id(stream_ptr: int) -> int:
+    """Which capture a stream is in, 0 for none."""
+    status, number = ctypes.c_int(0), ctypes.c_uint64(0)
+    rc = ctypes.CDLL("libcuda.so.1").cuStreamGetCaptureInfo_v2(ctypes.c_void_p(stream_ptr), ctypes.byref(status),
+                                                               ctypes.byref(number), None, None, None)
+    if rc != 0:
+        raise RuntimeError(f"cuStreamGetCaptureInfo: error {rc}")
+    return number.value if status.value else 0
+
+
 @dataclass
 class PackedWeight:
     """A packed affine table (device memory owned by the torch tensor `packed`)."""
@@ -173,7 +201,7 @@ def pack(codes: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor, bits: 
     if codes.dtype != torch.uint8 or scales.dtype != torch.bfloat16 or biases.dtype != torch.bfloat16:
         raise ValueError("pack wants uint8 codes and bf16 scales and biases")
     nbytes = packed_bytes(bits, group, N, K)
-    packed = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=codes.device)
+    packed = _empty(max(nbytes, 1), torch.uint8, codes.device, stream)
     _check(lib().affqmm_pack(bits, group, N, K, codes.data_ptr(), scales.data_ptr(), biases.data_ptr(),
                              packed.data_ptr(), _stream_ptr(stream)), "affqmm_pack")
     return PackedWeight(bits, group, N, K, packed)
@@ -207,16 +235,35 @@ def workspace_bytes_stacked(ws, M: int) -> int:
 
 class Workspace:
     """A zero-filled device buffer that grows on demand.  The library leaves it
-    zeroed after every call; calls sharing one must be stream-ordered."""
+    zeroed after every call; calls sharing one must be stream-ordered.  It is
+    made and filled on the stream of the call that needs it.  A captured graph
+    keeps a buffer's address, so one that is outgrown is kept too (each is at
+    least twice the last), and one made during a capture, which only a replay
+    fills, serves that capture alone."""
 
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
+        self._kept: list = []        # outgrown buffers
+        self._capture = 0            # the capture that fills `buf`, 0: it is filled
 
-    def get(self, nbytes: int) -> torch.Tensor:
-        if self.buf.numel() < nbytes:
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+    def get(self, nbytes: int, stream=None) -> torch.Tensor:
+        """The buffer for a call on `stream` (the current one if None)."""
+        if self._capture or self.buf.numel() < nbytes:
+            self._make(nbytes, stream)
         return self.buf
+
+    def _make(self, nbytes: int, stream):
+        with _under(stream, self.device):
+            capture = _capture_id(_stream_ptr(stream, self.device.index)) if torch.cuda.is_current_stream_capturing() else 0
+            if capture and capture == self._capture and self.buf.numel() >= nbytes:
+                return
+            if not self._capture:    # the memory of one made during a capture stays with its graph
+                if self.buf.numel():
+                    self._kept.append(self.buf)
+                nbytes = max(nbytes, 2 * self.buf.numel())
+            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self._capture = capture
 
 
 _workspaces: dict = {}
@@ -246,11 +293,11 @@ def run(w: PackedWeight, x: torch.Tensor, y: torch.Tensor | None = None, workspa
     M = x.shape[0]
     dev = x.get_device()
     if y is None:
-        y = torch.empty(M, w.N, dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, w.N), torch.bfloat16, x.device, stream)
     sp = _stream_ptr(stream, dev)
     ws = workspace or default_workspace(dev, sp)
     need = workspace_bytes(w, M)
-    buf = ws.get(need)
+    buf = ws.get(need, stream)
     cw = w.cstruct()
     _check(lib().affqmm_run(ctypes.byref(cw), x.data_ptr(), M, y.data_ptr(), buf.data_ptr() if need else None,
                             buf.numel(), sp), "affqmm_run")
@@ -265,11 +312,11 @@ def run_exact(w: PackedWeight, x: torch.Tensor, y: torch.Tensor | None = None, w
     M = x.shape[0]
     dev = x.get_device()
     if y is None:
-        y = torch.empty(M, w.N, dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, w.N), torch.bfloat16, x.device, stream)
     sp = _stream_ptr(stream, dev)
     ws = workspace or default_workspace(dev, sp)
     need = workspace_bytes(w, M)
-    buf = ws.get(need)
+    buf = ws.get(need, stream)
     cw = w.cstruct()
     _check(lib().affqmm_run_exact(ctypes.byref(cw), x.data_ptr(), M, y.data_ptr(), buf.data_ptr() if need else None,
                                   buf.numel(), sp), "affqmm_run_exact")
@@ -295,11 +342,11 @@ def run_exact_sums(w: PackedWeight, x: torch.Tensor, xsums: torch.Tensor, y: tor
     _check_xsums(xsums, M, w, x)
     dev = x.get_device()
     if y is None:
-        y = torch.empty(M, w.N, dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, w.N), torch.bfloat16, x.device, stream)
     sp = _stream_ptr(stream, dev)
     ws = workspace or default_workspace(dev, sp)
     need = workspace_bytes(w, M)
-    buf = ws.get(need)
+    buf = ws.get(need, stream)
     cw = w.cstruct()
     _check(lib().affqmm_run_exact_sums(ctypes.byref(cw), x.data_ptr(), xsums.data_ptr(), M, y.data_ptr(),
                                        buf.data_ptr() if need else None, buf.numel(), sp), "affqmm_run_exact_sums")
@@ -316,11 +363,11 @@ def run_geglu(w: PackedWeight, x: torch.Tensor, form: int = FORM_ROUNDED, xsums:
         _check_xsums(xsums, M, w, x)
     dev = x.get_device()
     if h is None:
-        h = torch.empty(M, w.N // 2, dtype=torch.bfloat16, device=x.device)
+        h = _empty((M, w.N // 2), torch.bfloat16, x.device, stream)
     sp = _stream_ptr(stream, dev)
     ws = workspace or default_workspace(dev, sp)
     need = workspace_bytes(w, M)
-    buf = ws.get(need)
+    buf = ws.get(need, stream)
     cw = w.cstruct()
     xs = xsums.data_ptr() if (form == FORM_EXACT_SUMS and xsums is not None) else None
     _check(lib().affqmm_run_geglu(ctypes.byref(cw), x.data_ptr(), xs, M, int(form), h.data_ptr(),
@@ -347,7 +394,7 @@ def run_host(w: PackedWeight, x: torch.Tensor, y: torch.Tensor, x_dev: torch.Ten
     sp = _stream_ptr(stream, dev)
     ws = workspace or default_workspace(dev, sp)
     need = workspace_bytes(w, M)
-    buf = ws.get(need)
+    buf = ws.get(need, stream)
     cw = w.cstruct()
     _check(lib().affqmm_run_host(ctypes.byref(cw), x.data_ptr(), M, y.data_ptr(), x_dev.data_ptr(), y_dev.data_ptr(),
                                  buf.data_ptr() if need else None, buf.numel(), sp), "affqmm_run_host")
@@ -360,11 +407,11 @@ def run_stacked(ws_list, x: torch.Tensor, ys=None, workspace: Workspace | None =
     _check_x(x, K)
     M = x.shape[0]
     if ys is None:
-        ys = [torch.empty(M, w.N, dtype=torch.bfloat16, device=x.device) for w in ws_list]
+        ys = [_empty((M, w.N), torch.bfloat16, x.device, stream) for w in ws_list]
     sp = _stream_ptr(stream, x.get_device())
     wsp = workspace or default_workspace(x.get_device(), sp)
     need = workspace_bytes_stacked(ws_list, M)
-    buf = wsp.get(need)
+    buf = wsp.get(need, stream)
     arr = _warray(ws_list)
     yp = (ctypes.c_void_p * len(ys))(*[y.data_ptr() for y in ys])
     _check(lib().affqmm_run_stacked(len(ws_list), arr, x.data_ptr(), M, yp, buf.data_ptr() if need else None,
@@ -374,7 +421,7 @@ def run_stacked(ws_list, x: torch.Tensor, ys=None, workspace: Workspace | None =
 
 def dequant(w: PackedWeight, stream=None) -> torch.Tensor:
     """The bf16 [N, K] weights as the run kernels dequantize them (test hook)."""
-    out = torch.empty(w.N, w.K, dtype=torch.bfloat16, device=w.packed.device)
+    out = _empty((w.N, w.K), torch.bfloat16, w.packed.device, stream)
     cw = w.cstruct()
     _check(lib().affqmm_dequant(ctypes.byref(cw), out.data_ptr(), _stream_ptr(stream)), "affqmm_dequant")
     return out
@@ -409,12 +456,12 @@ def run_noalloc(w: PackedWeight, x: torch.Tensor, y: torch.Tensor, stream=None) 
     return y
 
 
-def _embed_args(w: PackedWeight, ids: torch.Tensor, scale, out):
+def _embed_args(w: PackedWeight, ids: torch.Tensor, scale, out, stream):
     if not ids.is_cuda or ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 CUDA vector")
     T = ids.shape[0]
     if out is None:
-        out = torch.empty(T, w.K, dtype=torch.bfloat16, device=ids.device)
+        out = _empty((T, w.K), torch.bfloat16, ids.device, stream)
     if out.dtype != torch.bfloat16 or tuple(out.shape) != (T, w.K) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 [{T}, {w.K}] tensor")
     sbits = 0 if scale is None else int(torch.tensor([scale], dtype=torch.bfloat16).view(torch.int16).item()) & 0xFFFF
@@ -425,7 +472,7 @@ def embed_rows(w: PackedWeight, ids: torch.Tensor, scale: float | None = None, o
                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[t, k] = bf16(W[ids[t], k] * bf16(scale)) (or W's rows when scale is None),
     W = bf16(s*q + b): rows gathered from the packed table.  ids: int32 CUDA [T]."""
-    T, out, sbits = _embed_args(w, ids, scale, out)
+    T, out, sbits = _embed_args(w, ids, scale, out, stream)
     cw = w.cstruct()
     _check(lib().affqmm_embed_rows(ctypes.byref(cw), ids.data_ptr(), T, 0 if scale is None else 1, sbits,
                                    out.data_ptr(), status.data_ptr() if status is not None else None,
@@ -442,7 +489,7 @@ def rows_bytes(bits: int, group: int, N: int, K: int) -> int:
 def pack_rows(w: PackedWeight, stream=None) -> torch.Tensor:
     """The row-contiguous copy of a packed table that embed_rows_copy gathers from."""
     nbytes = rows_bytes(w.bits, w.group, w.N, w.K)
-    rows = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=w.packed.device)
+    rows = _empty(max(nbytes, 1), torch.uint8, w.packed.device, stream)
     cw = w.cstruct()
     _check(lib().affqmm_pack_rows(ctypes.byref(cw), rows.data_ptr(), _stream_ptr(stream)), "affqmm_pack_rows")
     return rows
@@ -451,7 +498,7 @@ def pack_rows(w: PackedWeight, stream=None) -> torch.Tensor:
 def embed_rows_copy(w: PackedWeight, rows: torch.Tensor, ids: torch.Tensor, scale: float | None = None,
                     out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """embed_rows, reading the rows from `rows` = pack_rows(w) (the same values)."""
-    T, out, sbits = _embed_args(w, ids, scale, out)
+    T, out, sbits = _embed_args(w, ids, scale, out, stream)
     if not rows.is_cuda or rows.dtype != torch.uint8 or rows.numel() < rows_bytes(w.bits, w.group, w.N, w.K):
         raise ValueError("rows must be the uint8 CUDA copy made by pack_rows(w)")
     cw = w.cstruct()
@@ -623,7 +670,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
         raise ValueError("q must be [tokens, query heads, dim]")
     T = shape[0]
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=cache.device)
+        out = _empty(shape, _BF16, cache.device, stream)
     sq, sk, sv, so, sp = q.stride(), k.stride(), v.stride(), out.stride(), positions.stride()
     if not (shape[2] == dim and out.shape == shape and kshape == (T, cache.heads, dim) == v.shape
             and q.dtype is k.dtype is v.dtype is out.dtype is _BF16 and sq[2] == sk[2] == sv[2] == so[2] == 1
@@ -676,7 +723,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     if not -1 << 31 <= window < 1 << 31:         # the ABI's int; ctypes would drop the upper bits
         raise ValueError("window must fit 32 bits")
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=cache.device)
+        out = _empty(shape, _BF16, cache.device, stream)
     sq, so, st, tshape = q.stride(), out.stride(), table.stride(), table.shape
     if not (d == dim and out.shape == shape and q.dtype is out.dtype is _BF16 and sq[-1] == so[-1] == 1
             and q.get_device() == out.get_device() == table.get_device() == lens.get_device() == dev
@@ -689,7 +736,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
                          f"or None, all on {cache.device}")
     sp = _stream_ptr(stream, dev)
     buf = (workspace or default_workspace(dev, sp)).get(
-        cache._ws.get((tokens, heads)) or paged_attention_workspace_bytes(cache, tokens, heads))
+        cache._ws.get((tokens, heads)) or paged_attention_workspace_bytes(cache, tokens, heads), stream)
     _check((_lib or lib()).affqmm_paged_attention(
         cache._ref, _LANES(q.data_ptr(), sq[0], sq[-3], sq[-2]), _LANES(out.data_ptr(), so[0], so[-3], so[-2]),
         lse.data_ptr() if lse is not None else None, batch, tokens, heads, table.data_ptr(), st[0], tshape[1],
