@@ -24,10 +24,11 @@ namespace affqmm {
 namespace {
 
 constexpr int PL_THREADS = 1024;
-constexpr uint32_t PL_MOST = (1u << 30) - 1;   // sums saturate here: no pool and no capacity reaches it
+constexpr uint32_t PL_LIMIT = 0x7fffffffu;      // sums saturate here: beyond every pool (below 2^30) and capacity (up to 2^30)
 constexpr uint32_t PL_SERVED = 1u << 31, PL_FINISHED = 1u << 30;
+constexpr uint32_t PL_PAGE = PL_FINISHED - 1;   // and below the flags, a page's place among the pages taken or given back
 
-__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, PL_MOST); }
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, PL_LIMIT); }
 
 // Exclusive prefix sums of two values over the block's threads (saturating, so
 // the order of the additions does not matter), and their totals.
@@ -68,7 +69,7 @@ __device__ __forceinline__ Ask ask_of(const PlanParams& p, int i) {
     // a length that no table row can hold, or a negative count: the request is left alone
     a.bad = len < 0 || (int64_t)len > ((int64_t)p.wide << p.page_shift) || (!a.done && fresh < 0);
     a.len = a.bad ? 0u : (uint32_t)len;
-    a.fresh = (a.bad || a.done) ? 0u : min((uint32_t)fresh, PL_MOST);
+    a.fresh = (a.bad || a.done) ? 0u : (uint32_t)fresh;
     return a;
 }
 
@@ -140,9 +141,9 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
         const bool served = fits[k] && (need[k] == 0 || need_at <= free);
         if (fits[k] && !served) bits |= 1u;
         if (served && need[k]) got = need_at;
-        uint32_t word = served ? (before | PL_SERVED) : before;
+        uint32_t word = served ? (before | PL_SERVED) : 0u;   // before <= free, below 2^30
         if (a.done) {
-            word = back_at | PL_FINISHED;
+            word = (back_at & PL_PAGE) | PL_FINISHED;         // used where all pages given back fit the pool
             back_at = sat_add(back_at, (a.len + page_mask) >> p.page_shift);
         }
         if (i0 + k < p.batch) {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
                     int32_t* entry = p.table + (int64_t)r * p.table_stride + pg;
                     if (look || pg != have_pg) {
                         have_pg = pg;
-                        uint32_t x = head + (word & PL_MOST) + (pg - held);
+                        uint32_t x = head + (word & PL_PAGE) + (pg - held);
                         if (x >= pool) x -= pool;
                         page = pg >= held ? p.ring[x] : *entry;
                     }
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(PlanParams p) {
 #pragma unroll
                 for (int k = 0; k < GO; ++k)
                     if (j0 + 32 * k < held) {
-                        uint32_t x = head + free + (word & PL_MOST) + j0 + 32 * k;
+                        uint32_t x = head + free + (word & PL_PAGE) + j0 + 32 * k;
                         if (x >= pool) x -= pool;
                         if (x >= pool) x -= pool;
                         p.ring[x] = page[k];

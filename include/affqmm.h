@@ -409,9 +409,10 @@ typedef struct {
 
 /* What affqmm_paged_plan writes, all device memory.
  *   starts      int32 [batch + 1]: first token of each request in the step,
- *               and the number of tokens
+ *               and the number of tokens (2^31 - 1 where it would be more)
  *   lens        int32 [batch]: tokens in the cache after the step
  *   ring_state  int32 [2]: the ring's head and count after the step
+ *   capacity    tokens that the step can hold, up to 2^30
  *   slots       int32 [capacity], 16-byte aligned: each token's slot, -1 where
  *               it has none
  *   positions   int32 [capacity], 16-byte aligned: each token's place in its

@@ -99,6 +99,24 @@ def test_counts_that_cannot_be():
     assert int(step.status[0]) == 6 and bool((step.slots == -1).all()) and np.array_equal(step.lens.cpu().numpy(), sc["lens"])
 
 
+@pytest.mark.parametrize("capacity", [2 ** 30, 2 ** 30 - 1])
+def test_sums_beyond_the_largest_capacity(capacity):
+    """More tokens than 2^30 in a step that could hold 2^30: the request that lies beyond is not served."""
+    page, wide = 1 << 16, 1 << 14
+    pool = wide + 7
+    table = torch.full((3, wide), -1, dtype=torch.int32, device="cuda")
+    ring = torch.arange(pool, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    fresh = torch.tensor([capacity - 3, 10, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    step = api.PagedStep.empty(3, capacity)
+    api.paged_plan(lens, fresh, None, table, ring, torch.tensor([5, pool], dtype=torch.int32, device="cuda"), page, out=step)
+    assert int(step.status[0]) == 4 + 2 and step.lens.tolist() == [capacity - 3, 0, 0]
+    assert step.starts[:3].tolist() == [0, capacity - 3, capacity + 7]
+    assert step.ring_state.tolist() == [(5 + wide) % pool, 7]
+    assert step.slots[-5:].tolist() == [(4 + wide) % pool * page + page - 5 - (2 ** 30 - capacity), (4 + wide) % pool * page + page - 4 - (2 ** 30 - capacity), -1, -1, -1]
+    assert step.positions[-4:].tolist() == [capacity - 4, 0, 1, 2] and step.requests[-4:].tolist() == [0, 1, 1, 1]
+
+
 def test_more_pages_back_than_the_ring_holds():
     rng = np.random.default_rng(6)
     sc = scene(rng, 10, 16, 4, 4, most=4)
