@@ -434,7 +434,7 @@ def workspace_status(buf: torch.Tensor, stream=None) -> int:
 
 
 def test_fault_wait(cycles: int) -> None:
-    """Test hook: while cycles > 0, decode launches (M <= 16) first wait, at
+    """Test hook: while cycles > 0, decode (M <= 16) and attention launches first wait, at
     most `cycles` SM clock cycles, on a barrier nothing completes, so the
     bounded wait runs out and the workspace status reports a timeout."""
     _check(lib().affqmm_test_fault_wait(int(cycles)), "affqmm_test_fault_wait")

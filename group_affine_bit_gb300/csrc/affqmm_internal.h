@@ -112,7 +112,7 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t
 // swizzle.  decode_allow_smem sets the kernels' shared-memory attributes and
 // reports how many decode CTAs one SM holds.
 cudaError_t decode_allow_smem(int* ctas_per_sm);
-// The decode launches' fault_wait test hook (affqmm_test_fault_wait).
+// The fault_wait test hook of the decode and attention launches (affqmm_test_fault_wait).
 int64_t decode_fault_wait();
 void decode_set_fault_wait(int64_t cycles);
 cudaError_t launch_decode(int bits, int group, const DecParams& p, const CUtensorMap& map, int grid, cudaStream_t st,

@@ -64,6 +64,8 @@ struct AttnParams {
     int32_t row_tiles;           // tiles of 8 NT (token, head) rows
     uint32_t m_group, m_row_tiles;   // ceil(2^32 / d) of the two
     float scale_log2;            // softmax scale times log2(e)
+    int64_t wait_limit;          // cycles after which a wait gives up
+    int32_t fault;               // test hook: the consumers wait on a barrier that nothing completes
     uint32_t* user_status;       // or null
     uint32_t* status;            // workspace: status word, merge counters, partial slots
     uint32_t* counters;

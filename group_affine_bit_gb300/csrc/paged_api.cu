@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "affqmm.h"
+#include "affqmm_async.cuh"
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
 
@@ -369,6 +370,9 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     p.row_tiles = (rows + shape.rows - 1) / shape.rows;
     p.m_group = reciprocal(p.group), p.m_row_tiles = reciprocal(p.row_tiles);
     p.scale_log2 = scale * 1.4426950408889634f;
+    const int64_t fault = decode_fault_wait();
+    p.fault = fault > 0;
+    p.wait_limit = fault > 0 ? fault : kWaitLimitCycles;
     p.user_status = status;
     uint8_t* base = static_cast<uint8_t*>(workspace);
     p.status = reinterpret_cast<uint32_t*>(base);

@@ -62,6 +62,12 @@
 // keeps it in registers if the others are in by then, as they mostly are;
 // else the last to count in joins.
 //
+// Failure.  Every wait on a barrier is bounded; one that gives up is reported in
+// the workspace's status word.  A consumer warp that gave up goes on through the
+// barriers it shares, with whatever shared memory holds, and frees no slot of
+// the ring, so that the producers give up too and wait for their copies; what
+// it had a part in is neither counted in nor written.
+//
 // Measured (GB300, device time): 64 requests of up to 32768 keys, dim 128, 4.47
 // GB: 656 us, the measured copy rate; one request of 262143 keys 165 us, 96 % of
 // it; 32 requests of up to 4096 keys, dim 256, 559 MB: 90-93 us, 89-91 %; e4m3,
@@ -226,6 +232,14 @@ __device__ __forceinline__ bool consumers_all(bool v) {
 }
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() { asm volatile("barrier.cta.sync 3, %0;" ::"n"(THREADS) : "memory"); }
+// Wait for the phase of parity `parity` of `bar` to complete; false if it has not within `limit` cycles.
+__device__ __forceinline__ bool mbar_wait_within(uint32_t bar, uint32_t parity, long long limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > limit) return false;
+    return true;
+}
 // 16-byte chunk `c` of row `row` of a tile: panels of PW bytes of every row,
 // swizzled as TMA swizzles rows of 128 (64) bytes, so that the eight rows that
 // one fragment load reads fall into eight bank groups.
@@ -326,10 +340,12 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     const uint32_t decided = counted + 16u;                      // whether the other parts of its unit are there
     auto joined = [&](int s) { return counted + 24u + 8u * s; };  // parts of other runs are in the group's share of the ring
     const uint32_t drained = counted + 40u;                      // the q warp has written every row
+    const uint32_t never = counted + 48u;                        // completed by nothing: the fault_wait test hook waits on it
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
     __shared__ float kscale[4], vscale[4];   // of each q buffer, of each key head of the unit
     __shared__ int found_b;
     __shared__ uint32_t last_flag, late_join, others_in;
+    __shared__ volatile uint32_t spoilt;     // a consumer gave up: what is stored from then on is not whole
 
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
@@ -347,7 +363,9 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
         mbar_init(decided, 1);
         for (int s = 0; s < C::NG; ++s) mbar_init(joined(s), W);
         mbar_init(drained, 1);
+        mbar_init(never, 1);
         fence_mbar_init();
+        spoilt = 0;
     }
     if (wid == PRODUCER && lane == 0) {
         prefetch_tmap(&k_map);
@@ -413,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     walk.left = (int)run_tiles;
     bool ok = true;                       // no bounded wait has given up; after one, no wait is made
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = mbar_wait(bar, parity);
+        if (ok) ok = mbar_wait_within(bar, parity, p.wait_limit);
     };
 
     if (wid == PRODUCER || wid == PRODUCER + 1) {
@@ -583,12 +601,13 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 const bool part = walk.t0 > 0 || walk.t1 < walk.s.tiles;
                 if (part && walk.left <= 0) break;          // the consumers end the run
                 wait(stored(i % C::QBUF), (i / C::QBUF - 1) & 1);
+                ok = __all_sync(~0u, ok && !spoilt);
                 if (!part) {
                     copy_rows(walk.b, walk.u, i % C::QBUF, lane, 32);
                     __syncwarp();
                 } else if (lane == 0) {
                     const Parts x = parts_of(walk.unit0, walk.s.tiles);
-                    late_join = count_part(p.counters + x.first) == (uint32_t)x.count - 1;
+                    late_join = ok && count_part(p.counters + x.first) == (uint32_t)x.count - 1;
                     mbar_arrive(counted);
                 }
                 if (walk.left <= 0) break;
@@ -637,8 +656,14 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     const float NINF = __int_as_float(0xff800000);
     auto advance = [&] {
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty(slot));
+        if (lane == 0 && ok) mbar_arrive(empty(slot));           // its copy is complete
         if (++slot == C::NS) slot = 0, phase ^= 1u;
+    };
+    auto arrive_stored = [&](int buf) {
+        ok = __all_sync(~0u, ok);
+        if (lane != 0) return;
+        if (!ok) spoilt = 1;
+        mbar_arrive(stored(buf));
     };
     auto clear = [&] {
 #pragma unroll
@@ -650,6 +675,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     };
     auto slot_of = [&](const Parts& x, int i) { return p.slots + (size_t)(2 * (x.first + i) + (i == 0 ? 1 : 0)) * C::SLOT_FLOATS + group * C::PART_FLOATS; };
     int join_round = 0;                      // of `joined`
+    if (p.fault) wait(never, 0);
 
     // this run's part of a unit, to its slot
     auto store_part = [&](bool first) {
@@ -690,7 +716,8 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll 1
         for (int c0 = 0; c0 < x.count; c0 += ROOM) {
             const int n = min(ROOM, x.count - c0), i0 = own && c0 == 0 ? 1 : 0;
-            if (lane == 0 && ok) {
+            if (!ok) break;
+            if (lane == 0) {
                 asm volatile("fence.proxy.async;" ::: "memory");   // others' stores, before the copies read them
                 uint32_t mine = 0;
 #pragma unroll 1
@@ -699,7 +726,9 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll 1
                 for (int i = i0 + cw; i < n; i += W) bulk_g2s(ring_u + group * SHARE + i * BYTES, slot_of(x, c0 + i), BYTES, joined(group));
             }
-            wait(joined(group), join_round++ & 1);
+            const uint32_t parity = join_round++ & 1;
+            wait(joined(group), parity);
+            if (!ok) mbar_wait(joined(group), parity);       // no copy is in flight when the CTA ends
             const float* parts = reinterpret_cast<const float*>(ring + group * SHARE);
             const float* stats = parts + C::STATS + 2 * row;
             float high = top;
@@ -739,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                         acc[mt][nt][3] = fmaf(w.y, a.w, acc[mt][nt][3]);
                     }
                 }
-            consumer_sync();                             // the ring, `weight` and `red` serve the next parts
+            ok = !consumer_any(!ok);                     // the ring, `weight` and `red` serve the next parts
         }
         weight[ct] = sum;
         if (p0 == 0) red[row] = top;
@@ -1141,8 +1170,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 store_part(false);
                 early = true;
                 early_b = b, early_u = u, early_scale = v_scale, early_parts = parts;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(stored(buf));
+                arrive_stored(buf);
                 continue;
             }
             if (part) {
@@ -1153,8 +1181,8 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 }
                 if (!direct) {
                     store_part(walk.t0 == 0);
-                    consumers_sync<C::CONSUMERS>();
-                    if (tid == 0) last_flag = count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
+                    ok = consumers_all<C::CONSUMERS>(ok);
+                    if (tid == 0) last_flag = ok && count_part(p.counters + parts.first) == (uint32_t)parts.count - 1;
                     consumers_sync<C::CONSUMERS>();
                     if (last_flag == 0) continue;
                 }
@@ -1163,15 +1191,14 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
         if (part) join(parts, direct);
         stage_out(v_scale, buf);
         if (!part) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(stored(buf));             // the q warp writes the rows
+            arrive_stored(buf);                                  // the q warp writes the rows
         } else {
-            consumers_sync<C::CONSUMERS>();
+            ok = consumers_all<C::CONSUMERS>(ok);
             copy_rows(b, u, buf, tid, C::CONSUMERS);
             consumers_sync<C::CONSUMERS>();                                // before the buffer is staged again
         }
     }
-    if (!ok && lane == 0) atomicOr(p.status, 1u);
+    if (!ok) atomicOr(p.status, 1u);
 }
 
 template <int DP, int NA, bool E4M3, bool LASTING, bool PAIR>

@@ -318,9 +318,11 @@ AFFQMM_API int affqmm_embed_rows_copy(const affqmm_weight* w, const void* rows, 
 AFFQMM_API int affqmm_workspace_status(void* workspace, void* stream);
 
 /* Test hook for the timeout path (no counterpart on the pages): while
- * `cycles` > 0, every decode launch (M <= 16) that this process makes
+ * `cycles` > 0, every decode launch (M <= 16) and every launch of
+ * affqmm_paged_attention that this process makes
  * afterwards first has its consumer warps wait, at most `cycles` SM clock
- * cycles, on a barrier that nothing completes.  The wait runs out; the launch
+ * cycles, on a barrier that nothing completes (and attention's other waits
+ * have the same limit).  The wait runs out; the launch
  * sets its workspace status word (affqmm_workspace_status then returns
  * AFFQMM_E_TIMEOUT), writes no output, waits for the copies it started and
  * exits.  0 restores normal launches.  Not for production use.
@@ -536,7 +538,8 @@ AFFQMM_API int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cac
  * A token that sees no key, or whose scores are all -infinity, gets zeros, and
  * lse -infinity.  What the cache holds outside the visible keys (NaN, say) does
  * not matter; the rest of a page with a visible key may be read.  A bounded wait
- * that gave up is reported by affqmm_workspace_status.  Sums are fp32; the
+ * that gave up is reported by affqmm_workspace_status; out and lse are then
+ * invalid, written in part or not at all.  Sums are fp32; the
  * probabilities keep 16 bits beside a bf16 cache; beside an e4m3 one 11 bits
  * down to 2^-27 of a row's largest, and smaller ones are off by 2^-38 of it at
  * most.  The same inputs give the same bits on a device.
