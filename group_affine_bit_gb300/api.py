@@ -156,6 +156,15 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _status_ptr(status: torch.Tensor | None, device_index: int) -> int | None:
+    """The address of a call's status word."""
+    if status is None:
+        return None
+    if status.get_device() != device_index or status.dtype not in (torch.int32, torch.uint32) or status.numel() < 1:
+        raise ValueError(f"status must be an int32 or uint32 tensor of one word on cuda:{device_index}")
+    return status.data_ptr()
+
+
 def _capture_id(stream_ptr: int) -> int:
     """Which capture a stream is in, 0 for none."""
     status, number = ctypes.c_int(0), ctypes.c_uint64(0)
@@ -475,7 +484,7 @@ def embed_rows(w: PackedWeight, ids: torch.Tensor, scale: float | None = None, o
     T, out, sbits = _embed_args(w, ids, scale, out, stream)
     cw = w.cstruct()
     _check(lib().affqmm_embed_rows(ctypes.byref(cw), ids.data_ptr(), T, 0 if scale is None else 1, sbits,
-                                   out.data_ptr(), status.data_ptr() if status is not None else None,
+                                   out.data_ptr(), _status_ptr(status, ids.get_device()),
                                    _stream_ptr(stream)), "affqmm_embed_rows")
     return out
 
@@ -504,7 +513,7 @@ def embed_rows_copy(w: PackedWeight, rows: torch.Tensor, ids: torch.Tensor, scal
     cw = w.cstruct()
     _check(lib().affqmm_embed_rows_copy(ctypes.byref(cw), rows.data_ptr(), ids.data_ptr(), T,
                                         0 if scale is None else 1, sbits, out.data_ptr(),
-                                        status.data_ptr() if status is not None else None, _stream_ptr(stream)),
+                                        _status_ptr(status, ids.get_device()), _stream_ptr(stream)),
            "affqmm_embed_rows_copy")
     return out
 
@@ -687,7 +696,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     _check((_lib or lib()).affqmm_rope_append(
         cache._ref, rope.cstruct(axes), _ROWS(q.data_ptr(), sq[0], sq[1]), _ROWS(k.data_ptr(), sk[0], sk[1]),
         _ROWS(v.data_ptr(), sv[0], sv[1]), _ROWS(out.data_ptr(), so[0], so[1]), T, shape[1], positions.data_ptr(),
-        sp[0] if axes > 1 else 0, slots.data_ptr(), status.data_ptr() if status is not None else None,
+        sp[0] if axes > 1 else 0, slots.data_ptr(), _status_ptr(status, dev),
         _stream_ptr(stream, dev)), "affqmm_rope_append")
     return out
 
@@ -741,5 +750,5 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
         cache._ref, _LANES(q.data_ptr(), sq[0], sq[-3], sq[-2]), _LANES(out.data_ptr(), so[0], so[-3], so[-2]),
         lse.data_ptr() if lse is not None else None, batch, tokens, heads, table.data_ptr(), st[0], tshape[1],
         lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
-        status.data_ptr() if status is not None else None, buf.data_ptr(), buf.numel(), sp), "affqmm_paged_attention")
+        _status_ptr(status, dev), buf.data_ptr(), buf.numel(), sp), "affqmm_paged_attention")
     return out

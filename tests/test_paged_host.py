@@ -110,6 +110,13 @@ def test_the_binding_refuses_host_tensors():
         api.PagedStep(i, i, i, i, i, i, i)
 
 
+def test_a_status_word_must_be_on_the_calls_device():
+    assert api._status_ptr(None, 0) is None
+    for t in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            api._status_ptr(t, 0)
+
+
 def test_rope_turns_are_the_frequencies_fractions():
     f = paged_ref.turns_of(64) + [0.0, 2 * math.pi, 7.5]
     got = [x % (1 << 64) for x in api.rope_turns(f, "cpu").tolist()]
