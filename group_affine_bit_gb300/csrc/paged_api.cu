@@ -197,6 +197,12 @@ bool lasting_tiles(const affqmm_kv_cache* c, int64_t batch, int64_t keys, int sm
     return batch * c->heads * ((keys + 127) / 128) >= (int64_t)8 * 2 * sms;
 }
 
+// Tiles of all units, with two more for each: keys are counted from a multiple of a tile on, and a unit's end counts
+// as one (paged_attn.cuh).
+int64_t count_tiles(const AttnShape& s, int64_t batch, int heads, int rows, int64_t keys) {
+    return batch * heads * ((rows + s.rows - 1) / s.rows) * ((keys + s.keys - 1) / s.keys + 2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -329,12 +335,14 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     if (!aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(status, 4)) return AFFQMM_E_ALIGN;
     for (const affqmm_lanes* r : {q, out})
         if ((rc = check_rows(r->p, r->batch_stride, r->token_stride, r->head_stride))) return rc;
-    int sms = 0;
-    if ((rc = device_sms(&sms))) return rc;
     const int group = heads_q / cache->heads, rows = tokens * group;
     int64_t keys = wide * cache->page;       // that a request can have, and a window sees
     if (window >= keys) window = 0;          // it hides nothing (and the kernel's sums of lengths and windows stay within 32 bits)
     if (window > 0 && keys > (int64_t)window + tokens) keys = (int64_t)window + tokens;
+    // so many tiles are always lasting ones
+    if (count_tiles(attn_shape(cache, rows, true, false), batch, cache->heads, rows, keys) >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
     const bool lasting = lasting_tiles(cache, batch, keys, sms);
     const bool pair = lasting && pairable(cache, rows);
     const AttnShape shape = attn_shape(cache, rows, lasting, pair);
@@ -379,9 +387,7 @@ int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, 
     p.counters = reinterpret_cast<uint32_t*>(base + kStatusBytes);
     p.slots = reinterpret_cast<float*>(base + kSlotsOffset);
     // one CTA for each that the SMs hold, or for each tile that the tables have room for
-    keys += shape.keys;                      // counted from a multiple of a tile on
-    const int64_t tiles = batch * cache->heads * p.row_tiles * ((keys + shape.keys - 1) / shape.keys + 1);
-    if (tiles >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
+    const int64_t tiles = count_tiles(shape, batch, cache->heads, rows, keys);
     const int64_t most = (int64_t)sms * shape.ctas_per_sm;
     const int grid = (int)(tiles < most ? tiles : most);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -525,8 +525,12 @@ AFFQMM_API int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cac
  *             h * group + group - 1 (group = heads_q / cache heads) read key
  *             head h
  *   lse       device, fp32 [batch, tokens, heads_q] contiguous, or NULL
- *   table     device, int32 [batch, wide], rows table_stride apart; batch x key
- *             heads x wide x page below 2^37
+ *   table     device, int32 [batch, wide], rows table_stride apart; wide x page
+ *             below 2^31 - 1024, and batch x key heads x R x (K + 2) below 2^31:
+ *             R = tokens x group / 64 row tiles (at dim above 128 / 32, above 256
+ *             / 16), K = wide x page / 128 tiles of keys (/ 64 where a padded
+ *             head has more than 256 bytes; of window + tokens keys where that is
+ *             less), both rounded up
  *   lens      device, int32 [batch]: tokens in the cache, the step's own
  *             included
  *   scale     of the scores; finite

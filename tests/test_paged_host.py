@@ -70,6 +70,21 @@ def test_attention_refusals(L):
     assert name(L.affqmm_paged_attention_workspace_bytes(ctypes.byref(cache()), 1, 9, ctypes.byref(n))) == "AFFQMM_E_SHAPE"
 
 
+def test_the_most_tiles_of_a_call(L):
+    """Below the documented bound a call gets as far as the device or the workspace; at it, it is refused."""
+    def edge(batch, c, **kw):
+        return attend(L, c, batch=batch, **kw) == "AFFQMM_E_SHAPE"
+
+    c = cache(pages=1 << 26)                             # 2 key heads x (2^30 / 128 + 2) tiles
+    big = dict(wide=1 << 26, stride=0)
+    assert not edge(127, c, **big) and edge(128, c, **big)
+    wide = cache(pages=1 << 16, heads=8, dim=512, ps=65536, ts=4096, hs=512)
+    rows = dict(wide=1 << 16, stride=0, hq=64, tokens=64)    # 8 x 32 row tiles x (2^20 / 64 + 2)
+    assert not edge(511, wide, **rows) and edge(512, wide, **rows)
+    rows["window"] = 64                                  # 128 keys that a window sees: two tiles and two more
+    assert not edge(16384, wide, **rows)
+
+
 def test_append_refusals(L):
     assert append(L, None) == "AFFQMM_E_NULL"
     R = api.CRope
