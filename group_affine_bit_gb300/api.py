@@ -534,6 +534,17 @@ def _check_ints(t: torch.Tensor, name: str, shape: tuple, device=None, dtype=tor
                          + (f" on {device}" if device is not None else ""))
 
 
+def _unstepped(rc: int, *rows: torch.Tensor):
+    """After a call was refused for a misaligned stride: its tensors with stride 0 for the axes of one, which are never
+    stepped along and whose torch strides may be anything; None if that changes nothing."""
+    if STATUS_NAMES.get(rc) != "AFFQMM_E_ALIGN":
+        return None
+    plain = [[s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape)] + [1] for t in rows]
+    if all(list(t.stride()) == p for t, p in zip(rows, plain)):
+        return None
+    return [t.as_strided(t.shape, p) for t, p in zip(rows, plain)]
+
+
 class KVCache:
     """A pool of pages of keys and values: k and v [pages, page, heads, dim],
     bf16 or float8_e4m3fn, with the values of a head contiguous and the other
@@ -669,9 +680,9 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
                 stream=None) -> torch.Tensor:
     """affqmm_rope_append: rotary positions on q and k, and k and v written to
     their slots of the cache.  q [tokens, query heads, dim], k and v [tokens,
-    cache heads, dim], bf16, of any token and head strides (views of the stacked
-    projection's output serve); positions int32 [tokens] or [axes, tokens];
-    slots int32 [tokens], -1 for a token that is not kept.  Returns q turned,
+    cache heads, dim], bf16, token and head strides multiples of 8 (views of the
+    stacked projection's output serve); positions int32 [tokens] or [axes,
+    tokens]; slots int32 [tokens], -1 for a token that is not kept.  Returns q turned,
     in `out` (which may be q)."""
     dev, dim = cache._dev, cache.dim
     shape, kshape, pshape = q.shape, k.shape, positions.shape
@@ -693,11 +704,16 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     if T == 0:
         return out
     axes = pshape[0] if len(pshape) == 2 else 1
-    _check((_lib or lib()).affqmm_rope_append(
+    rc = (_lib or lib()).affqmm_rope_append(
         cache._ref, rope.cstruct(axes), _ROWS(q.data_ptr(), sq[0], sq[1]), _ROWS(k.data_ptr(), sk[0], sk[1]),
         _ROWS(v.data_ptr(), sv[0], sv[1]), _ROWS(out.data_ptr(), so[0], so[1]), T, shape[1], positions.data_ptr(),
         sp[0] if axes > 1 else 0, slots.data_ptr(), _status_ptr(status, dev),
-        _stream_ptr(stream, dev)), "affqmm_rope_append")
+        _stream_ptr(stream, dev))
+    if rc:
+        rows = _unstepped(rc, q, k, v, out)
+        if rows is None:
+            raise AffqmmError(rc, "affqmm_rope_append")
+        rope_append(*rows[:3], positions, slots, rope, cache, rows[3], status, stream)
     return out
 
 
@@ -717,7 +733,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
                     status: torch.Tensor | None = None, workspace: Workspace | None = None, stream=None) -> torch.Tensor:
     """affqmm_paged_attention: each request's newest tokens against its pages.
     q bf16 [batch, query heads, dim] (one new token) or [batch, tokens, query
-    heads, dim], any strides; table int32 [batch, wide]; lens int32 [batch], the
+    heads, dim], strides multiples of 8; table int32 [batch, wide]; lens int32 [batch], the
     step's own tokens included; scale defaults to dim ** -0.5; window > 0 keeps
     the last `window` keys of each token.  `lse` (float32, q's shape without its
     last axis) gets the log of each row's sum of exponentials.  Returns `out`,
@@ -746,9 +762,14 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     sp = _stream_ptr(stream, dev)
     buf = (workspace or default_workspace(dev, sp)).get(
         cache._ws.get((tokens, heads)) or paged_attention_workspace_bytes(cache, tokens, heads), stream)
-    _check((_lib or lib()).affqmm_paged_attention(
+    rc = (_lib or lib()).affqmm_paged_attention(
         cache._ref, _LANES(q.data_ptr(), sq[0], sq[-3], sq[-2]), _LANES(out.data_ptr(), so[0], so[-3], so[-2]),
         lse.data_ptr() if lse is not None else None, batch, tokens, heads, table.data_ptr(), st[0], tshape[1],
         lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
-        _status_ptr(status, dev), buf.data_ptr(), buf.numel(), sp), "affqmm_paged_attention")
+        _status_ptr(status, dev), buf.data_ptr(), buf.numel(), sp)
+    if rc:
+        lanes = _unstepped(rc, q, out)
+        if lanes is None:
+            raise AffqmmError(rc, "affqmm_paged_attention")
+        paged_attention(lanes[0], cache, table, lens, scale, window, lanes[1], lse, status, workspace, stream)
     return out

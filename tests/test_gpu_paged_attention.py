@@ -280,6 +280,24 @@ def test_views_streams_and_one_token_shape():
     assert bool((big[:, :, :64] == 5).all()) and bool((big[:, :, 192:] == 5).all())
 
 
+def test_axes_of_one_have_any_stride():
+    s = scene([100], 2, 1, 64, 16, seed=20)
+    want, _, _ = attend(s)
+    cache, table, lens = api.KVCache(s["k"].cuda(), s["v"].cuda()), s["table"].cuda(), s["lens"].cuda()
+    rows = torch.zeros(3, 2 * 64 + 3, dtype=torch.bfloat16, device="cuda")
+    q = rows.as_strided((3, 2, 64), (131, 64, 1))[:1]     # the first of rows whose pitch is odd
+    q.copy_(s["q"][:, 0].cuda())
+    assert q.stride(0) % 8 != 0
+    assert torch.equal(api.paged_attention(q, cache, table, lens).cpu(), want[:, 0])
+    flat = s["q"][0, 0].cuda()
+    q4 = flat.as_strided((1, 1, 2, 64), (3, 5, 64, 1))
+    assert torch.equal(api.paged_attention(q4, cache, table, lens, out=torch.empty_like(flat).as_strided((1, 1, 2, 64), (7, 1, 64, 1))).cpu(), want)
+    rope, i = api.Rope(api.rope_turns([0.5] * 32)), torch.tensor([3], dtype=torch.int32, device="cuda")
+    plain = api.rope_append(q.contiguous(), q[:, :1].contiguous(), q[:, :1].contiguous(), i, i, rope, cache)
+    k1 = flat.as_strided((1, 1, 64), (9, 11, 1))
+    assert torch.equal(api.rope_append(q, k1, k1, i, i, rope, cache), plain)
+
+
 def test_offsets_beyond_32_bits():
     """A pool whose last pages begin beyond 2^31 elements (and 2^32 bytes)."""
     pages, page, hk, dim = (1 << 31) // (64 * 2 * 256) + 40, 64, 2, 256
