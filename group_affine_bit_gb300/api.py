@@ -586,7 +586,9 @@ class KVCache:
 class Rope:
     """Rotary positions: `turns` int64 [rotary / 2], pair i's turns a position
     as a 64-bit fraction of a turn (rope_turns makes them), and `axis` uint8
-    [rotary / 2] or None, the axis of positions by which each pair turns.
+    [rotary / 2] or None, the axis of positions by which each pair turns (one
+    beyond the positions' axes: the last, so that with [tokens] positions a
+    rope of several axes turns every pair by them).
     neighbour=False pairs values i and i + rotary / 2, True 2i and 2i + 1."""
 
     def __init__(self, turns: torch.Tensor, axis: torch.Tensor | None = None, neighbour: bool = False):

@@ -464,7 +464,8 @@ AFFQMM_API int affqmm_paged_plan(int64_t batch, const int32_t* lens, const int32
  *             dropped): floor(2^64 frac(frequency_i / 2 pi)); 0 leaves a pair
  *             as it is
  *   axis      device, uint8 [rotary / 2] or NULL (0): the axis by whose
- *             position pair i turns
+ *             position pair i turns; one beyond `axes` counts as the last, so
+ *             that with one row of positions (text) every pair turns by it
  *   rotary    values of a head that turn: even, up to the head's dim; the rest
  *             is left as it is
  *   neighbour 0: pair i is values i and i + rotary / 2; 1: values 2i, 2i + 1

@@ -122,6 +122,23 @@ def test_positions_up_to_the_last_integer():
     run_and_check(64, 4, 2, 128, 128, 1, False, 16, "bf16", seed=5, high=2 ** 31 - 1)
 
 
+def test_an_axis_beyond_the_positions_is_the_last():
+    """A rope of three axes with the positions of text, and with two axes."""
+    g = gen(7)
+    q = torch.randn(9, 4, 64, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(9, 2, 64, generator=g).bfloat16().cuda() for _ in "kv")
+    pos = torch.randint(0, 5000, (2, 9), generator=g, dtype=torch.int32).cuda()
+    slots, turns = torch.arange(9, dtype=torch.int32, device="cuda"), api.rope_turns(paged_ref.turns_of(64))
+    axis = torch.tensor([i % 3 for i in range(32)], dtype=torch.uint8, device="cuda")
+    for positions, same in ((pos[0], None), (pos[:1], None), (pos, axis.clamp(max=1))):
+        got, want = (api.KVCache.empty(1, 16, 2, 64) for _ in "ab")
+        for c in (got, want):
+            c.k.zero_(), c.v.zero_()
+        a = api.rope_append(q, k, v, positions, slots, api.Rope(turns, axis), got)
+        b = api.rope_append(q, k, v, positions, slots, api.Rope(turns, same), want)
+        assert torch.equal(a, b) and torch.equal(got.k, want.k) and torch.equal(got.v, want.v)
+
+
 def test_a_frequency_of_zero_turns_nothing():
     g = gen(6)
     q = torch.randn(7, 4, 64, generator=g).bfloat16().cuda()
