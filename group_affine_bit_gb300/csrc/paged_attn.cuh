@@ -69,10 +69,10 @@
 // it had a part in is neither counted in nor written.
 //
 // Measured (GB300, device time): 64 requests of up to 32768 keys, dim 128, 4.47
-// GB: 656 us, the measured copy rate; one request of 262143 keys 165 us, 96 % of
-// it; 32 requests of up to 4096 keys, dim 256, 559 MB: 90-93 us, 89-91 %; e4m3,
-// 659 MB: 108 us, 90 %; one request of 577 keys 8.6 us, of which 0.7 is the
-// launch, 3 lead to the first tile and 4 are the join of its parts.
+// GB: 657 us, the measured copy rate; one request of 262143 keys 165 us, 96 % of
+// it; 32 requests of up to 4096 keys, dim 256, 559 MB: 93 us, 89 %; e4m3, 659
+// MB: 109 us, 89 %; one request of 577 keys 8.7 us, of which 0.7 is the launch, 3
+// lead to the first tile and 4 are the join of its parts.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
