@@ -158,8 +158,8 @@ def _need(top, kv):
     """The scale of a block whose largest magnitude is `top`."""
     if kv == "int8":
         return (top / 127).clamp(LEAST, MOST)
-    m, e = torch.frexp(top / 448)
-    return torch.ldexp(torch.ones_like(top), e - (m == 0.5).int()).clamp(LEAST, MOST)
+    m, e = torch.frexp((top / 448).clamp(LEAST, MOST))
+    return torch.ldexp(torch.ones_like(top), e - (m == 0.5).int())
 
 
 def _coded(x, kv):
@@ -489,6 +489,7 @@ def _append_exact(case, s):
             if kv == "e4m3":
                 need = torch.exp2(torch.ceil(torch.log2(top / 448)))
                 need = torch.where(need / 2 * 448 >= top, need / 2, need)  # a logarithm just above a whole number
+            need = need.clamp(LEAST, MOST)
             old = torch.zeros_like(need) if 0 in place else scales[p, i]
             scale = torch.maximum(old, need)
             if 0 not in place:
