@@ -52,6 +52,12 @@ class CCache(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
+class CBlockCache(ctypes.Structure):
+    _fields_ = [("kv", CCache), ("block", ctypes.c_int32), ("s_page_stride", ctypes.c_int64),
+                ("s_block_stride", ctypes.c_int64), ("s_head_stride", ctypes.c_int64), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
+
+
 class CStep(ctypes.Structure):
     _fields_ = [("capacity", ctypes.c_int64), ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
                 ("ring_state", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
@@ -110,6 +116,12 @@ def lib() -> ctypes.CDLL:
             "affqmm_paged_attention_workspace_bytes": (i32, [vp, i32, i32, szp]),
             "affqmm_paged_attention": (i32, [vp, vp, vp, vp, i64, i32, i32, vp, i64, i64, vp, ctypes.c_float, i32, vp, vp,
                                              ctypes.c_size_t, vp]),
+            "affqmm_block_append": (i32, [vp, vp, vp, vp, vp, vp, i64, i32, vp, i64, vp, vp, vp]),
+            "affqmm_block_attention_workspace_bytes": (i32, [vp, i32, i32, szp]),
+            "affqmm_block_attention": (i32, [vp, vp, vp, vp, i64, i32, i32, vp, i64, i64, vp, ctypes.c_float, i32, vp, vp,
+                                             ctypes.c_size_t, vp]),
+            "affqmm_paged_read": (i32, [vp, vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp]),
+            "affqmm_block_read": (i32, [vp, vp, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -521,7 +533,9 @@ def embed_rows_copy(w: PackedWeight, rows: torch.Tensor, ids: torch.Tensor, scal
 # ----------------------------------------------------------------------------- the paged key-value cache
 PAGED_MAX_BATCH = 16384              # requests of a call
 PAGED_MAX_TOKENS = 64                # query tokens of a request
+BLOCK_MAX = 128                      # tokens of a block of a BlockCache
 _KV_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+_BLOCK_TYPES = {torch.float8_e4m3fn: 1, torch.int8: 2}
 _BF16, _I32, _F32, _BOOL = torch.bfloat16, torch.int32, torch.float32, torch.bool
 # affqmm_rows and affqmm_lanes as bytes: a small part of what a ctypes structure costs a call
 _ROWS, _LANES = struct.Struct("Pqq").pack, struct.Struct("Pqqq").pack
@@ -576,11 +590,57 @@ class KVCache:
         self._ref = ctypes.addressof(self._c)
         self._ws: dict = {}          # (tokens, query heads) -> workspace bytes
 
+    _append, _attention, _read = "affqmm_rope_append", "affqmm_paged_attention", "affqmm_paged_read"
+
     @classmethod
     def empty(cls, pages: int, page: int, heads: int, dim: int, dtype=torch.bfloat16, device="cuda", k_scale=None,
               v_scale=None) -> "KVCache":
         k, v = (torch.empty(pages, page, heads, dim, dtype=dtype, device=device) for _ in "kv")
         return cls(k, v, k_scale, v_scale)
+
+
+class BlockCache:
+    """A pool of pages whose 8-bit values have a scale for each block of tokens
+    and key head, made as the cache is written: k and v [pages, page, heads,
+    dim], int8 or float8_e4m3fn, as a KVCache's; k_scale and v_scale float32
+    [pages, blocks of a page, heads], any strides that do not overlap.  A block
+    has page / blocks tokens, a power of two up to BLOCK_MAX.  rope_append,
+    paged_attention and paged_read take it where they take a KVCache; in an
+    append, the tokens of one block come one after another.  The object keeps
+    the tensors' addresses: build it once per pool."""
+
+    _append, _attention, _read = "affqmm_block_append", "affqmm_block_attention", "affqmm_block_read"
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must be [pages, page, heads, dim] tensors of one type, shape, stride and device")
+        if k.dtype not in _BLOCK_TYPES or not k.is_cuda:
+            raise ValueError("k and v must be CUDA int8 or float8_e4m3fn tensors")
+        if k.stride(3) != 1 and k.shape[3] > 1:
+            raise ValueError("the values of a head must be contiguous")
+        self.pages, self.page, self.heads, self.dim = k.shape
+        blocks = k_scale.shape[1] if k_scale.dim() == 3 else 0
+        if blocks < 1 or self.page % blocks or k_scale.stride() != v_scale.stride():
+            raise ValueError("k_scale and v_scale must be [pages, blocks of a page, heads] tensors of one stride")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _check_ints(t, name, (self.pages, blocks, self.heads), k.device, torch.float32, contiguous=False)
+        self.k, self.v, self.k_scale, self.v_scale, self.block = k, v, k_scale, v_scale, self.page // blocks
+        self.device, self._dev = k.device, k.get_device()
+        ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
+        self._c = CBlockCache(CCache(_BLOCK_TYPES[k.dtype], self.page, self.heads, self.dim, self.pages, *k.stride()[:3],
+                                     ptr(k), ptr(v), None, None), self.block, *k_scale.stride(), ptr(k_scale), ptr(v_scale))
+        self._ref = ctypes.addressof(self._c)
+        self._ws: dict = {}          # (tokens, query heads) -> workspace bytes
+
+    @classmethod
+    def empty(cls, pages: int, page: int, heads: int, dim: int, dtype=torch.int8, block: int | None = None,
+              device="cuda") -> "BlockCache":
+        """A pool of pages in blocks of `block` tokens (None: 16, or a page's fewer)."""
+        block = min(page, 16) if block is None else block
+        if block < 1 or page % block:
+            raise ValueError("a block must divide a page")
+        k, v = (torch.empty(pages, page, heads, dim, dtype=dtype, device=device) for _ in "kv")
+        return cls(k, v, *(torch.zeros(pages, page // block, heads, device=device) for _ in "kv"))
 
 
 class Rope:
@@ -678,10 +738,10 @@ def paged_plan(lens: torch.Tensor, fresh: torch.Tensor, finished: torch.Tensor |
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
-                rope: Rope, cache: KVCache, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                rope: Rope, cache: KVCache | BlockCache, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
-    """affqmm_rope_append: rotary positions on q and k, and k and v written to
-    their slots of the cache.  q [tokens, query heads, dim], k and v [tokens,
+    """affqmm_rope_append, or affqmm_block_append for a BlockCache: rotary
+    positions on q and k, and k and v written to their slots of the cache.  q [tokens, query heads, dim], k and v [tokens,
     cache heads, dim], bf16, token and head strides multiples of 8 (views of the
     stacked projection's output serve); positions int32 [tokens] or [axes,
     tokens]; slots int32 [tokens], -1 for a token that is not kept.  Returns q turned,
@@ -706,7 +766,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     if T == 0:
         return out
     axes = pshape[0] if len(pshape) == 2 else 1
-    rc = (_lib or lib()).affqmm_rope_append(
+    rc = getattr(_lib or lib(), cache._append)(
         cache._ref, rope.cstruct(axes), _ROWS(q.data_ptr(), sq[0], sq[1]), _ROWS(k.data_ptr(), sk[0], sk[1]),
         _ROWS(v.data_ptr(), sv[0], sv[1]), _ROWS(out.data_ptr(), so[0], so[1]), T, shape[1], positions.data_ptr(),
         sp[0] if axes > 1 else 0, slots.data_ptr(), _status_ptr(status, dev),
@@ -714,26 +774,27 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     if rc:
         rows = _unstepped(rc, q, k, v, out)
         if rows is None:
-            raise AffqmmError(rc, "affqmm_rope_append")
+            raise AffqmmError(rc, cache._append)
         rope_append(*rows[:3], positions, slots, rope, cache, rows[3], status, stream)
     return out
 
 
-def paged_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> int:
+def paged_attention_workspace_bytes(cache: KVCache | BlockCache, tokens: int, heads: int) -> int:
     need = cache._ws.get((tokens, heads))
     if need is None:
         got = ctypes.c_size_t(0)
         with torch.cuda.device(cache.device):
-            _check(lib().affqmm_paged_attention_workspace_bytes(cache._ref, tokens, heads, ctypes.byref(got)),
-                   "affqmm_paged_attention_workspace_bytes")
+            name = cache._attention + "_workspace_bytes"
+            _check(getattr(lib(), name)(cache._ref, tokens, heads, ctypes.byref(got)), name)
         need = cache._ws[(tokens, heads)] = got.value
     return need
 
 
-def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+def paged_attention(q: torch.Tensor, cache: KVCache | BlockCache, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
                     window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     status: torch.Tensor | None = None, workspace: Workspace | None = None, stream=None) -> torch.Tensor:
-    """affqmm_paged_attention: each request's newest tokens against its pages.
+    """affqmm_paged_attention, or affqmm_block_attention for a BlockCache: each
+    request's newest tokens against its pages.
     q bf16 [batch, query heads, dim] (one new token) or [batch, tokens, query
     heads, dim], strides multiples of 8; table int32 [batch, wide]; lens int32 [batch], the
     step's own tokens included; scale defaults to dim ** -0.5; window > 0 keeps
@@ -764,7 +825,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     sp = _stream_ptr(stream, dev)
     buf = (workspace or default_workspace(dev, sp)).get(
         cache._ws.get((tokens, heads)) or paged_attention_workspace_bytes(cache, tokens, heads), stream)
-    rc = (_lib or lib()).affqmm_paged_attention(
+    rc = getattr(_lib or lib(), cache._attention)(
         cache._ref, _LANES(q.data_ptr(), sq[0], sq[-3], sq[-2]), _LANES(out.data_ptr(), so[0], so[-3], so[-2]),
         lse.data_ptr() if lse is not None else None, batch, tokens, heads, table.data_ptr(), st[0], tshape[1],
         lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
@@ -772,6 +833,43 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     if rc:
         lanes = _unstepped(rc, q, out)
         if lanes is None:
-            raise AffqmmError(rc, "affqmm_paged_attention")
+            raise AffqmmError(rc, cache._attention)
         paged_attention(lanes[0], cache, table, lens, scale, window, lanes[1], lse, status, workspace, stream)
     return out
+
+
+def paged_read(cache: KVCache | BlockCache, table: torch.Tensor, starts: torch.Tensor, first: torch.Tensor | None = None,
+               k: torch.Tensor | None = None, v: torch.Tensor | None = None, rows: int | None = None,
+               status: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """affqmm_paged_read, or affqmm_block_read for a BlockCache: tokens of the
+    requests as rows of bf16 again.  Row starts[b] + j of k and v [rows, cache
+    heads, dim] is token first[b] + j (first None: j) of request b, for j below
+    starts[b + 1] - starts[b]; rows behind the last are left as they are.  table
+    int32 [batch, wide], starts int32 [batch + 1], first int32 [batch]; k and v
+    as rope_append's, or made here, `rows` of them.  Returns k and v."""
+    dev, heads, dim = cache._dev, cache.heads, cache.dim
+    if (k is None) != (v is None) or (k is None) == (rows is None):
+        raise ValueError("paged_read wants k and v, or the number of rows to make them of")
+    if k is None:
+        k, v = (_empty((rows, heads, dim), _BF16, cache.device, stream) for _ in "kv")
+    shape, tshape = k.shape, table.shape
+    sk, sv, st = k.stride(), v.stride(), table.stride()
+    if not (len(shape) == 3 and shape[1] == heads and shape[2] == dim and v.shape == shape and k.dtype is v.dtype is _BF16
+            and sk[2] == sv[2] == 1 and len(tshape) == 2 and table.dtype is starts.dtype is _I32
+            and (st[1] == 1 or tshape[1] <= 1) and starts.shape == (tshape[0] + 1,) and starts.is_contiguous()
+            and k.get_device() == v.get_device() == table.get_device() == starts.get_device() == dev
+            and (first is None or (first.dtype is _I32 and first.shape == tshape[:1] and first.get_device() == dev
+                                   and first.is_contiguous()))):
+        raise ValueError(f"paged_read wants CUDA bf16 k and v [rows, {heads}, {dim}], the values of a head contiguous, int32 "
+                         f"table [batch, wide] with contiguous rows, starts [batch + 1] and first [batch] or None, all on "
+                         f"{cache.device}")
+    rc = getattr(_lib or lib(), cache._read)(
+        cache._ref, _ROWS(k.data_ptr(), sk[0], sk[1]), _ROWS(v.data_ptr(), sv[0], sv[1]), shape[0], tshape[0], table.data_ptr(),
+        st[0], tshape[1], starts.data_ptr(), first.data_ptr() if first is not None else None, _status_ptr(status, dev),
+        _stream_ptr(stream, dev))
+    if rc:
+        plain = _unstepped(rc, k, v)
+        if plain is None:
+            raise AffqmmError(rc, cache._read)
+        paged_read(cache, table, starts, first, *plain, None, status, stream)
+    return k, v

@@ -20,8 +20,10 @@ LIB = os.path.join(PKG, "libaffqmm.so")
 
 SOURCES = ["affqmm_api.cu", "plan.cu", "pack.cu", "decode.cu", "prompt.cu", "embed.cu", "hostio.cu",
            "paged_api.cu", "paged_plan.cu", "rope_append.cu", "paged_attn_64.cu", "paged_attn_128.cu",
-           "paged_attn_256.cu", "paged_attn_512.cu"]
-HEADERS = ["affqmm_format.cuh", "affqmm_internal.h", "affqmm_async.cuh", "affqmm_tc.cuh", "affqmm_paged.h", "paged_attn.cuh"]
+           "paged_attn_256.cu", "paged_attn_512.cu", "paged_attn_blocks_64.cu", "paged_attn_blocks_128.cu",
+           "paged_attn_blocks_256.cu", "paged_attn_blocks_512.cu", "block_append.cu", "paged_read.cu"]
+HEADERS = ["affqmm_format.cuh", "affqmm_internal.h", "affqmm_async.cuh", "affqmm_tc.cuh", "affqmm_paged.h", "paged_attn.cuh",
+           "rope_pieces.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -11,6 +11,10 @@
 
 namespace affqmm {
 
+// Between which the scale of a block lies, so that 2^(score + log2 of V's scale) and one over that scale stay within
+// fp32 whatever the blocks that a row sees.
+constexpr float kLeastScale = 0x1p-48f, kMostScale = 0x1p48f;
+
 // ---- paged_plan.cu
 struct PlanParams {
     const int32_t* lens;
@@ -47,6 +51,34 @@ struct RopeParams {
 };
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t st);
 
+// ---- block_append.cu
+struct BlockParams {
+    RopeParams rope;             // e4m3: the codes' type, else int8; no scales of heads
+    float *k_scales, *v_scales;
+    int64_t s_ps, s_bs, s_hs;    // page, block and head strides of the two, elements
+    int32_t block_shift;
+};
+cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st);
+
+// ---- paged_read.cu
+enum { READ_BF16, READ_E4M3, READ_E4M3_BLOCKS, READ_I8_BLOCKS };
+struct ReadParams {
+    const uint8_t *kc, *vc;
+    int64_t page_bytes, token_bytes, head_bytes, pages;
+    const float *k_scale, *v_scale;     // of heads, or null; or of blocks and heads
+    int64_t s_ps, s_bs, s_hs;
+    int32_t block_shift, page_shift, heads, dim;
+    uint16_t *k, *v;
+    int64_t k_ts, k_hs, v_ts, v_hs;
+    int64_t rows;
+    int32_t batch, wide;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t *starts, *first;
+    uint32_t* status;
+};
+cudaError_t launch_paged_read(const ReadParams& p, int kind, int sms, cudaStream_t st);
+
 // ---- paged_attn_*.cu (paged_attn.cuh)
 struct AttnParams {
     const uint16_t* q;
@@ -55,7 +87,10 @@ struct AttnParams {
     int64_t q_bs, q_ts, q_hs, o_bs, o_ts, o_hs;   // elements
     int64_t pages;
     int32_t axis1, axis2, axis3; // what the cache's tensor maps have as axes 1 .. 3: 0 token, 1 head, 2 page
-    const float *k_scale, *v_scale;
+    const float *k_scale, *v_scale;     // of each head, or null
+    const float *k_scales, *v_scales;   // of each block of tokens and head
+    int64_t s_ps, s_bs, s_hs;           // page, block and head strides of the two, elements
+    int32_t block_shift;
     const int32_t* table;
     int64_t table_stride;
     const int32_t* lens;
@@ -79,17 +114,22 @@ struct AttnShape {
     int keys = 0;                // and its keys
     size_t slot_floats = 0;
 };
-// DP: head dim padded to 64, 128, 256 or 512; rows: (token, head) rows that share a key head; lasting: the tables
-// have room for many tiles; pair: two key heads to a CTA.
-#define AFFQMM_ATTN_DECL(DP)                                                                            \
-    AttnShape attn_shape_##DP(bool e4m3, bool lasting, bool pair, int rows);                            \
-    cudaError_t attn_allow_smem_##DP();                                                                 \
-    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, \
-                                 const CUtensorMap& v, int grid, cudaStream_t st);
+// NAME: head dim padded to 64, 128, 256 or 512, of a cache with scales for each block after `blocks_`; bytes: e4m3 rather than
+// bf16, with blocks int8 rather than e4m3; rows: (token, head) rows that share a key head; lasting: the tables have room for
+// many tiles; pair: two key heads to a CTA.
+#define AFFQMM_ATTN_DECL(NAME)                                                                          \
+    AttnShape attn_shape_##NAME(bool bytes, bool lasting, bool pair, int rows);                         \
+    cudaError_t attn_allow_smem_##NAME();                                                               \
+    cudaError_t launch_attn_##NAME(bool bytes, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, \
+                                   const CUtensorMap& v, int grid, cudaStream_t st);
 AFFQMM_ATTN_DECL(64)
 AFFQMM_ATTN_DECL(128)
 AFFQMM_ATTN_DECL(256)
 AFFQMM_ATTN_DECL(512)
+AFFQMM_ATTN_DECL(blocks_64)
+AFFQMM_ATTN_DECL(blocks_128)
+AFFQMM_ATTN_DECL(blocks_256)
+AFFQMM_ATTN_DECL(blocks_512)
 #undef AFFQMM_ATTN_DECL
 
 // affqmm_api.cu: the current device's SM count (AFFQMM_E_DEVICE where it is no sm_103 GPU).

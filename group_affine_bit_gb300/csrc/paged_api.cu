@@ -52,11 +52,15 @@ Axes axes_of(const affqmm_kv_cache* c) {
     return a;
 }
 
-int check_cache(const affqmm_kv_cache* c, bool memory) {
+// Bytes of a stored value.
+int value_bytes(const affqmm_kv_cache* c) { return c->type == AFFQMM_KV_BF16 ? 2 : 1; }
+
+// `blocks`: with a scale for each block of tokens and head.
+int check_cache(const affqmm_kv_cache* c, bool memory, bool blocks = false) {
     if (!c) return AFFQMM_E_NULL;
-    if (c->type != AFFQMM_KV_BF16 && c->type != AFFQMM_KV_E4M3) return AFFQMM_E_ARG;
+    if (c->type != AFFQMM_KV_E4M3 && c->type != (blocks ? AFFQMM_KV_I8 : AFFQMM_KV_BF16)) return AFFQMM_E_ARG;
     if (page_shift_of(c->page) < 0) return AFFQMM_E_ARG;
-    if (c->type == AFFQMM_KV_BF16 && (c->k_scale || c->v_scale)) return AFFQMM_E_ARG;
+    if ((c->type != AFFQMM_KV_E4M3 || blocks) && (c->k_scale || c->v_scale)) return AFFQMM_E_ARG;
     if (c->heads < 1 || c->heads > 4096 || c->dim < 16 || c->dim > 512 || c->dim % 16) return AFFQMM_E_SHAPE;
     if (c->pages < 1 || c->pages >= kMost || c->pages * c->page >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
     const int64_t size[3] = {c->pages, c->page, c->heads}, stride[3] = {c->page_stride, c->token_stride, c->head_stride};
@@ -64,7 +68,7 @@ int check_cache(const affqmm_kv_cache* c, bool memory) {
         if (size[i] > 1 && (stride[i] < c->dim || stride[i] >= (int64_t)1 << 38)) return AFFQMM_E_SHAPE;
     if (!memory) return AFFQMM_OK;
     if (!c->k || !c->v) return AFFQMM_E_NULL;
-    const int64_t each = c->type == AFFQMM_KV_E4M3 ? 16 : 8;
+    const int64_t each = 16 / value_bytes(c);
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return AFFQMM_E_ALIGN;
     for (int i = 0; i < 3; ++i)
@@ -75,6 +79,38 @@ int check_cache(const affqmm_kv_cache* c, bool memory) {
     return AFFQMM_OK;
 }
 
+// The scales of a cache's blocks.
+struct Scales {
+    float *k, *v;
+    int64_t page_stride, block_stride, head_stride;   // 0 for an axis of one
+    int shift;                                        // of a block's tokens
+};
+int check_scales(const affqmm_block_cache* c, bool memory, Scales* s) {
+    const int shift = page_shift_of(c->block);
+    if (shift < 0 || c->block > AFFQMM_BLOCK_MAX || c->block > c->kv.page) return AFFQMM_E_ARG;
+    const int64_t size[3] = {c->kv.pages, c->kv.page >> shift, c->kv.heads};
+    int64_t stride[3] = {c->s_page_stride, c->s_block_stride, c->s_head_stride};
+    for (int i = 0; i < 3; ++i) {
+        if (size[i] == 1) stride[i] = 0;
+        else if (stride[i] < 1 || stride[i] >= (int64_t)1 << 38) return AFFQMM_E_SHAPE;
+    }
+    // no two scales in one place: of two axes, the one with the larger stride steps over the other
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j) {
+            const int in = stride[i] < stride[j] ? i : j, out = in == i ? j : i;
+            if (stride[in] && stride[out] < stride[in] * size[in]) return AFFQMM_E_SHAPE;
+        }
+    *s = {c->k_scales, c->v_scales, stride[0], stride[1], stride[2], shift};
+    if (!memory) return AFFQMM_OK;
+    if (!c->k_scales || !c->v_scales) return AFFQMM_E_NULL;
+    return aligned(c->k_scales, 4) && aligned(c->v_scales, 4) ? AFFQMM_OK : AFFQMM_E_ALIGN;
+}
+int check_blocks(const affqmm_block_cache* c, bool memory, Scales* s) {
+    if (!c) return AFFQMM_E_NULL;
+    const int rc = check_cache(&c->kv, memory, true);
+    return rc ? rc : check_scales(c, memory, s);
+}
+
 int check_rows(const void* p, int64_t s0, int64_t s1, int64_t s2) {
     if (!p) return AFFQMM_E_NULL;
     if (s0 < 0 || s1 < 0 || s2 < 0) return AFFQMM_E_SHAPE;
@@ -82,28 +118,36 @@ int check_rows(const void* p, int64_t s0, int64_t s1, int64_t s2) {
     return AFFQMM_OK;
 }
 
-// Shared-memory limits of the attention kernels, set once per device and head dim.
-std::once_flag g_once[kMaxDevices][4];
-bool g_ok[kMaxDevices][4];
+// The attention kernels of one padded head dim (64 << which), of caches without and with scales of blocks.
+struct Kernels {
+    AttnShape (*shape)(bool, bool, bool, int);
+    cudaError_t (*allow)();
+    cudaError_t (*launch)(bool, bool, bool, int, const AttnParams&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+};
+#define AFFQMM_ATTN_KERNELS(NAME) {attn_shape_##NAME, attn_allow_smem_##NAME, launch_attn_##NAME}
+const Kernels g_kernels[8] = {AFFQMM_ATTN_KERNELS(64),        AFFQMM_ATTN_KERNELS(128),        AFFQMM_ATTN_KERNELS(256),
+                              AFFQMM_ATTN_KERNELS(512),       AFFQMM_ATTN_KERNELS(blocks_64),  AFFQMM_ATTN_KERNELS(blocks_128),
+                              AFFQMM_ATTN_KERNELS(blocks_256), AFFQMM_ATTN_KERNELS(blocks_512)};
+#undef AFFQMM_ATTN_KERNELS
+
+// Their shared-memory limits, set once per device and set of kernels.
+std::once_flag g_once[kMaxDevices][8];
+bool g_ok[kMaxDevices][8];
 
 int allow_attn(int which) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return AFFQMM_E_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return AFFQMM_E_DEVICE;
     std::call_once(g_once[dev][which], [&] {
-        const cudaError_t e = which == 0   ? attn_allow_smem_64()
-                              : which == 1 ? attn_allow_smem_128()
-                              : which == 2 ? attn_allow_smem_256()
-                                           : attn_allow_smem_512();
-        g_ok[dev][which] = e == cudaSuccess;
+        g_ok[dev][which] = g_kernels[which].allow() == cudaSuccess;
     });
     return g_ok[dev][which] ? AFFQMM_OK : AFFQMM_E_CUDA;
 }
 
-// The kernels' padded head dim: 64 << this.  (e4m3 rows of 64 bytes cannot be
+// The kernels' padded head dim: 64 << this.  (8-bit rows of 64 bytes cannot be
 // TMA's destination one by one: pages of one token take the next.)
 int which_dim(const affqmm_kv_cache* c) {
-    if (c->dim <= 64 && c->type == AFFQMM_KV_E4M3 && c->page == 1) return 1;
+    if (c->dim <= 64 && value_bytes(c) == 1 && c->page == 1) return 1;
     return c->dim <= 64 ? 0 : c->dim <= 128 ? 1 : c->dim <= 256 ? 2 : 3;
 }
 
@@ -129,8 +173,7 @@ EncodeTiledFn encode_tiled() {
 int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, CUtensorMap* v, int32_t (&axis)[3]) {
     EncodeTiledFn enc = encode_tiled();
     if (!enc) return AFFQMM_E_CUDA;
-    const bool e4m3 = c->type == AFFQMM_KV_E4M3;
-    const int es = e4m3 ? 1 : 2, panel = padded * es < 128 ? padded * es : 128;
+    const int es = value_bytes(c), panel = padded * es < 128 ? padded * es : 128;
     const int box = c->page < keys ? c->page : keys;
     const int64_t size[3] = {c->page, c->heads, c->pages};
     const Axes a = axes_of(c);
@@ -143,7 +186,7 @@ int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, C
         boxes[i + 1] = a.order[i] == 0 ? (cuuint32_t)box : 1u;
     }
     for (int kv = 0; kv < 2; ++kv)
-        if (enc(kv ? v : k, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv ? c->v : c->k, dims,
+        if (enc(kv ? v : k, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, kv ? c->v : c->k, dims,
                 strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 panel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -151,14 +194,11 @@ int cache_maps(const affqmm_kv_cache* c, int padded, int keys, CUtensorMap* k, C
     return AFFQMM_OK;
 }
 
-AttnShape attn_shape(const affqmm_kv_cache* c, int rows, bool lasting, bool pair) {
-    const bool e4m3 = c->type == AFFQMM_KV_E4M3;
-    switch (which_dim(c)) {
-        case 0: return attn_shape_64(e4m3, lasting, pair, rows);
-        case 1: return attn_shape_128(e4m3, lasting, pair, rows);
-        case 2: return attn_shape_256(e4m3, lasting, pair, rows);
-        default: return attn_shape_512(e4m3, lasting, pair, rows);
-    }
+// Whether a set of kernels' other type it is: e4m3 rather than bf16, int8 rather than e4m3.
+bool other_type(const affqmm_kv_cache* c, bool blocks) { return c->type == (blocks ? AFFQMM_KV_I8 : AFFQMM_KV_E4M3); }
+
+AttnShape attn_shape(const affqmm_kv_cache* c, bool blocks, int rows, bool lasting, bool pair) {
+    return g_kernels[which_dim(c) + (blocks ? 4 : 0)].shape(other_type(c, blocks), lasting, pair, rows);
 }
 
 uint32_t reciprocal(int d) { return d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u; }
@@ -174,17 +214,17 @@ int check_heads(const affqmm_kv_cache* c, int tokens, int heads_q) {
 // pages of 64: 173 -> 113).  Not for pages below 32 tokens, whose small boxes want the producers of two CTAs an SM
 // (pages of 16: 207 us with one head to a CTA, 262 with two).
 bool pairable(const affqmm_kv_cache* c, int rows) {
-    const int row_bytes = (64 << which_dim(c)) * (c->type == AFFQMM_KV_E4M3 ? 1 : 2);
+    const int row_bytes = (64 << which_dim(c)) * value_bytes(c);
     return rows <= 8 && c->heads % 2 == 0 && row_bytes <= 128 && c->page >= 32 && c->head_stride < c->token_stride;
 }
 
 // Two partial slots for each CTA that the SMs hold, of whichever kernel a call may take.
-size_t attn_workspace(const affqmm_kv_cache* c, int rows, int sms) {
+size_t attn_workspace(const affqmm_kv_cache* c, bool blocks, int rows, int sms) {
     size_t most = 0;
     for (const bool lasting : {false, true})
         for (const bool pair : {false, true}) {
             if (pair && !(lasting && pairable(c, rows))) continue;
-            const AttnShape s = attn_shape(c, rows, lasting, pair);
+            const AttnShape s = attn_shape(c, blocks, rows, lasting, pair);
             const size_t floats = (size_t)2 * s.ctas_per_sm * sms * s.slot_floats;
             if (floats > most) most = floats;
         }
@@ -201,6 +241,205 @@ bool lasting_tiles(const affqmm_kv_cache* c, int64_t batch, int64_t keys, int sm
 // as one (paged_attn.cuh).
 int64_t count_tiles(const AttnShape& s, int64_t batch, int heads, int rows, int64_t keys) {
     return batch * heads * ((rows + s.rows - 1) / s.rows) * ((keys + s.keys - 1) / s.keys + 2);
+}
+
+// The two appends: `scales` is null for a cache without scales of blocks.  The cache has been checked.
+int append(const affqmm_kv_cache* cache, const Scales* scales, const affqmm_rope* rope, const affqmm_rows* q,
+           const affqmm_rows* k, const affqmm_rows* v, const affqmm_rows* out, int64_t tokens, int heads_q,
+           const int32_t* positions, int64_t position_stride, const int32_t* slots, uint32_t* status, void* stream) {
+    int rc;
+    if (!rope || !q || !k || !v || !out) return AFFQMM_E_NULL;
+    if (rope->rotary < 0 || rope->rotary % 2 || rope->rotary > cache->dim) return AFFQMM_E_SHAPE;
+    if ((rope->neighbour != 0 && rope->neighbour != 1) || rope->axes < 1 || rope->axes > 256) return AFFQMM_E_ARG;
+    if (tokens < 0 || tokens >= kMost || heads_q < 1 || heads_q > 4096 || position_stride < 0) return AFFQMM_E_SHAPE;
+    if (tokens == 0) return AFFQMM_OK;
+    if (!positions || !slots || (rope->rotary > 0 && !rope->turns)) return AFFQMM_E_NULL;
+    if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(rope->turns, 8) || !aligned(status, 4))
+        return AFFQMM_E_ALIGN;
+    for (const affqmm_rows* r : {q, k, v, out})
+        if ((rc = check_rows(r->p, r->token_stride, r->head_stride, 0))) return rc;
+    if (out->p == q->p && (out->token_stride != q->token_stride || out->head_stride != q->head_stride))
+        return AFFQMM_E_ARG;
+    int sms = 0;
+    rc = device_sms(&sms);
+    if (rc) return rc;
+    const int es = value_bytes(cache);
+    BlockParams all = {};
+    RopeParams& p = all.rope;
+    p.q = q->p, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
+    p.k = k->p, p.k_ts = k->token_stride, p.k_hs = k->head_stride;
+    p.v = v->p, p.v_ts = v->token_stride, p.v_hs = v->head_stride;
+    p.out = out->p, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
+    p.positions = positions;
+    p.pos_stride = position_stride;
+    p.axes = rope->axes;
+    p.slots = slots;
+    p.turns = reinterpret_cast<const int64_t*>(rope->turns);
+    p.axis = rope->axis;
+    p.rotary = rope->rotary;
+    p.neighbour = rope->neighbour;
+    p.tokens = tokens;
+    p.heads_q = heads_q;
+    p.heads_kv = cache->heads;
+    p.dim = cache->dim;
+    p.page_shift = page_shift_of(cache->page);
+    p.e4m3 = cache->type == AFFQMM_KV_E4M3;
+    p.kc = static_cast<uint8_t*>(cache->k);
+    p.vc = static_cast<uint8_t*>(cache->v);
+    p.page_bytes = cache->page_stride * es;
+    p.token_bytes = cache->token_stride * es;
+    p.head_bytes = cache->head_stride * es;
+    p.pages = cache->pages;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.status = status;
+    p.stream = tokens * (heads_q * 2 + (int64_t)cache->heads * 2 * es) * cache->dim > (int64_t)63 << 20;
+    cudaError_t e;
+    if (scales) {
+        all.k_scales = scales->k, all.v_scales = scales->v;
+        all.s_ps = scales->page_stride, all.s_bs = scales->block_stride, all.s_hs = scales->head_stride;
+        all.block_shift = scales->shift;
+        e = launch_block_append(all, sms, static_cast<cudaStream_t>(stream));
+    } else {
+        e = launch_rope_append(p, sms, static_cast<cudaStream_t>(stream));
+    }
+    return e == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
+}
+
+int attention_workspace(const affqmm_kv_cache* cache, bool blocks, int tokens, int heads_q, size_t* bytes) {
+    int rc = check_heads(cache, tokens, heads_q);
+    if (rc) return rc;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    *bytes = attn_workspace(cache, blocks, tokens * (heads_q / cache->heads), sms);
+    return AFFQMM_OK;
+}
+
+// The two attentions: `scales` is null for a cache without scales of blocks.  The cache has been checked.
+int attention(const affqmm_kv_cache* cache, const Scales* scales, const affqmm_lanes* q, const affqmm_lanes* out, float* lse,
+              int64_t batch, int tokens, int heads_q, const int32_t* table, int64_t table_stride, int64_t wide,
+              const int32_t* lens, float scale, int window, uint32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+    const bool blocks = scales != nullptr;
+    int rc = check_heads(cache, tokens, heads_q);
+    if (rc) return rc;
+    if (!q || !out) return AFFQMM_E_NULL;
+    if (batch < 0 || batch > AFFQMM_PAGED_MAX_BATCH || wide < 0 || table_stride < 0) return AFFQMM_E_SHAPE;
+    if (wide * cache->page >= ((int64_t)1 << 31) - 1024 || wide >= kMost) return AFFQMM_E_SHAPE;   // room to count tiles past the end
+    if (!std::isfinite(scale) || window < 0) return AFFQMM_E_ARG;
+    if (batch == 0) return AFFQMM_OK;
+    if (!lens || (wide > 0 && !table)) return AFFQMM_E_NULL;
+    if (!aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(status, 4)) return AFFQMM_E_ALIGN;
+    for (const affqmm_lanes* r : {q, out})
+        if ((rc = check_rows(r->p, r->batch_stride, r->token_stride, r->head_stride))) return rc;
+    const int group = heads_q / cache->heads, rows = tokens * group;
+    int64_t keys = wide * cache->page;       // that a request can have, and a window sees
+    if (window >= keys) window = 0;          // it hides nothing (and the kernel's sums of lengths and windows stay within 32 bits)
+    if (window > 0 && keys > (int64_t)window + tokens) keys = (int64_t)window + tokens;
+    // so many tiles are always lasting ones
+    if (count_tiles(attn_shape(cache, blocks, rows, true, false), batch, cache->heads, rows, keys) >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    const bool lasting = lasting_tiles(cache, batch, keys, sms);
+    const bool pair = lasting && pairable(cache, rows);
+    const AttnShape shape = attn_shape(cache, blocks, rows, lasting, pair);
+    if (!workspace || ws_bytes < attn_workspace(cache, blocks, rows, sms)) return AFFQMM_E_WORKSPACE;
+    if (!aligned(workspace, 256)) return AFFQMM_E_ALIGN;
+    const int which = which_dim(cache), kernels = which + (blocks ? 4 : 0);
+    if ((rc = allow_attn(kernels))) return rc;
+
+    AttnParams p = {};
+    CUtensorMap k_map, v_map;
+    int32_t axis[3];
+    if ((rc = cache_maps(cache, 64 << which, shape.keys, &k_map, &v_map, axis))) return rc;
+    p.axis1 = axis[0], p.axis2 = axis[1], p.axis3 = axis[2];
+    p.q = q->p, p.q_bs = q->batch_stride, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
+    p.out = out->p, p.o_bs = out->batch_stride, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
+    p.lse = lse;
+    p.pages = cache->pages;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    if (blocks) {
+        p.k_scales = scales->k, p.v_scales = scales->v;
+        p.s_ps = scales->page_stride, p.s_bs = scales->block_stride, p.s_hs = scales->head_stride;
+        p.block_shift = scales->shift;
+    }
+    p.table = table;
+    p.table_stride = table_stride;
+    p.lens = lens;
+    p.batch = (int32_t)batch;
+    p.tokens = tokens;
+    p.heads_q = heads_q;
+    p.heads_kv = cache->heads;
+    p.group = group;
+    p.dim = cache->dim;
+    p.wide = (int32_t)wide;
+    p.page_shift = page_shift_of(cache->page);
+    p.window = window;
+    p.row_tiles = (rows + shape.rows - 1) / shape.rows;
+    p.m_group = reciprocal(p.group), p.m_row_tiles = reciprocal(p.row_tiles);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int64_t fault = decode_fault_wait();
+    p.fault = fault > 0;
+    p.wait_limit = fault > 0 ? fault : kWaitLimitCycles;
+    p.user_status = status;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    p.status = reinterpret_cast<uint32_t*>(base);
+    p.counters = reinterpret_cast<uint32_t*>(base + kStatusBytes);
+    p.slots = reinterpret_cast<float*>(base + kSlotsOffset);
+    // one CTA for each that the SMs hold, or for each tile that the tables have room for
+    const int64_t tiles = count_tiles(shape, batch, cache->heads, rows, keys);
+    const int64_t most = (int64_t)sms * shape.ctas_per_sm;
+    const int grid = (int)(tiles < most ? tiles : most);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = g_kernels[kernels].launch(other_type(cache, blocks), lasting, pair, rows, p, k_map, v_map, grid, st);
+    return e == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
+}
+
+// The two reads.  The cache has been checked.
+int read_rows(const affqmm_kv_cache* cache, const Scales* scales, const affqmm_rows* k, const affqmm_rows* v, int64_t rows,
+              int64_t batch, const int32_t* table, int64_t table_stride, int64_t wide, const int32_t* starts,
+              const int32_t* first, uint32_t* status, void* stream) {
+    if (!k || !v) return AFFQMM_E_NULL;
+    if (batch < 0 || batch > AFFQMM_PAGED_MAX_BATCH || rows < 0 || rows >= kMost || wide < 0 || table_stride < 0) return AFFQMM_E_SHAPE;
+    if (wide >= kMost || wide * cache->page >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
+    if (batch == 0 || rows == 0) return AFFQMM_OK;
+    if (!starts || (wide > 0 && !table)) return AFFQMM_E_NULL;
+    if (!aligned(starts, 4) || !aligned(first, 4) || !aligned(table, 4) || !aligned(status, 4)) return AFFQMM_E_ALIGN;
+    int rc;
+    for (const affqmm_rows* r : {k, v})
+        if ((rc = check_rows(r->p, r->token_stride, r->head_stride, 0))) return rc;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    const int es = value_bytes(cache);
+    ReadParams p = {};
+    p.kc = static_cast<const uint8_t*>(cache->k);
+    p.vc = static_cast<const uint8_t*>(cache->v);
+    p.page_bytes = cache->page_stride * es;
+    p.token_bytes = cache->token_stride * es;
+    p.head_bytes = cache->head_stride * es;
+    p.pages = cache->pages;
+    p.k_scale = scales ? scales->k : cache->k_scale;
+    p.v_scale = scales ? scales->v : cache->v_scale;
+    if (scales) {
+        p.s_ps = scales->page_stride, p.s_bs = scales->block_stride, p.s_hs = scales->head_stride;
+        p.block_shift = scales->shift;
+    }
+    p.page_shift = page_shift_of(cache->page);
+    p.heads = cache->heads;
+    p.dim = cache->dim;
+    p.k = k->p, p.k_ts = k->token_stride, p.k_hs = k->head_stride;
+    p.v = v->p, p.v_ts = v->token_stride, p.v_hs = v->head_stride;
+    p.rows = rows;
+    p.batch = (int32_t)batch;
+    p.wide = (int32_t)wide;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.starts = starts;
+    p.first = first;
+    p.status = status;
+    const int kind = scales ? (cache->type == AFFQMM_KV_I8 ? READ_I8_BLOCKS : READ_E4M3_BLOCKS)
+                            : (cache->type == AFFQMM_KV_E4M3 ? READ_E4M3 : READ_BF16);
+    return launch_paged_read(p, kind, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
 }
 
 }  // namespace
@@ -258,147 +497,64 @@ int affqmm_rope_append(const affqmm_kv_cache* cache, const affqmm_rope* rope, co
                        const affqmm_rows* k, const affqmm_rows* v, const affqmm_rows* out, int64_t tokens, int heads_q,
                        const int32_t* positions, int64_t position_stride, const int32_t* slots, uint32_t* status,
                        void* stream) {
-    int rc = check_cache(cache, true);
-    if (rc) return rc;
-    if (!rope || !q || !k || !v || !out) return AFFQMM_E_NULL;
-    if (rope->rotary < 0 || rope->rotary % 2 || rope->rotary > cache->dim) return AFFQMM_E_SHAPE;
-    if ((rope->neighbour != 0 && rope->neighbour != 1) || rope->axes < 1 || rope->axes > 256) return AFFQMM_E_ARG;
-    if (tokens < 0 || tokens >= kMost || heads_q < 1 || heads_q > 4096 || position_stride < 0) return AFFQMM_E_SHAPE;
-    if (tokens == 0) return AFFQMM_OK;
-    if (!positions || !slots || (rope->rotary > 0 && !rope->turns)) return AFFQMM_E_NULL;
-    if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(rope->turns, 8) || !aligned(status, 4))
-        return AFFQMM_E_ALIGN;
-    for (const affqmm_rows* r : {q, k, v, out})
-        if ((rc = check_rows(r->p, r->token_stride, r->head_stride, 0))) return rc;
-    if (out->p == q->p && (out->token_stride != q->token_stride || out->head_stride != q->head_stride))
-        return AFFQMM_E_ARG;
-    int sms = 0;
-    rc = device_sms(&sms);
-    if (rc) return rc;
-    const int es = cache->type == AFFQMM_KV_E4M3 ? 1 : 2;
-    RopeParams p = {};
-    p.q = q->p, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
-    p.k = k->p, p.k_ts = k->token_stride, p.k_hs = k->head_stride;
-    p.v = v->p, p.v_ts = v->token_stride, p.v_hs = v->head_stride;
-    p.out = out->p, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
-    p.positions = positions;
-    p.pos_stride = position_stride;
-    p.axes = rope->axes;
-    p.slots = slots;
-    p.turns = reinterpret_cast<const int64_t*>(rope->turns);
-    p.axis = rope->axis;
-    p.rotary = rope->rotary;
-    p.neighbour = rope->neighbour;
-    p.tokens = tokens;
-    p.heads_q = heads_q;
-    p.heads_kv = cache->heads;
-    p.dim = cache->dim;
-    p.page_shift = page_shift_of(cache->page);
-    p.e4m3 = es == 1;
-    p.kc = static_cast<uint8_t*>(cache->k);
-    p.vc = static_cast<uint8_t*>(cache->v);
-    p.page_bytes = cache->page_stride * es;
-    p.token_bytes = cache->token_stride * es;
-    p.head_bytes = cache->head_stride * es;
-    p.pages = cache->pages;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
-    p.status = status;
-    p.stream = tokens * (heads_q * 2 + (int64_t)cache->heads * 2 * es) * cache->dim > (int64_t)63 << 20;
-    return launch_rope_append(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
+    const int rc = check_cache(cache, true);
+    return rc ? rc : append(cache, nullptr, rope, q, k, v, out, tokens, heads_q, positions, position_stride, slots, status, stream);
+}
+
+int affqmm_block_append(const affqmm_block_cache* cache, const affqmm_rope* rope, const affqmm_rows* q,
+                        const affqmm_rows* k, const affqmm_rows* v, const affqmm_rows* out, int64_t tokens, int heads_q,
+                        const int32_t* positions, int64_t position_stride, const int32_t* slots, uint32_t* status,
+                        void* stream) {
+    Scales s;
+    const int rc = check_blocks(cache, true, &s);
+    return rc ? rc : append(&cache->kv, &s, rope, q, k, v, out, tokens, heads_q, positions, position_stride, slots, status, stream);
 }
 
 int affqmm_paged_attention_workspace_bytes(const affqmm_kv_cache* cache, int tokens, int heads_q, size_t* bytes) {
     if (!bytes) return AFFQMM_E_NULL;
-    int rc = check_cache(cache, false);
-    if (rc) return rc;
-    if ((rc = check_heads(cache, tokens, heads_q))) return rc;
-    int sms = 0;
-    if ((rc = device_sms(&sms))) return rc;
-    *bytes = attn_workspace(cache, tokens * (heads_q / cache->heads), sms);
-    return AFFQMM_OK;
+    const int rc = check_cache(cache, false);
+    return rc ? rc : attention_workspace(cache, false, tokens, heads_q, bytes);
+}
+
+int affqmm_block_attention_workspace_bytes(const affqmm_block_cache* cache, int tokens, int heads_q, size_t* bytes) {
+    if (!bytes) return AFFQMM_E_NULL;
+    Scales s;
+    const int rc = check_blocks(cache, false, &s);
+    return rc ? rc : attention_workspace(&cache->kv, true, tokens, heads_q, bytes);
 }
 
 int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm_lanes* q, const affqmm_lanes* out, float* lse,
                            int64_t batch, int tokens, int heads_q, const int32_t* table, int64_t table_stride,
                            int64_t wide, const int32_t* lens, float scale, int window, uint32_t* status,
                            void* workspace, size_t ws_bytes, void* stream) {
-    int rc = check_cache(cache, true);
-    if (rc) return rc;
-    if ((rc = check_heads(cache, tokens, heads_q))) return rc;
-    if (!q || !out) return AFFQMM_E_NULL;
-    if (batch < 0 || batch > AFFQMM_PAGED_MAX_BATCH || wide < 0 || table_stride < 0) return AFFQMM_E_SHAPE;
-    if (wide * cache->page >= ((int64_t)1 << 31) - 1024 || wide >= kMost) return AFFQMM_E_SHAPE;   // room to count tiles past the end
-    if (!std::isfinite(scale) || window < 0) return AFFQMM_E_ARG;
-    if (batch == 0) return AFFQMM_OK;
-    if (!lens || (wide > 0 && !table)) return AFFQMM_E_NULL;
-    if (!aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(status, 4)) return AFFQMM_E_ALIGN;
-    for (const affqmm_lanes* r : {q, out})
-        if ((rc = check_rows(r->p, r->batch_stride, r->token_stride, r->head_stride))) return rc;
-    const int group = heads_q / cache->heads, rows = tokens * group;
-    int64_t keys = wide * cache->page;       // that a request can have, and a window sees
-    if (window >= keys) window = 0;          // it hides nothing (and the kernel's sums of lengths and windows stay within 32 bits)
-    if (window > 0 && keys > (int64_t)window + tokens) keys = (int64_t)window + tokens;
-    // so many tiles are always lasting ones
-    if (count_tiles(attn_shape(cache, rows, true, false), batch, cache->heads, rows, keys) >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
-    int sms = 0;
-    if ((rc = device_sms(&sms))) return rc;
-    const bool lasting = lasting_tiles(cache, batch, keys, sms);
-    const bool pair = lasting && pairable(cache, rows);
-    const AttnShape shape = attn_shape(cache, rows, lasting, pair);
-    if (!workspace || ws_bytes < attn_workspace(cache, rows, sms)) return AFFQMM_E_WORKSPACE;
-    if (!aligned(workspace, 256)) return AFFQMM_E_ALIGN;
-    const int which = which_dim(cache);
-    if ((rc = allow_attn(which))) return rc;
+    const int rc = check_cache(cache, true);
+    return rc ? rc : attention(cache, nullptr, q, out, lse, batch, tokens, heads_q, table, table_stride, wide, lens, scale, window, status,
+                               workspace, ws_bytes, stream);
+}
 
-    const bool e4m3 = cache->type == AFFQMM_KV_E4M3;
-    AttnParams p = {};
-    CUtensorMap k_map, v_map;
-    int32_t axis[3];
-    if ((rc = cache_maps(cache, 64 << which, shape.keys, &k_map, &v_map, axis))) return rc;
-    p.axis1 = axis[0], p.axis2 = axis[1], p.axis3 = axis[2];
-    p.q = q->p, p.q_bs = q->batch_stride, p.q_ts = q->token_stride, p.q_hs = q->head_stride;
-    p.out = out->p, p.o_bs = out->batch_stride, p.o_ts = out->token_stride, p.o_hs = out->head_stride;
-    p.lse = lse;
-    p.pages = cache->pages;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
-    p.table = table;
-    p.table_stride = table_stride;
-    p.lens = lens;
-    p.batch = (int32_t)batch;
-    p.tokens = tokens;
-    p.heads_q = heads_q;
-    p.heads_kv = cache->heads;
-    p.group = group;
-    p.dim = cache->dim;
-    p.wide = (int32_t)wide;
-    p.page_shift = page_shift_of(cache->page);
-    p.window = window;
-    p.row_tiles = (rows + shape.rows - 1) / shape.rows;
-    p.m_group = reciprocal(p.group), p.m_row_tiles = reciprocal(p.row_tiles);
-    p.scale_log2 = scale * 1.4426950408889634f;
-    const int64_t fault = decode_fault_wait();
-    p.fault = fault > 0;
-    p.wait_limit = fault > 0 ? fault : kWaitLimitCycles;
-    p.user_status = status;
-    uint8_t* base = static_cast<uint8_t*>(workspace);
-    p.status = reinterpret_cast<uint32_t*>(base);
-    p.counters = reinterpret_cast<uint32_t*>(base + kStatusBytes);
-    p.slots = reinterpret_cast<float*>(base + kSlotsOffset);
-    // one CTA for each that the SMs hold, or for each tile that the tables have room for
-    const int64_t tiles = count_tiles(shape, batch, cache->heads, rows, keys);
-    const int64_t most = (int64_t)sms * shape.ctas_per_sm;
-    const int grid = (int)(tiles < most ? tiles : most);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    switch (which) {
-        case 0: e = launch_attn_64(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
-        case 1: e = launch_attn_128(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
-        case 2: e = launch_attn_256(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
-        default: e = launch_attn_512(e4m3, lasting, pair, rows, p, k_map, v_map, grid, st); break;
-    }
-    return e == cudaSuccess ? AFFQMM_OK : AFFQMM_E_CUDA;
+int affqmm_block_attention(const affqmm_block_cache* cache, const affqmm_lanes* q, const affqmm_lanes* out, float* lse,
+                           int64_t batch, int tokens, int heads_q, const int32_t* table, int64_t table_stride,
+                           int64_t wide, const int32_t* lens, float scale, int window, uint32_t* status,
+                           void* workspace, size_t ws_bytes, void* stream) {
+    Scales s;
+    const int rc = check_blocks(cache, true, &s);
+    return rc ? rc : attention(&cache->kv, &s, q, out, lse, batch, tokens, heads_q, table, table_stride, wide, lens, scale, window, status,
+                               workspace, ws_bytes, stream);
+}
+
+int affqmm_paged_read(const affqmm_kv_cache* cache, const affqmm_rows* k, const affqmm_rows* v, int64_t rows, int64_t batch,
+                      const int32_t* table, int64_t table_stride, int64_t wide, const int32_t* starts, const int32_t* first,
+                      uint32_t* status, void* stream) {
+    const int rc = check_cache(cache, true);
+    return rc ? rc : read_rows(cache, nullptr, k, v, rows, batch, table, table_stride, wide, starts, first, status, stream);
+}
+
+int affqmm_block_read(const affqmm_block_cache* cache, const affqmm_rows* k, const affqmm_rows* v, int64_t rows, int64_t batch,
+                      const int32_t* table, int64_t table_stride, int64_t wide, const int32_t* starts, const int32_t* first,
+                      uint32_t* status, void* stream) {
+    Scales s;
+    const int rc = check_blocks(cache, true, &s);
+    return rc ? rc : read_rows(&cache->kv, &s, k, v, rows, batch, table, table_stride, wide, starts, first, status, stream);
 }
 
 }  // extern "C"

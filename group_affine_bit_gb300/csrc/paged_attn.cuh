@@ -89,8 +89,10 @@ namespace attn {
 
 constexpr int W = 4;                       // consumer warps
 constexpr int GROUP = 32 * W;             // threads of a group of consumers
-constexpr float lazy(bool e4m3) { return e4m3 ? 2.f : 8.f; }   // log2 of how far a score may exceed the running maximum
-constexpr float lift(bool e4m3) { return e4m3 ? 13.f : 0.f; }  // log2 of what P is multiplied by: with lazy() below f16's 16
+// Kinds of cache: bf16; e4m3 with a scale for each key head; e4m3 and int8 with a scale for each block of tokens and key head.
+enum Kind { KV_BF16, KV_E4M3, KV_E4M3_BLOCKS, KV_I8_BLOCKS };
+constexpr float lazy(bool bytes) { return bytes ? 2.f : 8.f; }   // log2 of how far a score may exceed the running maximum
+constexpr float lift(bool bytes) { return bytes ? 13.f : 0.f; }  // log2 of what P is multiplied by: with lazy() below f16's 16
 constexpr size_t SM_SMEM = 233472;         // shared memory of an SM, 1 KB of it taken by each CTA
 constexpr size_t CTA_SMEM = 232448;        // and what one CTA may have of it
 constexpr size_t STATIC_SMEM = 1024;       // the kernel's few static variables, and the ring's alignment
@@ -102,13 +104,14 @@ constexpr int MAX_SLOTS = 16;
 // `lasting` tiles (dim 128: 678 -> 657 us for 64 requests of up to 32768 keys; 7.6 -> 8.2 for one of 577).
 constexpr int key_blocks(int pitch, int na, bool lasting) { return pitch <= 128 || (pitch == 256 && (na >= 4 || lasting)) ? 2 : 1; }
 
-template <int DP, int NA, bool E4M3, int KBLOCKS, bool PAIRED>
+template <int DP, int NA, int KIND, int KBLOCKS, bool PAIRED>
 struct Cfg {
+    static constexpr bool BYTES = KIND != KV_BF16, BLOCKS = KIND >= KV_E4M3_BLOCKS, I8 = KIND == KV_I8_BLOCKS;
     // PAIR: the two groups of consumer warps take two neighbouring key heads, whose rows lie side by side in the
     // pool, and a tile holds the keys of both.
     static constexpr bool PAIR = PAIRED;
     static constexpr int HEADS = PAIR ? 2 : 1;
-    static constexpr int ES = E4M3 ? 1 : 2;
+    static constexpr int ES = BYTES ? 1 : 2;
     static constexpr int ROWS = 8 * NA;
     static constexpr int PITCH = DP * ES;              // bytes of a cache row in shared memory
     static constexpr int PW = PITCH < 128 ? PITCH : 128;   // bytes of a row in one panel
@@ -116,16 +119,17 @@ struct Cfg {
     static constexpr int KB = KBLOCKS;
     static constexpr int KEYS = 16 * W * KB;
     static constexpr int HEAD_TILE = KEYS * PITCH, TILE = HEADS * HEAD_TILE;
+    static constexpr int SCALES = BLOCKS ? 2 * HEADS * KEYS : 0;   // floats of a tile's scales: [K, V][head][block, at most KEYS]
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int QBUF = (DP == 512 && NA > 1) ? 1 : 2;
-    static constexpr int PN = E4M3 ? 1 : 2;            // numbers that make one P
+    static constexpr int PN = BYTES ? 1 : 2;           // numbers that make one P
     static constexpr int MT = DP / (16 * W);           // 16-dim tiles of a consumer warp
     static constexpr int JOIN = 32;                    // most parts that a join takes at once
     static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PN * NA * KEYS * 16 + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
-                                    JOIN * ROWS * 4 + 512;
+                                    JOIN * ROWS * 4 + (BLOCKS ? 448 : 512);   // and the barriers
     static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= 32;   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
-    static constexpr int CPS = (!PAIR && LIGHT && FIXED + 3 * TILE <= HALF) ? 2 : 1;
+    static constexpr int CPS = (!PAIR && LIGHT && FIXED + 3 * TILE + 2 * SCALES * 4 <= HALF) ? 2 : 1;
     // With one CTA an SM, the rows go to two groups of consumer warps (where there are two row tiles), which share
     // the ring and q and nothing else: two warps to a scheduler, whose latencies overlap.
     static constexpr int NG = CPS == 1 && NA >= 2 ? 2 : 1;
@@ -134,8 +138,14 @@ struct Cfg {
     static constexpr int LOW = NT * KEYS * 16;         // from P's first numbers to the second
     static constexpr int PBYTES = PN * LOW;            // of a group: [PN][NT][keys][8 rows] of 16 bits
     static constexpr size_t ROOM = (CPS == 2 ? HALF : CTA_SMEM - STATIC_SMEM) - FIXED;
-    static constexpr int NS = ROOM / TILE > MAX_SLOTS ? MAX_SLOTS : (int)(ROOM / TILE);
-    static constexpr size_t SMEM = FIXED + (size_t)NS * TILE;
+    static constexpr int sets(int slots) { return (slots + 1) / 2; }   // of scales: one for each K tile that the ring can hold
+    static constexpr int slots_in(size_t room) {
+        int n = room / TILE > MAX_SLOTS ? MAX_SLOTS : (int)(room / TILE);
+        while (n > 0 && (size_t)n * TILE + (size_t)sets(n) * SCALES * 4 > room) --n;
+        return n;
+    }
+    static constexpr int NS = slots_in(ROOM), NSC = sets(NS);
+    static constexpr size_t SMEM = FIXED + (size_t)NS * TILE + (size_t)NSC * SCALES * 4;
     static constexpr size_t STATS = (size_t)W * MT * NT * 128;  // of a group's part: the accumulators, then [row]{m, l}
     static constexpr size_t PART_FLOATS = STATS + 2 * GROWS;
     static constexpr size_t SLOT_FLOATS = NG * PART_FLOATS;
@@ -167,6 +177,21 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t w) {
     asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(d) : "r"(w));
     return d;
 }
+// Four codes in a word to f16, exact: the first two and the last two, or (ACROSS) the even and the odd ones.
+// A signed byte b is the low byte of the f16 1024 + (b + 128).
+template <bool I8, bool ACROSS>
+__device__ __forceinline__ void bytes_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+    if constexpr (I8) {
+        w ^= 0x80808080u;
+        const __half2 zero = __half2half2(__ushort_as_half(0x6480));   // 1024 + 128
+        const uint32_t x = __byte_perm(w, 0x64646464u, ACROSS ? 0x4240 : 0x4140), y = __byte_perm(w, 0x64646464u, ACROSS ? 0x4341 : 0x4342);
+        const __half2 u = __hsub2(*reinterpret_cast<const __half2*>(&x), zero), v = __hsub2(*reinterpret_cast<const __half2*>(&y), zero);
+        a = *reinterpret_cast<const uint32_t*>(&u), b = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        if (ACROSS) w = __byte_perm(w, 0, 0x3120);
+        a = e4m3_f16x2(w), b = e4m3_f16x2(w >> 16);
+    }
+}
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -190,10 +215,12 @@ __device__ __forceinline__ uint32_t count_part(uint32_t* counter) {
 }
 // n / d by m = ceil(2^32 / d), exact for n < 2^32 / d (n up to 4096 heads x 64 tokens, d up to 4096)
 __device__ __forceinline__ int over(int n, int d, uint32_t m) { return d == 1 ? n : (int)__umulhi((uint32_t)n, m); }
-// Whether one of the values in a word (two bf16, or four e4m3) is an infinity or NaN.
-template <bool E4M3>
+// Whether one of the values in a word (two bf16, or four codes) is an infinity or NaN.
+template <int KIND>
 __device__ __forceinline__ bool not_finite(uint32_t w) {
-    if constexpr (E4M3) {
+    if constexpr (KIND == KV_I8_BLOCKS) {
+        return false;
+    } else if constexpr (KIND != KV_BF16) {
         bool any = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) any |= ((w >> (8 * i)) & 0x7fu) == 0x7fu;
@@ -240,6 +267,8 @@ __device__ __forceinline__ bool mbar_wait_within(uint32_t bar, uint32_t parity, 
         if (clock64() - t0 > limit) return false;
     return true;
 }
+// A block's scale as it counts: between the bounds that the append keeps to (NaN: the lower).
+__device__ __forceinline__ float within_scales(float x) { return fminf(fmaxf(x, kLeastScale), kMostScale); }
 // 16-byte chunk `c` of row `row` of a tile: panels of PW bytes of every row,
 // swizzled as TMA swizzles rows of 128 (64) bytes, so that the eight rows that
 // one fragment load reads fall into eight bank groups.
@@ -313,18 +342,20 @@ __device__ __forceinline__ uint32_t run_of(uint32_t x, uint32_t total, uint32_t 
     return (uint32_t)(top / total);
 }
 
-template <int DP, int NA, bool E4M3, int KBLOCKS, bool PAIRED>
-__global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::CPS) paged_attn_kernel(
+template <int DP, int NA, int KIND, int KBLOCKS, bool PAIRED>
+__global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::CPS) paged_attn_kernel(
     const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>;
+    using C = Cfg<DP, NA, KIND, KBLOCKS, PAIRED>;
+    constexpr bool BYTES = C::BYTES, BLOCKS = C::BLOCKS;
     constexpr int KEYS = C::KEYS, THREADS = C::THREADS, PRODUCER = C::NG * W;   // the first warp that is no consumer
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
-    uint8_t* qbuf = ring + (size_t)C::NS * C::TILE;
+    float* scales = reinterpret_cast<float*>(ring + (size_t)C::NS * C::TILE);   // [NSC][K, V][head][KEYS]
+    uint8_t* qbuf = reinterpret_cast<uint8_t*>(scales + (size_t)C::NSC * C::SCALES);
     uint8_t* pbuf = qbuf + C::QBUF * C::QBYTES;
     float* red = reinterpret_cast<float*>(pbuf + 2 * C::NG * C::PBYTES);      // of each group: [W][rows] maxima
     float* lred = red + W * C::ROWS;                                  // of each group: [W][rows] sums
-    float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] e4m3: scale of the row's scores
+    float* qscale = lred + W * C::ROWS;                               // [QBUF][ROWS] of 8-bit caches: scale of the row's scores
     int* row_token = reinterpret_cast<int*>(qscale + C::QBUF * C::ROWS);   // [QBUF][ROWS] token of a row, -1: none
     int* row_head = row_token + C::QBUF * C::ROWS;                    // [QBUF][ROWS] and its query head
     float* stats = reinterpret_cast<float*>(row_head + C::QBUF * C::ROWS);   // [QBUF][ROWS]{m, l} of staged rows
@@ -341,6 +372,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     auto joined = [&](int s) { return counted + 24u + 8u * s; };  // parts of other runs are in the group's share of the ring
     const uint32_t drained = counted + 40u;                      // the q warp has written every row
     const uint32_t never = counted + 48u;                        // completed by nothing: the fault_wait test hook waits on it
+    auto scaled = [&](int s) { return counted + 56u + 8u * s; };  // a K tile's scales are there (and its V tile's), of each set
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
     __shared__ float kscale[4], vscale[4];   // of each q buffer, of each key head of the unit
     __shared__ int found_b;
@@ -364,6 +396,8 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
         for (int s = 0; s < C::NG; ++s) mbar_init(joined(s), W);
         mbar_init(drained, 1);
         mbar_init(never, 1);
+        if constexpr (BLOCKS)
+            for (int s = 0; s < C::NSC; ++s) mbar_init(scaled(s), 32);
         fence_mbar_init();
         spoilt = 0;
     }
@@ -445,6 +479,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
         int slot = is_v ? 1 : 0;
         uint32_t phase = 0;
         int64_t turn = slot;                 // of the ring, over the whole run
+        int set = 0;                         // of scales
         while (ok && walk.next(p, units)) {
             const Span s = walk.s;
             const int32_t* table = p.table + (int64_t)walk.b * p.table_stride;
@@ -472,6 +507,19 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 const uint32_t dst = ring_u + (uint32_t)slot * C::TILE, bar = full(slot);
+                const int e0 = key0 >> p.page_shift;    // the tile's first entry, and the tile's pages in the lanes
+                int tile_page = 0;
+                if constexpr (BLOCKS)
+                    if (!is_v && p.page_shift >= 2) {
+#pragma unroll 1
+                        while (e0 - have >= 32) {
+                            have += 32;
+                            cur = nxt;
+                            nxt = entries(have + 32 + lane);
+                        }
+                        const int e = e0 - have + lane, x = __shfl_sync(~0u, cur, e & 31), y = __shfl_sync(~0u, nxt, e & 31);
+                        tile_page = e < 32 ? x : y;
+                    }
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::HEADS * C::PANELS * box_bytes);
                 __syncwarp();
 #pragma unroll 1
@@ -498,6 +546,32 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                                             bar);
                     }
                 }
+                if constexpr (BLOCKS)
+                    if (!is_v) {
+                        // the scales of the tile's blocks, K's and V's, a word to a lane; zeros where there is no page or
+                        // nothing that a query may see
+                        const int count_shift = max(0, (KEYS == 128 ? 7 : 6) - p.block_shift), count = 1 << count_shift;
+                        const uint32_t to = smem_u32(scales + set * C::SCALES);
+#pragma unroll 1
+                        for (int i0 = 0; i0 < 2 * C::HEADS * count; i0 += 32) {
+                            const int i = i0 + lane, block = i & (count - 1), which = i >> count_shift;   // which: V or K, head
+                            const int key = key0 + (block << p.block_shift), e = (key >> p.page_shift) - e0;
+                            int page = __shfl_sync(~0u, tile_page, e & 31);
+                            const bool seen = key < s.hi && key + (1 << p.block_shift) > s.lo;
+                            if (p.page_shift < 2) page = seen ? table[e0 + e] : -1;
+                            if (which < 2 * C::HEADS) {
+                                const bool there = seen && (uint32_t)page < (uint64_t)p.pages;
+                                const float* from = (which >= C::HEADS ? p.v_scales : p.k_scales) +
+                                                    (there ? page * p.s_ps + (int64_t)(((uint32_t)key & page_mask) >> p.block_shift) * p.s_bs +
+                                                                 (head0 + which % C::HEADS) * p.s_hs
+                                                           : 0);
+                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (uint32_t)(which * KEYS + block) * 4u),
+                                             "l"(from), "r"(there ? 4u : 0u) : "memory");
+                            }
+                        }
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(scaled(set)) : "memory");
+                        if (++set == C::NSC) set = 0;
+                    }
                 turn += 2;
                 slot += 2;
                 if (slot >= C::NS) slot -= C::NS, phase ^= 1u;
@@ -506,6 +580,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
         // The next kernel's CTAs may come as this one's end: what this kernel waited for is complete.
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // no copy is in flight when the CTA ends, whatever its consumers did
+        if constexpr (BLOCKS) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
         for (int64_t i = turn - 2; i >= 0 && i >= turn - C::NS; i -= 2)
             if (!mbar_wait(full((int)(i % C::NS)), (uint32_t)(i / C::NS) & 1u)) ok = false;
@@ -549,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
             if (p.lse && ch == 0) {
                 const float top = stat[2 * r], sum = stat[2 * r + 1];
                 p.lse[((int64_t)b * p.tokens + at.token) * p.heads_q + at.head] =
-                    ((top == __int_as_float(0xff800000) ? 0.f : top) + __log2f(sum) - lift(E4M3)) * 0.69314718055994531f;
+                    ((top == __int_as_float(0xff800000) ? 0.f : top) + __log2f(sum) - lift(BYTES)) * 0.69314718055994531f;
             }
         }
     };
@@ -585,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + qchunk_at<QCH>(i / QCH, i % QCH)),
                              "l"(src ? src : p.q), "r"(src ? 16u : 0u) : "memory");
             }
-            if constexpr (E4M3)
+            if constexpr (BYTES)
                 if (lane < C::HEADS) {
                     kscale[2 * qs + lane] = p.k_scale ? p.k_scale[hk + lane] : 1.f;
                     vscale[2 * qs + lane] = p.v_scale ? p.v_scale[hk + lane] : 1.f;
@@ -648,8 +723,8 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     weight += group * C::JOIN * GROWS;
     auto consumer_sync = [&] { group_sync(group); };
     auto consumer_any = [&](bool v) { return group_any(group, v); };
-    int slot = 0, qs = 0;
-    uint32_t phase = 0, qphase = 0;
+    int slot = 0, qs = 0, set = 0;
+    uint32_t phase = 0, qphase = 0, sphase = 0;
     const uint32_t ring_u = smem_u32(ring), qbuf_u = smem_u32(qbuf), pbuf_u = smem_u32(pbuf) + group * 2 * C::PBYTES;
     uint32_t turn = 0;                       // which half of pbuf
     float acc[MT][NT][4], m[NT][2], l[NT][2];
@@ -802,9 +877,9 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 if (cw == 0 && g == 0) stat[2 * r] = m[nt][e], stat[2 * r + 1] = l[nt][e];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const int d = (cw * MT + mt) * 16 + (E4M3 ? 2 * g : g);
+                    const int d = (cw * MT + mt) * 16 + (BYTES ? 2 * g : g);
                     uint8_t* to = stage + qchunk_at<QCH>(r, d >> 3) + (d & 7) * 2;
-                    if constexpr (E4M3) {
+                    if constexpr (BYTES) {
                         *reinterpret_cast<uint32_t*>(to) = pack2<false>(acc[mt][nt][e] * inv, acc[mt][nt][e + 2] * inv);
                     } else {
                         *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(acc[mt][nt][e] * inv);
@@ -846,7 +921,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 l[nt][0] = l[nt][1] = 0.f;
             }
             wait(qfull(qs), qphase);
-            if constexpr (E4M3) {
+            if constexpr (BYTES) {
                 // q to f16, a warp to a row: times a power of two that brings the row's largest magnitude into
                 // [2^13, 2^14), and within 16 dims in the order in which an 8-bit K fragment holds them: a thread's
                 // four bytes 4t .. 4t + 3 are k = 2t, 2t + 1, 2t + 8, 2t + 9
@@ -877,12 +952,12 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 }
                 consumer_sync();
             }
-            v_scale = E4M3 ? vscale[2 * qs + (C::PAIR ? group : 0)] : 1.f;
+            v_scale = BYTES ? vscale[2 * qs + (C::PAIR ? group : 0)] : 1.f;
             float sc[NT][2];                     // of the scores: softmax scale, log2(e), k's scale, q's power of two
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) sc[nt][e] = E4M3 ? qscale[qs * C::ROWS + rb + 8 * nt + t2 + e] : p.scale_log2;
+                for (int e = 0; e < 2; ++e) sc[nt][e] = BYTES ? qscale[qs * C::ROWS + rb + 8 * nt + t2 + e] : p.scale_log2;
             const uint32_t q_u = qbuf_u + qs * C::QBYTES;
 
 #pragma unroll 1
@@ -905,13 +980,13 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
                             const int krow = 16 * (cw + W * kb) + (lane & 15);
-                            if constexpr (E4M3) {
+                            if constexpr (BYTES) {
                                 uint32_t r[4];
                                 ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 2 * s2 + (lane >> 4)), r);
-                                a0[kb][0] = e4m3_f16x2(r[0]), a0[kb][2] = e4m3_f16x2(r[0] >> 16);
-                                a0[kb][1] = e4m3_f16x2(r[1]), a0[kb][3] = e4m3_f16x2(r[1] >> 16);
-                                a1[kb][0] = e4m3_f16x2(r[2]), a1[kb][2] = e4m3_f16x2(r[2] >> 16);
-                                a1[kb][1] = e4m3_f16x2(r[3]), a1[kb][3] = e4m3_f16x2(r[3] >> 16);
+                                bytes_f16<C::I8, false>(r[0], a0[kb][0], a0[kb][2]);
+                                bytes_f16<C::I8, false>(r[1], a0[kb][1], a0[kb][3]);
+                                bytes_f16<C::I8, false>(r[2], a1[kb][0], a1[kb][2]);
+                                bytes_f16<C::I8, false>(r[3], a1[kb][1], a1[kb][3]);
                             } else {
                                 ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + (lane >> 4)), a0[kb]);
                                 ldsm4(kt + chunk_at<C::PW, KEYS>(krow, 4 * s2 + 2 + (lane >> 4)), a1[kb]);
@@ -922,11 +997,28 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                             uint32_t b[4];
                             ldsm4(q_u + qchunk_at<QCH>(rb + 8 * nt + (lane & 7), 4 * s2 + (lane >> 3)), b);
 #pragma unroll
-                            for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a0[kb], b[0], b[1]);
+                            for (int kb = 0; kb < KB; ++kb) mma<BYTES>(sT[kb][nt], a0[kb], b[0], b[1]);
 #pragma unroll
-                            for (int kb = 0; kb < KB; ++kb) mma<E4M3>(sT[kb][nt], a1[kb], b[2], b[3]);
+                            for (int kb = 0; kb < KB; ++kb) mma<BYTES>(sT[kb][nt], a1[kb], b[2], b[3]);
                         }
                     }
+                }
+                // the scales of this thread's keys: K's; log2 of V's, by which P grows; and one over V's
+                float ks[KB][2], lv[KB][2], rv[KB][2];
+                if constexpr (BLOCKS) {
+                    wait(scaled(set), sphase);
+                    const float* of = scales + set * C::SCALES + (C::PAIR ? group * KEYS : 0);
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int block = (16 * (cw + W * kb) + g + 8 * h) >> p.block_shift;
+                            const float v = within_scales(of[C::HEADS * KEYS + block]);
+                            ks[kb][h] = within_scales(of[block]);
+                            lv[kb][h] = __log2f(v);
+                            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rv[kb][h]) : "f"(v));
+                        }
+                    if (++set == C::NSC) set = 0, sphase ^= 1u;
                 }
                 advance();   // the K tile has been read
 
@@ -938,7 +1030,10 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sT[kb][nt][e] *= sc[nt][e & 1];
+                        for (int e = 0; e < 4; ++e) {
+                            sT[kb][nt][e] *= sc[nt][e & 1];
+                            if constexpr (BLOCKS) sT[kb][nt][e] = fmaf(sT[kb][nt][e], ks[kb][e >> 1], lv[kb][e >> 1]);
+                        }
                 if (!whole) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -960,7 +1055,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + lazy(E4M3);
+                        for (int e = 0; e < 4; ++e) need |= sT[kb][nt][e] > m[nt][e & 1] + lazy(BYTES);
 
                 // ---- P^T = 2^(s - m + lift), to [nt][key][row]
                 const uint32_t p_u = pbuf_u + turn * C::PBYTES;
@@ -968,7 +1063,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                 auto make_p = [&] {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float m0 = (m[nt][0] == NINF ? 0.f : m[nt][0]) - lift(E4M3), m1 = (m[nt][1] == NINF ? 0.f : m[nt][1]) - lift(E4M3);
+                        const float m0 = (m[nt][0] == NINF ? 0.f : m[nt][0]) - lift(BYTES), m1 = (m[nt][1] == NINF ? 0.f : m[nt][1]) - lift(BYTES);
                         sum[nt][0] = sum[nt][1] = 0.f;
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb) {
@@ -976,9 +1071,14 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
 #pragma unroll
                             for (int e = 0; e < 4; e += 2) {
                                 const float x = exp2_approx(sT[kb][nt][e] - m0), y = exp2_approx(sT[kb][nt][e + 1] - m1);
-                                sum[nt][0] += x;
-                                sum[nt][1] += y;
-                                if constexpr (E4M3) {
+                                if constexpr (BLOCKS) {
+                                    sum[nt][0] = fmaf(x, rv[kb][e >> 1], sum[nt][0]);
+                                    sum[nt][1] = fmaf(y, rv[kb][e >> 1], sum[nt][1]);
+                                } else {
+                                    sum[nt][0] += x;
+                                    sum[nt][1] += y;
+                                }
+                                if constexpr (BYTES) {
                                     st_shared(at + e * 64, pack2<true>(x, y));
                                 } else {         // the upper halves, and what they leave of P (1 + 2^-23)
                                     const uint32_t bx = __float_as_uint(x), by = __float_as_uint(y);
@@ -1053,22 +1153,19 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                         for (int i = ct; i < n * PCH; i += GROUP) {
                             const int r = i / PCH, row = r < a1 - z0 ? z0 + r : b0 + r - (a1 - z0);
                             const uint4 w = *reinterpret_cast<const uint4*>(v + chunk_at<C::PW, KEYS>(row, i % PCH));
-                            apart |= not_finite<E4M3>(w.x) || not_finite<E4M3>(w.y) || not_finite<E4M3>(w.z) || not_finite<E4M3>(w.w);
+                            apart |= not_finite<KIND>(w.x) || not_finite<KIND>(w.y) || not_finite<KIND>(w.z) || not_finite<KIND>(w.w);
                         }
                         fence_proxy_async_smem();        // before TMA writes the slot again
                         apart = consumer_any(apart);
                     }
                     // V^T fragments of 16-dim tile mt: keys 32 kp .. 32 kp + 31, two k-steps
                     auto v_frags = [&](int kp, int mt, uint32_t (&f)[2][4]) {
-                        if constexpr (E4M3) {
+                        if constexpr (BYTES) {
                             uint32_t r[4];
                             ldsm4t(vt + chunk_at<C::PW, KEYS>(32 * kp + lane, cw * MT + mt), r);
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const uint32_t x = __byte_perm(r[h], 0, 0x3120);   // (key, key + 1) of dim 2g, then of 2g + 1
-                                f[h >> 1][(h & 1) * 2] = e4m3_f16x2(x);
-                                f[h >> 1][(h & 1) * 2 + 1] = e4m3_f16x2(x >> 16);
-                            }
+                            for (int h = 0; h < 4; ++h)              // (key, key + 1) of dim 2g, then of 2g + 1
+                                bytes_f16<C::I8, true>(r[h], f[h >> 1][(h & 1) * 2], f[h >> 1][(h & 1) * 2 + 1]);
                         } else {
                             const int key = 32 * kp + (lane & 7) + ((lane >> 4) << 3);
                             const int c = 2 * (cw * MT + mt) + ((lane >> 3) & 1);
@@ -1096,8 +1193,8 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                                 for (int n = 0; n < C::PN; ++n)
 #pragma unroll
                                     for (int nt = 0; nt < NT; ++nt) {
-                                        mma<E4M3>(acc[mt][nt], f[0], b[n][nt][0], b[n][nt][1]);
-                                        mma<E4M3>(acc[mt][nt], f[1], b[n][nt][2], b[n][nt][3]);
+                                        mma<BYTES>(acc[mt][nt], f[0], b[n][nt][0], b[n][nt][1]);
+                                        mma<BYTES>(acc[mt][nt], f[1], b[n][nt][2], b[n][nt][3]);
                                     }
                             }
                         }
@@ -1124,8 +1221,8 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
                                         float d[4] = {acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]};
 #pragma unroll
                                         for (int n = 0; n < C::PN; ++n) {
-                                            mma<E4M3>(d, f[0], b[n][nt][0], b[n][nt][1]);
-                                            mma<E4M3>(d, f[1], b[n][nt][2], b[n][nt][3]);
+                                            mma<BYTES>(d, f[0], b[n][nt][0], b[n][nt][1]);
+                                            mma<BYTES>(d, f[1], b[n][nt][2], b[n][nt][3]);
                                         }
 #pragma unroll
                                         for (int e = 0; e < 4; ++e)
@@ -1201,10 +1298,10 @@ __global__ void __launch_bounds__(Cfg<DP, NA, E4M3, KBLOCKS, PAIRED>::THREADS, C
     if (!ok) atomicOr(p.status, 1u);
 }
 
-template <int DP, int NA, bool E4M3, bool LASTING, bool PAIR>
+template <int DP, int NA, int KIND, bool LASTING, bool PAIR>
 struct Launch {
-    static constexpr int KB = key_blocks(DP * (E4M3 ? 1 : 2), NA, LASTING);
-    using C = Cfg<DP, NA, E4M3, KB, PAIR>;
+    static constexpr int KB = key_blocks(DP * (KIND == KV_BF16 ? 2 : 1), NA, LASTING);
+    using C = Cfg<DP, NA, KIND, KB, PAIR>;
     static AttnShape shape() {
         AttnShape s;
         s.ctas_per_sm = C::CPS;
@@ -1214,10 +1311,10 @@ struct Launch {
         return s;
     }
     static cudaError_t allow() {
-        return cudaFuncSetAttribute(paged_attn_kernel<DP, NA, E4M3, KB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        return cudaFuncSetAttribute(paged_attn_kernel<DP, NA, KIND, KB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     }
     static cudaError_t launch(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid, cudaStream_t st) {
-        return launch_pdl(paged_attn_kernel<DP, NA, E4M3, KB, PAIR>, dim3((unsigned)grid), C::THREADS, C::SMEM, st, p, k, v);
+        return launch_pdl(paged_attn_kernel<DP, NA, KIND, KB, PAIR>, dim3((unsigned)grid), C::THREADS, C::SMEM, st, p, k, v);
     }
 };
 
@@ -1225,53 +1322,55 @@ struct Launch {
 // (32 at dim 256, whose accumulators fill the registers, and 16 at dim 512,
 // whose tiles fill shared memory); more rows go to several tiles, each of
 // which reads the keys again, the later ones mostly from L2.
-template <int DP, typename Then>
-auto with_rows(bool e4m3, bool lasting, bool pair, int rows, Then then) {
+// BLOCKS: a scale for each block of tokens and head; bytes: e4m3 rather than bf16, with BLOCKS int8 rather than e4m3.
+template <int DP, bool BLOCKS, typename Then>
+auto with_rows(bool bytes, bool lasting, bool pair, int rows, Then then) {
     constexpr int MOST = DP <= 128 ? 8 : DP == 256 ? 4 : 2;
+    constexpr int ONE = BLOCKS ? KV_E4M3_BLOCKS : KV_BF16, OTHER = BLOCKS ? KV_I8_BLOCKS : KV_E4M3;
     auto typed = [&](auto na) {
         constexpr int NA = decltype(na)::value;
-        if (e4m3) return lasting ? then(Launch<DP, NA, true, true, false>{}) : then(Launch<DP, NA, true, false, false>{});
-        return lasting ? then(Launch<DP, NA, false, true, false>{}) : then(Launch<DP, NA, false, false, false>{});
+        if (bytes) return lasting ? then(Launch<DP, NA, OTHER, true, false>{}) : then(Launch<DP, NA, OTHER, false, false>{});
+        return lasting ? then(Launch<DP, NA, ONE, true, false>{}) : then(Launch<DP, NA, ONE, false, false>{});
     };
     if constexpr (DP <= 128)
-        if (pair && e4m3) return then(Launch<DP, 2, true, true, true>{});
-    if constexpr (DP <= 64)
-        if (pair) return then(Launch<DP, 2, false, true, true>{});
+        if (pair && bytes) return then(Launch<DP, 2, OTHER, true, true>{});
+    if constexpr (DP <= 64 || (BLOCKS && DP <= 128))
+        if (pair) return then(Launch<DP, 2, ONE, true, true>{});
     if (rows <= 8) return typed(std::integral_constant<int, 1>{});
     if (rows <= 16 || MOST == 2) return typed(std::integral_constant<int, 2>{});
     if (rows <= 32 || MOST == 4) return typed(std::integral_constant<int, MOST < 4 ? 2 : 4>{});
     return typed(std::integral_constant<int, MOST < 8 ? 2 : 8>{});
 }
 
-template <int DP>
-AttnShape shape(bool e4m3, bool lasting, bool pair, int rows) {
-    return with_rows<DP>(e4m3, lasting, pair, rows, [](auto l) { return l.shape(); });
+template <int DP, bool BLOCKS>
+AttnShape shape(bool bytes, bool lasting, bool pair, int rows) {
+    return with_rows<DP, BLOCKS>(bytes, lasting, pair, rows, [](auto l) { return l.shape(); });
 }
-template <int DP>
+template <int DP, bool BLOCKS>
 cudaError_t allow_all() {
     for (int i = 0; i < 32; ++i) {
-        const cudaError_t e = with_rows<DP>(i & 1, i & 2, i & 4, 8 << (i >> 3), [](auto l) { return l.allow(); });
+        const cudaError_t e = with_rows<DP, BLOCKS>(i & 1, i & 2, i & 4, 8 << (i >> 3), [](auto l) { return l.allow(); });
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
-template <int DP>
-cudaError_t launch(bool e4m3, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid,
+template <int DP, bool BLOCKS>
+cudaError_t launch(bool bytes, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int grid,
                    cudaStream_t st) {
-    return with_rows<DP>(e4m3, lasting, pair, rows, [&](auto l) { return l.launch(p, k, v, grid, st); });
+    return with_rows<DP, BLOCKS>(bytes, lasting, pair, rows, [&](auto l) { return l.launch(p, k, v, grid, st); });
 }
 
 }  // namespace attn
 }  // namespace affqmm
 
-#define AFFQMM_ATTN_DEFINE(DP)                                                                                              \
+#define AFFQMM_ATTN_DEFINE(DP, NAME, BLOCKS)                                                                                \
     namespace affqmm {                                                                                                      \
-    AttnShape attn_shape_##DP(bool e4m3, bool lasting, bool pair, int rows) {                                               \
-        return attn::shape<DP>(e4m3, lasting, pair, rows);                                                                  \
+    AttnShape attn_shape_##NAME(bool bytes, bool lasting, bool pair, int rows) {                                            \
+        return attn::shape<DP, BLOCKS>(bytes, lasting, pair, rows);                                                         \
     }                                                                                                                       \
-    cudaError_t attn_allow_smem_##DP() { return attn::allow_all<DP>(); }                                                    \
-    cudaError_t launch_attn_##DP(bool e4m3, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k,   \
-                                 const CUtensorMap& v, int grid, cudaStream_t st) {                                         \
-        return attn::launch<DP>(e4m3, lasting, pair, rows, p, k, v, grid, st);                                              \
+    cudaError_t attn_allow_smem_##NAME() { return attn::allow_all<DP, BLOCKS>(); }                                          \
+    cudaError_t launch_attn_##NAME(bool bytes, bool lasting, bool pair, int rows, const AttnParams& p, const CUtensorMap& k, \
+                                   const CUtensorMap& v, int grid, cudaStream_t st) {                                       \
+        return attn::launch<DP, BLOCKS>(bytes, lasting, pair, rows, p, k, v, grid, st);                                     \
     }                                                                                                                       \
     }

@@ -1,0 +1,4 @@
+// Attention over the paged cache with a scale for each block of tokens and head, head dim padded to 512 (paged_attn.cuh).
+#include "paged_attn.cuh"
+
+AFFQMM_ATTN_DEFINE(512, blocks_512, true)

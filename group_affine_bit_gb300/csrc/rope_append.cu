@@ -23,33 +23,14 @@
 // multiplication.  A call whose output is more than half of L2 (126 MB) loads
 // and stores what leaves L2 first: 8192 tokens, 201 MB, in 32.6 us instead of
 // 35.1; a smaller one leaves its output there for the attention that reads it.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
+#include "rope_pieces.cuh"
 
 namespace affqmm {
 namespace {
 
 constexpr int RA_THREADS = 128;
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-    x[0] = bf_lo(w.x), x[1] = bf_hi(w.x), x[2] = bf_lo(w.y), x[3] = bf_hi(w.y);
-    x[4] = bf_lo(w.z), x[5] = bf_hi(w.z), x[6] = bf_lo(w.w), x[7] = bf_hi(w.w);
-}
-
-__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
 
 // Where a value goes: q's output rows (bf16), or a row of the cache in its type.
 struct Row {
@@ -100,9 +81,6 @@ __device__ __forceinline__ void copy8(const Row& r, int d, const uint16_t* src) 
     }
 }
 
-// n / d by m = ceil(2^32 / d), exact for n < 2^32 / d (heads <= 8192, pieces <= 512)
-__device__ __forceinline__ int over(int n, uint32_t m, int d) { return d == 1 ? n : (int)__umulhi((uint32_t)n, m); }
-
 // WIDE: eight neighbouring values (half pairs: twice eight) to a thread, where
 // rotary / 2 (half pairs) or rotary / 8 allows it; otherwise a pair or a
 // single value to a thread.  The pieces of a head: `spun` that turn, `still`
@@ -116,10 +94,7 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(RopeParams p, i
     const int half = p.rotary >> 1, step = gridDim.y * RA_THREADS, idx0 = blockIdx.y * RA_THREADS + threadIdx.x;
     const int32_t slot = p.slots[t];
     for (int i = threadIdx.x; i < half; i += RA_THREADS) {
-        const int a = p.axis ? min((int)p.axis[i], p.axes - 1) : 0;
-        const int64_t pos = p.positions[a * p.pos_stride + t];
-        const int64_t phase = (int64_t)((uint64_t)pos * (uint64_t)p.turns[i]);   // modulo a whole turn
-        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sines[i], &cosines[i]);
+        turn_of(p, t, i, &sines[i], &cosines[i]);
     }
     const int64_t page = slot >> p.page_shift;
     const bool kept = slot >= 0 && page < p.pages;

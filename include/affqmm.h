@@ -383,6 +383,7 @@ AFFQMM_API int affqmm_run_noalloc(const affqmm_weight* w, const uint16_t* x, int
 /* Types of the cache's values. */
 #define AFFQMM_KV_BF16 0
 #define AFFQMM_KV_E4M3 1   /* 8-bit floats, times a scale of their key head */
+#define AFFQMM_KV_I8 2     /* 8-bit integers; only with a scale for each block of tokens and head */
 
 /* A cache: a non-owning view of the pool's keys and values.
  *   page          tokens of a page, a power of two up to 65536
@@ -553,6 +554,91 @@ AFFQMM_API int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm
                                       float* lse, int64_t batch, int tokens, int heads_q, const int32_t* table,
                                       int64_t table_stride, int64_t wide, const int32_t* lens, float scale,
                                       int window, uint32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- A cache with a scale for each block of tokens and key head.  A value is
+ * its code times its block's scale; both are made as the cache is written, so
+ * that nothing has to be calibrated beforehand. */
+
+/* Most tokens of a block, and the bounds of a scale: 2^-48 and 2^48. */
+#define AFFQMM_BLOCK_MAX 128
+
+/* Such a cache: a non-owning view.
+ *   kv            as for the other calls, with type AFFQMM_KV_E4M3 or
+ *                 AFFQMM_KV_I8 (codes -127 .. 127) and no k_scale and v_scale
+ *   block         tokens of a block: a power of two up to AFFQMM_BLOCK_MAX that
+ *                 divides kv.page; token i of a page is in its block i / block
+ *   s_*_stride    elements of the scales between pages, blocks and heads, in any
+ *                 order in memory: each at least what the axis inside it takes up
+ *                 (that of an axis of one does not matter)
+ *   k_scales, v_scales  device, fp32 [pages, page / block, heads].  What lies
+ *                 beyond 2^-48 and 2^48 counts as the nearer of the two where the
+ *                 cache is attended over or added to (NaN: the first) */
+typedef struct {
+    affqmm_kv_cache kv;
+    int32_t block;
+    int64_t s_page_stride, s_block_stride, s_head_stride;
+    float* k_scales;
+    float* v_scales;
+} affqmm_block_cache;
+
+/* affqmm_rope_append into such a cache.  Of each block that tokens of the call
+ * fall into, for each key head, and for k (after its rotation) and v apart:
+ *     top = the largest magnitude that the call brings
+ *     scale = top / 127 (AFFQMM_KV_I8), or the least power of two from top / 448
+ *             on (AFFQMM_KV_E4M3), within 2^-48 and 2^48
+ *     code = value / scale, rounded to nearest (ties to even) and saturating
+ * in fp32.  A call that brings a block's first token begins the block anew: what
+ * it held counts as gone.  Else the block's scale is kept where it is large
+ * enough already; where it is not, the block's other codes are brought to the
+ * new scale, and rounded once more (an e4m3 code loses bits only if it falls below
+ * the normal ones).  So a pool's pages can be used again as they are, the scales
+ * need no first value, and the same calls give the same codes.
+ * Infinities do not count for `top` and get the largest code; NaN stays NaN in
+ * e4m3 and becomes 0 in int8.
+ *   slots     as for affqmm_rope_append; and the tokens of one block come one
+ *             after another in the call (as affqmm_paged_plan orders them), with
+ *             no token of another block and no -1 between them
+ * The other arguments and the errors are those of affqmm_rope_append. */
+AFFQMM_API int affqmm_block_append(const affqmm_block_cache* cache, const affqmm_rope* rope, const affqmm_rows* q,
+                                   const affqmm_rows* k, const affqmm_rows* v, const affqmm_rows* out, int64_t tokens,
+                                   int heads_q, const int32_t* positions, int64_t position_stride,
+                                   const int32_t* slots, uint32_t* status, void* stream);
+
+/* affqmm_paged_attention over such a cache, with its arguments, results and
+ * errors.  The probabilities, each times its value's scale, keep 11 bits down to
+ * 2^-27 of the largest such product of a row, and smaller ones are off by 2^-38
+ * of it at most. */
+AFFQMM_API int affqmm_block_attention_workspace_bytes(const affqmm_block_cache* cache, int tokens, int heads_q,
+                                                      size_t* bytes);
+AFFQMM_API int affqmm_block_attention(const affqmm_block_cache* cache, const affqmm_lanes* q, const affqmm_lanes* out,
+                                      float* lse, int64_t batch, int tokens, int heads_q, const int32_t* table,
+                                      int64_t table_stride, int64_t wide, const int32_t* lens, float scale,
+                                      int window, uint32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/* Tokens of the requests as rows of bf16 again, request behind request: row
+ * starts[b] + j of k and v is token first[b] + j of request b, for j below
+ * starts[b + 1] - starts[b]: its stored values, or its codes times their scale,
+ * rounded once.  For attention over whole prompts, or a move to another pool.
+ *   k, v      [rows, cache heads, dim] rows; must not overlap the cache
+ *   rows      rows that k and v have room for, below 2^30; rows from starts[batch]
+ *             on are left as they are
+ *   batch     requests, up to AFFQMM_PAGED_MAX_BATCH
+ *   table     device, int32 [batch, wide], rows table_stride apart; wide x page
+ *             below 2^31
+ *   starts    device, int32 [batch + 1], not descending, the first of them 0
+ *             (affqmm_paged_plan's `starts` serve)
+ *   first     device, int32 [batch], or NULL: 0
+ *   status    device uint32 or NULL: bit 1 is set for a token outside its
+ *             request's row of the table, or whose entry is no page (its rows are
+ *             zeros), and for starts[batch] beyond `rows` (the rows that there are
+ *             are written)
+ * Errors: E_NULL, E_SHAPE, E_ALIGN, E_ARG, E_DEVICE, E_CUDA. */
+AFFQMM_API int affqmm_paged_read(const affqmm_kv_cache* cache, const affqmm_rows* k, const affqmm_rows* v, int64_t rows,
+                                 int64_t batch, const int32_t* table, int64_t table_stride, int64_t wide,
+                                 const int32_t* starts, const int32_t* first, uint32_t* status, void* stream);
+AFFQMM_API int affqmm_block_read(const affqmm_block_cache* cache, const affqmm_rows* k, const affqmm_rows* v, int64_t rows,
+                                 int64_t batch, const int32_t* table, int64_t table_stride, int64_t wide,
+                                 const int32_t* starts, const int32_t* first, uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }
