@@ -89,8 +89,9 @@ struct AttnParams {
     int32_t axis1, axis2, axis3; // what the cache's tensor maps have as axes 1 .. 3: 0 token, 1 head, 2 page
     const float *k_scale, *v_scale;     // of each head, or null
     const float *k_scales, *v_scales;   // of each block of tokens and head
-    int64_t s_ps, s_bs, s_hs;           // page, block and head strides of the two, elements
+    int32_t s_ps, s_bs, s_hs;           // page, block and head strides of the two, elements
     int32_t block_shift;
+    int32_t s_pairs;                    // the scales of heads 2i and 2i + 1 lie side by side, eight bytes on their boundary
     const int32_t* table;
     int64_t table_stride;
     const int32_t* lens;

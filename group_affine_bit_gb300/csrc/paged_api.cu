@@ -82,7 +82,7 @@ int check_cache(const affqmm_kv_cache* c, bool memory, bool blocks = false) {
 // The scales of a cache's blocks.
 struct Scales {
     float *k, *v;
-    int64_t page_stride, block_stride, head_stride;   // 0 for an axis of one
+    int32_t page_stride, block_stride, head_stride;   // 0 for an axis of one
     int shift;                                        // of a block's tokens
 };
 int check_scales(const affqmm_block_cache* c, bool memory, Scales* s) {
@@ -92,7 +92,7 @@ int check_scales(const affqmm_block_cache* c, bool memory, Scales* s) {
     int64_t stride[3] = {c->s_page_stride, c->s_block_stride, c->s_head_stride};
     for (int i = 0; i < 3; ++i) {
         if (size[i] == 1) stride[i] = 0;
-        else if (stride[i] < 1 || stride[i] >= (int64_t)1 << 38) return AFFQMM_E_SHAPE;
+        else if (stride[i] < 1 || stride[i] >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
     }
     // no two scales in one place: of two axes, the one with the larger stride steps over the other
     for (int i = 0; i < 3; ++i)
@@ -100,7 +100,7 @@ int check_scales(const affqmm_block_cache* c, bool memory, Scales* s) {
             const int in = stride[i] < stride[j] ? i : j, out = in == i ? j : i;
             if (stride[in] && stride[out] < stride[in] * size[in]) return AFFQMM_E_SHAPE;
         }
-    *s = {c->k_scales, c->v_scales, stride[0], stride[1], stride[2], shift};
+    *s = {c->k_scales, c->v_scales, (int32_t)stride[0], (int32_t)stride[1], (int32_t)stride[2], shift};
     if (!memory) return AFFQMM_OK;
     if (!c->k_scales || !c->v_scales) return AFFQMM_E_NULL;
     return aligned(c->k_scales, 4) && aligned(c->v_scales, 4) ? AFFQMM_OK : AFFQMM_E_ALIGN;
@@ -362,6 +362,7 @@ int attention(const affqmm_kv_cache* cache, const Scales* scales, const affqmm_l
         p.k_scales = scales->k, p.v_scales = scales->v;
         p.s_ps = scales->page_stride, p.s_bs = scales->block_stride, p.s_hs = scales->head_stride;
         p.block_shift = scales->shift;
+        p.s_pairs = p.s_hs == 1 && p.s_ps % 2 == 0 && p.s_bs % 2 == 0 && aligned(p.k_scales, 8) && aligned(p.v_scales, 8);
     }
     p.table = table;
     p.table_stride = table_stride;

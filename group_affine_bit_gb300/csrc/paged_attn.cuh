@@ -119,7 +119,7 @@ struct Cfg {
     static constexpr int KB = KBLOCKS;
     static constexpr int KEYS = 16 * W * KB;
     static constexpr int HEAD_TILE = KEYS * PITCH, TILE = HEADS * HEAD_TILE;
-    static constexpr int SCALES = BLOCKS ? 2 * HEADS * KEYS : 0;   // floats of a tile's scales: [K, V][head][block, at most KEYS]
+    static constexpr int SCALES = BLOCKS ? 2 * HEADS * KEYS : 0;   // floats of a tile's scales: [head][block, at most KEYS]{K, V}
     static constexpr int QBYTES = ROWS * DP * 2;
     static constexpr int QBUF = (DP == 512 && NA > 1) ? 1 : 2;
     static constexpr int PN = BYTES ? 1 : 2;           // numbers that make one P
@@ -127,14 +127,14 @@ struct Cfg {
     static constexpr int JOIN = 32;                    // most parts that a join takes at once
     static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PN * NA * KEYS * 16 + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
                                     JOIN * ROWS * 4 + (BLOCKS ? 448 : 512);   // and the barriers
-    static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= 32;   // registers allow two CTAs an SM
+    static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= (BLOCKS ? 48 : 32);   // registers allow two CTAs an SM
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
     static constexpr int CPS = (!PAIR && LIGHT && FIXED + 3 * TILE + 2 * SCALES * 4 <= HALF) ? 2 : 1;
     // With one CTA an SM, the rows go to two groups of consumer warps (where there are two row tiles), which share
     // the ring and q and nothing else: two warps to a scheduler, whose latencies overlap.
     static constexpr int NG = CPS == 1 && NA >= 2 ? 2 : 1;
     static constexpr int NT = NA / NG, GROWS = 8 * NT;           // row tiles, rows of a group
-    static constexpr int CONSUMERS = 32 * W * NG, THREADS = CONSUMERS + 96;
+    static constexpr int CONSUMERS = 32 * W * NG, THREADS = CONSUMERS + (BLOCKS ? 128 : 96);
     static constexpr int LOW = NT * KEYS * 16;         // from P's first numbers to the second
     static constexpr int PBYTES = PN * LOW;            // of a group: [PN][NT][keys][8 rows] of 16 bits
     static constexpr size_t ROOM = (CPS == 2 ? HALF : CTA_SMEM - STATIC_SMEM) - FIXED;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
     constexpr int KEYS = C::KEYS, THREADS = C::THREADS, PRODUCER = C::NG * W;   // the first warp that is no consumer
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* ring = smem;
-    float* scales = reinterpret_cast<float*>(ring + (size_t)C::NS * C::TILE);   // [NSC][K, V][head][KEYS]
+    float* scales = reinterpret_cast<float*>(ring + (size_t)C::NS * C::TILE);   // [NSC][head][KEYS]{K, V}
     uint8_t* qbuf = reinterpret_cast<uint8_t*>(scales + (size_t)C::NSC * C::SCALES);
     uint8_t* pbuf = qbuf + C::QBUF * C::QBYTES;
     float* red = reinterpret_cast<float*>(pbuf + 2 * C::NG * C::PBYTES);      // of each group: [W][rows] maxima
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
         mbar_init(drained, 1);
         mbar_init(never, 1);
         if constexpr (BLOCKS)
-            for (int s = 0; s < C::NSC; ++s) mbar_init(scaled(s), 32);
+            for (int s = 0; s < C::NSC; ++s) mbar_init(scaled(s), 1);
         fence_mbar_init();
         spoilt = 0;
     }
@@ -479,7 +479,6 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
         int slot = is_v ? 1 : 0;
         uint32_t phase = 0;
         int64_t turn = slot;                 // of the ring, over the whole run
-        int set = 0;                         // of scales
         while (ok && walk.next(p, units)) {
             const Span s = walk.s;
             const int32_t* table = p.table + (int64_t)walk.b * p.table_stride;
@@ -507,19 +506,6 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 const uint32_t dst = ring_u + (uint32_t)slot * C::TILE, bar = full(slot);
-                const int e0 = key0 >> p.page_shift;    // the tile's first entry, and the tile's pages in the lanes
-                int tile_page = 0;
-                if constexpr (BLOCKS)
-                    if (!is_v && p.page_shift >= 2) {
-#pragma unroll 1
-                        while (e0 - have >= 32) {
-                            have += 32;
-                            cur = nxt;
-                            nxt = entries(have + 32 + lane);
-                        }
-                        const int e = e0 - have + lane, x = __shfl_sync(~0u, cur, e & 31), y = __shfl_sync(~0u, nxt, e & 31);
-                        tile_page = e < 32 ? x : y;
-                    }
                 if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)max(0, i1 - i0) * C::HEADS * C::PANELS * box_bytes);
                 __syncwarp();
 #pragma unroll 1
@@ -546,32 +532,6 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
                                             bar);
                     }
                 }
-                if constexpr (BLOCKS)
-                    if (!is_v) {
-                        // the scales of the tile's blocks, K's and V's, a word to a lane; zeros where there is no page or
-                        // nothing that a query may see
-                        const int count_shift = max(0, (KEYS == 128 ? 7 : 6) - p.block_shift), count = 1 << count_shift;
-                        const uint32_t to = smem_u32(scales + set * C::SCALES);
-#pragma unroll 1
-                        for (int i0 = 0; i0 < 2 * C::HEADS * count; i0 += 32) {
-                            const int i = i0 + lane, block = i & (count - 1), which = i >> count_shift;   // which: V or K, head
-                            const int key = key0 + (block << p.block_shift), e = (key >> p.page_shift) - e0;
-                            int page = __shfl_sync(~0u, tile_page, e & 31);
-                            const bool seen = key < s.hi && key + (1 << p.block_shift) > s.lo;
-                            if (p.page_shift < 2) page = seen ? table[e0 + e] : -1;
-                            if (which < 2 * C::HEADS) {
-                                const bool there = seen && (uint32_t)page < (uint64_t)p.pages;
-                                const float* from = (which >= C::HEADS ? p.v_scales : p.k_scales) +
-                                                    (there ? page * p.s_ps + (int64_t)(((uint32_t)key & page_mask) >> p.block_shift) * p.s_bs +
-                                                                 (head0 + which % C::HEADS) * p.s_hs
-                                                           : 0);
-                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (uint32_t)(which * KEYS + block) * 4u),
-                                             "l"(from), "r"(there ? 4u : 0u) : "memory");
-                            }
-                        }
-                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(scaled(set)) : "memory");
-                        if (++set == C::NSC) set = 0;
-                    }
                 turn += 2;
                 slot += 2;
                 if (slot >= C::NS) slot -= C::NS, phase ^= 1u;
@@ -580,10 +540,113 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
         // The next kernel's CTAs may come as this one's end: what this kernel waited for is complete.
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // no copy is in flight when the CTA ends, whatever its consumers did
-        if constexpr (BLOCKS) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
         for (int64_t i = turn - 2; i >= 0 && i >= turn - C::NS; i -= 2)
             if (!mbar_wait(full((int)(i % C::NS)), (uint32_t)(i / C::NS) & 1u)) ok = false;
+        if (!ok && lane == 0) atomicOr(p.status, 1u);
+        return;
+    }
+    if (BLOCKS && wid == PRODUCER + 3) {
+        // ================= scales of each tile's blocks, K's and V's, to the set that goes with the K tile's slot, within
+        // bounds and V's as its logarithm.  The next tile's are loaded while this one's wait for their set.
+        constexpr int EACH = (C::HEADS * KEYS + 31) / 32;     // blocks of a tile to a lane, at most
+        const int count_shift = max(0, (KEYS == 128 ? 7 : 6) - p.block_shift), count = 1 << count_shift;   // of a head
+        const uint32_t page_mask = (1u << p.page_shift) - 1u;
+        int slot = 0, set = 0;
+        uint32_t phase = 0;
+        const int32_t* table = nullptr;
+        int head0 = 0, key0 = 0, have = 0, cur = 0, nxt = 0;
+        walk.t0 = walk.t1 = 0;
+        auto entry = [&](int e) {            // of a page that a query may see, -1 of any other
+            return ((int64_t)e << p.page_shift) < walk.s.hi && (((int64_t)e + 1) << p.page_shift) > walk.s.lo ? table[e] : -1;
+        };
+        float2 mine[EACH], next[EACH];
+        auto load = [&](float2 (&x)[EACH]) {
+            if (walk.t0 >= walk.t1) {
+                if (!walk.next(p, units)) return false;
+                table = p.table + (int64_t)walk.b * p.table_stride;
+                head0 = C::PAIR ? 2 * walk.u : over(walk.u, p.row_tiles, p.m_row_tiles);
+                key0 = walk.s.base + walk.t0 * KEYS;
+                have = ((key0 >> p.page_shift) & ~31) - 64, cur = nxt = -1;   // as the producers have them
+            }
+            const int e0 = key0 >> p.page_shift;
+            int tile_page = -1;              // the lane's entry of the tile, where a tile has 32 at most
+            if (p.page_shift >= 2) {
+#pragma unroll 1
+                while (e0 - have >= 32) {
+                    have += 32;
+                    cur = nxt;
+                    nxt = entry(have + 32 + lane);
+                }
+                const int e = e0 - have + lane, u = __shfl_sync(~0u, cur, e & 31), w = __shfl_sync(~0u, nxt, e & 31);
+                tile_page = e < 32 ? u : w;
+            }
+            const bool whole = key0 >= walk.s.lo && key0 + KEYS <= walk.s.hi;
+            // the lane's block `i` of the tile, of one head: where its scales are, or -1: zeros where there is no page, or
+            // nothing that a query may see
+            auto place = [&](int i, int head) {
+                const int key = key0 + ((i & (count - 1)) << p.block_shift), e = (key >> p.page_shift) - e0;
+                int page = __shfl_sync(~0u, tile_page, e & 31);
+                const bool seen = whole || (key < walk.s.hi && key + (1 << p.block_shift) > walk.s.lo);
+                if (p.page_shift < 2) page = seen ? table[e0 + e] : -1;
+                const int in_page = (int)(((uint32_t)key & page_mask) >> p.block_shift);
+                return seen && (uint32_t)page < (uint32_t)p.pages
+                           ? (int64_t)page * p.s_ps + (int64_t)in_page * p.s_bs + (int64_t)(head0 + head) * p.s_hs
+                           : -1;
+            };
+            if (C::PAIR && p.s_pairs) {
+                // the two heads' scales lie side by side: registers 2j and 2j + 1 are a block's two heads
+#pragma unroll
+                for (int j = 0; j < EACH / 2; ++j)
+                    if (32 * j < count) {
+                        const int64_t at = place(32 * j + lane, 0);
+                        float2 k = make_float2(0.f, 0.f), v = k;
+                        if (at >= 0 && 32 * j + lane < count) {
+                            k = *reinterpret_cast<const float2*>(p.k_scales + at);
+                            v = *reinterpret_cast<const float2*>(p.v_scales + at);
+                        }
+                        x[2 * j] = make_float2(k.x, v.x);
+                        x[2 * j + 1] = make_float2(k.y, v.y);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < EACH; ++j)
+                    if (32 * j < C::HEADS * count) {
+                        const int i = 32 * j + lane, head = i >> count_shift;
+                        const int64_t at = place(i, head);
+                        x[j] = make_float2(0.f, 0.f);
+                        if (at >= 0 && head < C::HEADS) x[j] = make_float2(p.k_scales[at], p.v_scales[at]);
+                    }
+            }
+            key0 += KEYS;
+            ++walk.t0;
+            return true;
+        };
+        bool more = load(next);
+        while (more) {
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) mine[j] = next[j];
+            more = load(next);
+            wait(empty(slot), phase ^ 1u);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            float2* of = reinterpret_cast<float2*>(scales + set * C::SCALES);
+            auto put = [&](int block, int head, float2 x) { of[head * KEYS + block] = make_float2(within_scales(x.x), __log2f(within_scales(x.y))); };
+            if (C::PAIR && p.s_pairs) {
+#pragma unroll
+                for (int j = 0; j < EACH; ++j)
+                    if (32 * (j >> 1) + lane < count) put(32 * (j >> 1) + lane, j & 1, mine[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < EACH; ++j)
+                    if (32 * j + lane < C::HEADS * count) put((32 * j + lane) & (count - 1), (32 * j + lane) >> count_shift, mine[j]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(scaled(set));
+            if (++set == C::NSC) set = 0;
+            slot += 2;
+            if (slot >= C::NS) slot -= C::NS, phase ^= 1u;
+        }
         if (!ok && lane == 0) atomicOr(p.status, 1u);
         return;
     }
@@ -971,6 +1034,9 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sT[kb][nt][e] = 0.f;
+                // of this thread's keys: K's scale; log2 of V's, by which P grows; and one over V's
+                float ks[KB][2], lv[KB][2], rv[KB][2];
+                if constexpr (BLOCKS) wait(scaled(set), sphase);
                 wait(full(slot), phase);
                 {
                     const uint32_t kt = ring_u + (uint32_t)slot * C::TILE + own_head;
@@ -1003,20 +1069,15 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
                         }
                     }
                 }
-                // the scales of this thread's keys: K's; log2 of V's, by which P grows; and one over V's
-                float ks[KB][2], lv[KB][2], rv[KB][2];
                 if constexpr (BLOCKS) {
-                    wait(scaled(set), sphase);
-                    const float* of = scales + set * C::SCALES + (C::PAIR ? group * KEYS : 0);
+                    const float2* of = reinterpret_cast<const float2*>(scales + set * C::SCALES) + (C::PAIR ? group * KEYS : 0);
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int block = (16 * (cw + W * kb) + g + 8 * h) >> p.block_shift;
-                            const float v = within_scales(of[C::HEADS * KEYS + block]);
-                            ks[kb][h] = within_scales(of[block]);
-                            lv[kb][h] = __log2f(v);
-                            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rv[kb][h]) : "f"(v));
+                            const float2 x = of[(16 * (cw + W * kb) + g + 8 * h) >> p.block_shift];
+                            ks[kb][h] = x.x, lv[kb][h] = x.y;
+                            rv[kb][h] = exp2_approx(-x.y);
                         }
                     if (++set == C::NSC) set = 0, sphase ^= 1u;
                 }

@@ -569,7 +569,7 @@ AFFQMM_API int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm
  *                 divides kv.page; token i of a page is in its block i / block
  *   s_*_stride    elements of the scales between pages, blocks and heads, in any
  *                 order in memory: each at least what the axis inside it takes up
- *                 (that of an axis of one does not matter)
+ *                 and below 2^31 (that of an axis of one does not matter)
  *   k_scales, v_scales  device, fp32 [pages, page / block, heads].  What lies
  *                 beyond 2^-48 and 2^48 counts as the nearer of the two where the
  *                 cache is attended over or added to (NaN: the first) */

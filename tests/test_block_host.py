@@ -42,7 +42,7 @@ REFUSALS = [
     (dict(pages=0), "AFFQMM_E_SHAPE"), (dict(k=None), "AFFQMM_E_NULL"), (dict(k=0x100008), "AFFQMM_E_ALIGN"), (dict(hs=136), "AFFQMM_E_ALIGN"),
     (dict(block=0), "AFFQMM_E_ARG"), (dict(block=3), "AFFQMM_E_ARG"), (dict(block=32), "AFFQMM_E_ARG"), (dict(block=-16), "AFFQMM_E_ARG"),
     (dict(page=256, block=256, ps=65536), "AFFQMM_E_ARG"), (dict(sps=0), "AFFQMM_E_SHAPE"), (dict(sps=1), "AFFQMM_E_SHAPE"), (dict(shs=0), "AFFQMM_E_SHAPE"),
-    (dict(shs=-1), "AFFQMM_E_SHAPE"), (dict(block=8, sbs=1), "AFFQMM_E_SHAPE"), (dict(block=8, sps=2, sbs=2), "AFFQMM_E_SHAPE"),
+    (dict(shs=-1), "AFFQMM_E_SHAPE"), (dict(sps=1 << 31), "AFFQMM_E_SHAPE"), (dict(block=8, sbs=1), "AFFQMM_E_SHAPE"), (dict(block=8, sps=2, sbs=2), "AFFQMM_E_SHAPE"),
     (dict(k_scales=None), "AFFQMM_E_NULL"), (dict(v_scales=None), "AFFQMM_E_NULL"), (dict(v_scales=0x2002), "AFFQMM_E_ALIGN")]
 
 
