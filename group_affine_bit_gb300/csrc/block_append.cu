@@ -23,8 +23,8 @@ namespace affqmm {
 namespace {
 
 constexpr int BA_THREADS = 128, BA_WARPS = BA_THREADS / 32;
-constexpr int HOLD = 4;                  // chunks of 16 values that a lane keeps between the maximum and the codes
-constexpr size_t BA_TABLE = 96 << 10;    // most shared memory for sines
+constexpr int HOLD = 4;                  // chunks of 16 values that a lane has in flight, and keeps while a block's maximum is found
+constexpr size_t BA_TABLE = 136 << 10;   // most shared memory for sines: all but those of 128 tokens at rotary 512
 
 // How a head's values pair: HALVES i with i + rotary / 2, in whole chunks of
 // 8 pairs (rotary a multiple of 16); NEIGHBOURS 2i with 2i + 1; ODD_HALVES as
@@ -32,7 +32,10 @@ constexpr size_t BA_TABLE = 96 << 10;    // most shared memory for sines
 enum Pairs { HALVES, NEIGHBOURS, ODD_HALVES };
 
 // Eight pairs of a head: chunk c has the pairs 8c .. 8c + 7, where values that do not turn are pairs of neighbours
-// (HALVES: of one run of eight and the next).
+// (HALVES: of one run of eight and the next).  Raw: as they are read, two runs of eight.
+struct Raw {
+    uint4 a, b;
+};
 struct Chunk {
     float a[8], b[8];
 };
@@ -45,33 +48,63 @@ __device__ __forceinline__ void runs_of(int c, int half, int& d0, int& d1) {
 }
 
 template <int PAIRS>
-__device__ __forceinline__ void load_chunk(const uint16_t* src, int c, int half, Chunk& x) {
+__device__ __forceinline__ Raw load_chunk(const uint16_t* src, int c, int half) {
+    Raw x;
     if constexpr (PAIRS == HALVES) {
         int d0, d1;
         runs_of(c, half, d0, d1);
-        unpack8(*reinterpret_cast<const uint4*>(src + d0), x.a);
-        unpack8(*reinterpret_cast<const uint4*>(src + d1), x.b);
+        x.a = *reinterpret_cast<const uint4*>(src + d0);
+        x.b = *reinterpret_cast<const uint4*>(src + d1);
     } else if constexpr (PAIRS == NEIGHBOURS) {
-        float lo[8], hi[8];
-        unpack8(*reinterpret_cast<const uint4*>(src + 16 * c), lo);
-        unpack8(*reinterpret_cast<const uint4*>(src + 16 * c + 8), hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x.a[e] = lo[2 * e], x.b[e] = lo[2 * e + 1], x.a[e + 4] = hi[2 * e], x.b[e + 4] = hi[2 * e + 1];
+        x.a = *reinterpret_cast<const uint4*>(src + 16 * c);
+        x.b = *reinterpret_cast<const uint4*>(src + 16 * c + 8);
     } else {
+        uint32_t a[8], b[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int i = 8 * c + e, d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
-            x.a[e] = __uint_as_float((uint32_t)src[d0] << 16);
-            x.b[e] = __uint_as_float((uint32_t)src[d1] << 16);
+            const int i = 8 * c + e;
+            a[e] = src[i < half ? i : 2 * i], b[e] = src[i < half ? i + half : 2 * i + 1];
         }
+        x.a = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
+        x.b = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+    }
+    return x;
+}
+template <int PAIRS>
+__device__ __forceinline__ void unpack(const Raw& r, Chunk& x) {
+    if constexpr (PAIRS == NEIGHBOURS) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.a[e] = bf_lo(w[e]), x.b[e] = bf_hi(w[e]);
+    } else {
+        unpack8(r.a, x.a);
+        unpack8(r.b, x.b);
     }
 }
 
-// The sines of chunk c's pairs, of a token's table.
+// The sine and cosine by which pair i of token t turns, from an eighth of a turn at most: its 2^-32 of a turn then
+// has 24 bits down to 2^-27 of one, so that a value seldom falls to the other side of a code's border.
+__device__ __forceinline__ void near_turn_of(const RopeParams& p, int64_t t, int i, float* sine, float* cosine) {
+    const int a = p.axis ? min((int)p.axis[i], p.axes - 1) : 0;
+    const int64_t pos = p.positions[a * p.pos_stride + t];
+    const uint32_t phase = (uint32_t)(((uint64_t)pos * (uint64_t)p.turns[i]) >> 32);   // of a turn, times 2^32
+    const uint32_t quarter = (phase + 0x20000000u) >> 30;
+    float s, c;
+    sincospif((float)(int32_t)(phase - (quarter << 30)) * 0x1p-31f, &s, &c);
+    if (quarter & 1u) {
+        const float x = s;
+        s = c, c = -x;
+    }
+    *sine = quarter & 2u ? -s : s;
+    *cosine = quarter & 2u ? -c : c;
+}
+
+// Chunk c turned, by a token's table of sines or, where that has no room for it, by sines made here (token t).
 template <int PAIRS>
-__device__ __forceinline__ void sines_of(int c, int half, const float* cosines, const float* sines, float (&co)[8], float (&si)[8]) {
+__device__ __forceinline__ void turn_chunk(Chunk& x, int c, int half, const float* cosines, const float* sines) {
+    if (8 * c >= half) return;
+    float co[8], si[8];
     if constexpr (PAIRS == HALVES) {
-        if (8 * c >= half) return;
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
             const float4 u = *reinterpret_cast<const float4*>(cosines + 8 * c + e), w = *reinterpret_cast<const float4*>(sines + 8 * c + e);
@@ -83,16 +116,23 @@ __device__ __forceinline__ void sines_of(int c, int half, const float* cosines, 
         for (int e = 0; e < 8; ++e)
             if (8 * c + e < half) co[e] = cosines[8 * c + e], si[e] = sines[8 * c + e];
     }
-}
-template <int PAIRS>
-__device__ __forceinline__ void turn_chunk(Chunk& x, int c, int half, const float (&co)[8], const float (&si)[8]) {
-    if (8 * c >= half) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         if (PAIRS != HALVES && 8 * c + e >= half) continue;
         const float a = x.a[e], b = x.b[e];
         x.a[e] = a * co[e] - b * si[e];
         x.b[e] = a * si[e] + b * co[e];
+    }
+}
+__device__ __forceinline__ void turn_chunk_far(const RopeParams& p, Chunk& x, int64_t t, int c, int half) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (8 * c + e >= half) continue;
+        float si, co;
+        near_turn_of(p, t, 8 * c + e, &si, &co);
+        const float a = x.a[e], b = x.b[e];
+        x.a[e] = a * co - b * si;
+        x.b[e] = a * si + b * co;
     }
 }
 
@@ -195,85 +235,90 @@ struct Grid {
     uint32_t m_chunks, m_half, m_parts, m_q_parts;
 };
 
-// One block's rows t .. t + n - 1 of the call, of one key head: x at `src` (rows src_ts apart), codes at `codes`.
-template <int PAIRS, bool I8>
-__device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, int64_t t, int n, bool fresh, const uint16_t* src, int64_t src_ts,
-                                            uint8_t* codes, float* scale_at, int half, const float* cosines, const float* sines) {
-    const int lane = threadIdx.x & 31, all = n * gr.chunks;
-    const int32_t* slots = p.rope.slots + t;
-    const int bs = p.block_shift;
-    const float old = fresh ? 0.f : fminf(fmaxf(*scale_at, kLeastScale), kMostScale);
-    auto chunk = [&](int i, Chunk& x) {
-        const int r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
-        load_chunk<PAIRS>(src + (int64_t)r * src_ts, c, half, x);
-        float co[8], si[8];
-        if (r < gr.table_rows) {
-            sines_of<PAIRS>(c, half, cosines + r * half, sines + r * half, co, si);
-        } else {
+// One block's rows t .. t + n - 1 of the call, of one key head.
+struct Rows {
+    const uint16_t* src;                 // rows `ts` apart
+    int64_t ts;
+    uint8_t* codes;                      // of the block's first token
+    float* scale;
+};
+
+template <int PAIRS>
+__device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int n, int first, int half, Raw (&raw)[HOLD]) {
+    const int all = n * gr.chunks;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (8 * c + e < half) turn_of(p.rope, t + r, 8 * c + e, si + e, co + e);
+    for (int j = 0; j < HOLD; ++j) {
+        const int i = first + 32 * j + (threadIdx.x & 31);
+        if (i < all) {
+            const int r = over(i, gr.m_chunks, gr.chunks);
+            raw[j] = load_chunk<PAIRS>(u.src + (int64_t)r * u.ts, i - r * gr.chunks, half);
         }
-        turn_chunk<PAIRS>(x, c, half, co, si);
+    }
+}
+
+// The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale.
+template <int PAIRS, bool I8>
+__device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, int64_t t, int n, bool fresh, const Rows& u, int half,
+                                            const float* cosines, const float* sines, Raw (&raw)[HOLD], float held) {
+    const int lane = threadIdx.x & 31, all = n * gr.chunks, bs = p.block_shift;
+    const float old = fresh ? 0.f : fminf(fmaxf(held, kLeastScale), kMostScale);
+    auto value = [&](int i, const Raw& w, Chunk& x, int& r, int& c) {
+        r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
+        unpack<PAIRS>(w, x);
+        if (r < gr.table_rows) turn_chunk<PAIRS>(x, c, half, cosines + r * half, sines + r * half);
+        else turn_chunk_far(p.rope, x, t + r, c, half);
     };
-    auto write = [&](int i, const Chunk& x, float by) {
-        const int r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
-        store_codes<PAIRS, I8>(codes + (int64_t)(slots[r] & ((1 << bs) - 1)) * p.rope.token_bytes, c, half, x, by);
-    };
-    Chunk held[HOLD];
     float top = 0.f;
-    const bool keep = all <= 32 * HOLD;
-    if (keep) {
+#pragma unroll 1
+    for (int first = 0; first < all; first += 32 * HOLD) {
+        if (first > 0) load_rows<PAIRS>(gr, u, n, first, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
-            if (lane + 32 * j < all) {
-                chunk(lane + 32 * j, held[j]);
-                top = fmaxf(top, top_of(held[j]));
+            if (first + 32 * j + lane < all) {
+                Chunk x;
+                int r, c;
+                value(first + 32 * j + lane, raw[j], x, r, c);
+                top = fmaxf(top, top_of(x));
             }
-    } else {
-#pragma unroll 1
-        for (int i = lane; i < all; i += 32) {
-            chunk(i, held[0]);
-            top = fmaxf(top, top_of(held[0]));
-        }
     }
     top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
     const float scale = fmaxf(old, scale_for<I8>(top));
-    if (lane == 0) *scale_at = scale;
+    if (lane == 0) *u.scale = scale;
     if (old > 0.f && old < scale) {
         // the block's codes to the new scale; those of this call's tokens are written after
         const float by = __fdiv_rn(old, scale);
-        const int pieces = p.rope.dim >> 4;
 #pragma unroll 1
-        for (int i = lane; i < pieces << bs; i += 32) {
-            const int r = over(i, gr.m_chunks, gr.chunks), c = i - r * pieces;
-            uint4* at = reinterpret_cast<uint4*>(codes + (int64_t)r * p.rope.token_bytes + 16 * c);
+        for (int i = lane; i < gr.chunks << bs; i += 32) {
+            const int r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
+            uint4* at = reinterpret_cast<uint4*>(u.codes + (int64_t)r * p.rope.token_bytes + 16 * c);
             uint4 w = *at;
-            for (uint32_t* u : {&w.x, &w.y, &w.z, &w.w}) {
+            for (uint32_t* k : {&w.x, &w.y, &w.z, &w.w}) {
                 float x[4];
-                values4<I8>(*u, x);
-                *u = codes4<I8>(x[0], x[1], x[2], x[3], by);
+                values4<I8>(*k, x);
+                *k = codes4<I8>(x[0], x[1], x[2], x[3], by);
             }
             *at = w;
         }
         __syncwarp();
     }
     const float by = __frcp_rn(scale);
-    if (keep) {
+#pragma unroll 1
+    for (int first = 0; first < all; first += 32 * HOLD) {
+        if (all > 32 * HOLD) load_rows<PAIRS>(gr, u, n, first, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
-            if (lane + 32 * j < all) write(lane + 32 * j, held[j], by);
-    } else {
-#pragma unroll 1
-        for (int i = lane; i < all; i += 32) {
-            chunk(i, held[0]);
-            write(i, held[0], by);
-        }
+            if (first + 32 * j + lane < all) {
+                Chunk x;
+                int r, c;
+                value(first + 32 * j + lane, raw[j], x, r, c);
+                const int place = p.rope.slots[t + r] & ((1 << bs) - 1);
+                store_codes<PAIRS, I8>(u.codes + (int64_t)place * p.rope.token_bytes, c, half, x, by);
+            }
     }
 }
 
 template <int PAIRS, bool I8>
-__global__ void __launch_bounds__(BA_THREADS) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
+__global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES ? 5 : 4) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
     extern __shared__ __align__(16) float table[];       // cosines, sines: [row][rotary / 2]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const RopeParams& r = p.rope;
@@ -283,68 +328,95 @@ __global__ void __launch_bounds__(BA_THREADS) block_append_kernel(const __grid_c
         // ================= q of one token
         const int at = (int)blockIdx.x - gr.kv_ctas;
         const int64_t t = over(at, gr.m_q_parts, gr.q_parts);
-        const int part = at - (int)t * gr.q_parts;
+        const int part = at - (int)t * gr.q_parts, all = r.heads_q * gr.chunks, step = gr.q_parts * BA_THREADS;
         float* sines = table + half;
-        for (int i = tid; i < half; i += BA_THREADS) turn_of(r, t, i, sines + i, cosines + i);
+        const uint16_t* q = r.q + t * r.q_ts;
+        uint16_t* out = r.out + t * r.o_ts;
+        int i = part * BA_THREADS + tid;
+        Raw w, next;
+        auto load = [&](int i) {
+            const int h = over(i, gr.m_chunks, gr.chunks);
+            return load_chunk<PAIRS>(q + h * r.q_hs, i - h * gr.chunks, half);
+        };
+        if (i < all) w = load(i);
+        for (int k = tid; k < half; k += BA_THREADS) near_turn_of(r, t, k, sines + k, cosines + k);
         __syncthreads();
-        for (int i = part * BA_THREADS + tid; i < r.heads_q * gr.chunks; i += gr.q_parts * BA_THREADS) {
+#pragma unroll 1
+        for (; i < all; i += step) {
+            if (i + step < all) next = load(i + step);
             const int h = over(i, gr.m_chunks, gr.chunks), c = i - h * gr.chunks;
             Chunk x;
-            load_chunk<PAIRS>(r.q + t * r.q_ts + h * r.q_hs, c, half, x);
-            float co[8], si[8];
-            sines_of<PAIRS>(c, half, cosines, sines, co, si);
-            turn_chunk<PAIRS>(x, c, half, co, si);
-            store_bf16<PAIRS>(r.out + t * r.o_ts + h * r.o_hs, c, half, x);
+            unpack<PAIRS>(w, x);
+            turn_chunk<PAIRS>(x, c, half, cosines, sines);
+            store_bf16<PAIRS>(out + h * r.o_hs, c, half, x);
+            w = next;
         }
         return;
     }
     // ================= k and v of the blocks that begin, for this call, in these rows
-    const int64_t t0 = (int64_t)over((int)blockIdx.x, gr.m_parts, gr.parts) * gr.rows;
-    const int part = (int)blockIdx.x - (int)(t0 / gr.rows) * gr.parts;
+    const int chunk_of_rows = over((int)blockIdx.x, gr.m_parts, gr.parts), part = (int)blockIdx.x - chunk_of_rows * gr.parts;
+    const int64_t t0 = (int64_t)chunk_of_rows * gr.rows;
     const int units = 2 * r.heads_kv, u0 = part * units / gr.parts, u1 = (part + 1) * units / gr.parts;   // k's heads, then v's
     const int bs = p.block_shift;
     float* sines = table + gr.table_rows * half;
 #pragma unroll 1
     for (int64_t t = t0; t < min(t0 + gr.rows, r.tokens); ++t) {
-        const int32_t slot = r.slots[t];
+        // lane l has the slot of token t - 1 + l
+        auto slot_at = [&](int64_t i) { return i >= 0 && i < r.tokens ? r.slots[i] : -1; };
+        const int32_t own = slot_at(t - 1 + lane), slot = __shfl_sync(~0u, own, 1), before = __shfl_sync(~0u, own, 0);
         const int64_t page = slot >> r.page_shift;
         if (slot < 0 || page >= r.pages) {
             if (slot != -1 && r.status && part == 0 && tid == 0) atomicOr(r.status, 2u);
             continue;
         }
         const int block = slot >> bs;
-        if (t > 0 && r.slots[t - 1] >= 0 && r.slots[t - 1] >> bs == block) continue;
+        if (before >= 0 && before >> bs == block) continue;
+        // how many of the tokens from t on lie in the block, and whether its first one is among them
         int n = 0;
         bool fresh = false;
-        for (;;) {
-            const int64_t next = t + n + lane;
-            const int32_t s = next < r.tokens ? r.slots[next] : -1;
-            const uint32_t same = __ballot_sync(~0u, s >= 0 && s >> bs == block), first = __ballot_sync(~0u, (s & ((1 << bs) - 1)) == 0);
+        for (int32_t s = own;;) {
+            const uint32_t skip = n == 0 ? 1u : 0u;                    // lane 0 of the first round
+            const uint32_t same = __ballot_sync(~0u, s >= 0 && s >> bs == block) | skip, first = __ballot_sync(~0u, (s & ((1 << bs) - 1)) == 0);
             const int run = same == ~0u ? 32 : __ffs(~same) - 1;
-            fresh |= (first & (run == 32 ? ~0u : (1u << run) - 1u)) != 0;
-            n += run;
+            fresh |= (first & ~skip & (run == 32 ? ~0u : (1u << run) - 1u)) != 0;
+            n += run - (int)skip;
             if (run < 32 || n >= 1 << bs) break;
+            s = slot_at(t + n + lane);
         }
         n = min(n, 1 << bs);                 // more would name a slot twice
+        const int first_of_block = (block << bs) & ((1 << r.page_shift) - 1);
+        const int64_t at = page * r.page_bytes + first_of_block * r.token_bytes, scale_at = page * p.s_ps + (int64_t)(first_of_block >> bs) * p.s_bs;
+        auto rows_of = [&](int u) {
+            const bool is_v = u >= r.heads_kv;
+            const int h = is_v ? u - r.heads_kv : u;
+            return is_v ? Rows{r.v + t * r.v_ts + h * r.v_hs, r.v_ts, r.vc + at + h * r.head_bytes, p.v_scales + scale_at + h * p.s_hs}
+                        : Rows{r.k + t * r.k_ts + h * r.k_hs, r.k_ts, r.kc + at + h * r.head_bytes, p.k_scales + scale_at + h * p.s_hs};
+        };
+        Raw raw[HOLD];
+        float held = 0.f;
+        Rows x = {};
+        auto load = [&](int u) {
+            x = rows_of(u);
+            held = *x.scale;
+            if (u < r.heads_kv) load_rows<PAIRS>(gr, x, n, 0, half, raw);
+            else load_rows<HALVES>(gr, x, n, 0, 0, raw);
+        };
+        int u = u0 + warp;
+        if (u < u1) load(u);
         if (u0 < r.heads_kv) {
             const int many = min(n, gr.table_rows) * half;
             for (int i = tid; i < many; i += BA_THREADS) {
                 const int row = over(i, gr.m_half, half);
-                turn_of(r, t + row, i - row * half, sines + i, cosines + i);
+                near_turn_of(r, t + row, i - row * half, sines + i, cosines + i);
             }
             __syncthreads();
         }
-        const int first_of_block = (block << bs) & ((1 << r.page_shift) - 1);
-        const int64_t at = page * r.page_bytes + first_of_block * r.token_bytes, scale_at = page * p.s_ps + (int64_t)(first_of_block >> bs) * p.s_bs;
-        for (int u = u0 + warp; u < u1; u += BA_WARPS) {
-            if (u < r.heads_kv)
-                write_block<PAIRS, I8>(p, gr, t, n, fresh, r.k + t * r.k_ts + u * r.k_hs, r.k_ts, r.kc + at + u * r.head_bytes,
-                                       p.k_scales + scale_at + u * p.s_hs, half, cosines, sines);
-            else {
-                const int h = u - r.heads_kv;
-                write_block<HALVES, I8>(p, gr, t, n, fresh, r.v + t * r.v_ts + h * r.v_hs, r.v_ts, r.vc + at + h * r.head_bytes,
-                                        p.v_scales + scale_at + h * p.s_hs, 0, cosines, sines);
-            }
+#pragma unroll 1
+        while (u < u1) {
+            if (u < r.heads_kv) write_block<PAIRS, I8>(p, gr, t, n, fresh, x, half, cosines, sines, raw, held);
+            else write_block<HALVES, I8>(p, gr, t, n, fresh, x, 0, cosines, sines, raw, held);
+            u += BA_WARPS;
+            if (u < u1) load(u);
         }
         __syncthreads();
     }
