@@ -22,7 +22,7 @@
 namespace affqmm {
 namespace {
 
-constexpr int BA_THREADS = 128, BA_WARPS = BA_THREADS / 32;
+constexpr int BA_THREADS = 256, BA_WARPS = BA_THREADS / 32;
 constexpr int HOLD = 4;                  // chunks of 16 values that a lane has in flight, and keeps while a block's maximum is found
 constexpr size_t BA_TABLE = 136 << 10;   // most shared memory for sines: all but those of 128 tokens at rotary 512
 
@@ -229,10 +229,10 @@ __device__ __forceinline__ float scale_for(float top) {
 
 struct Grid {
     int kv_ctas, rows, parts;            // of k and v: CTAs, rows of the call to a CTA, CTAs that share the heads
-    int q_parts;                         // CTAs to a token of q
+    int q_tokens, q_parts;               // of q: tokens to a CTA, or (one token) CTAs that share its heads
     int table_rows;                      // rows whose sines shared memory holds
     int chunks;                          // of a head
-    uint32_t m_chunks, m_half, m_parts, m_q_parts;
+    uint32_t m_chunks, m_half, m_parts, m_q_parts, m_heads_q;
 };
 
 // One block's rows t .. t + n - 1 of the call, of one key head.
@@ -243,12 +243,23 @@ struct Rows {
     float* scale;
 };
 
+// The warps that share a block's rows: `warps` of them, the `index`-th of the CTA's teams.
+struct Team {
+    int warps, index;
+    __device__ __forceinline__ int threads() const { return 32 * warps; }
+    __device__ __forceinline__ int thread() const { return (int)threadIdx.x & (threads() - 1); }
+    __device__ __forceinline__ void sync() const {
+        if (warps == 1) __syncwarp();
+        else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + index), "r"(threads()) : "memory");
+    }
+};
+
 template <int PAIRS>
-__device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int n, int first, int half, Raw (&raw)[HOLD]) {
+__device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int n, int first, int step, int half, Raw (&raw)[HOLD]) {
     const int all = n * gr.chunks;
 #pragma unroll
     for (int j = 0; j < HOLD; ++j) {
-        const int i = first + 32 * j + (threadIdx.x & 31);
+        const int i = first + step * j;
         if (i < all) {
             const int r = over(i, gr.m_chunks, gr.chunks);
             raw[j] = load_chunk<PAIRS>(u.src + (int64_t)r * u.ts, i - r * gr.chunks, half);
@@ -256,39 +267,46 @@ __device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int n, 
     }
 }
 
-// The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale.
-template <int PAIRS, bool I8>
+// The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale, `tops`: of the
+// CTA's warps.
+template <int PAIRS, bool I8, bool FAR>
 __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, int64_t t, int n, bool fresh, const Rows& u, int half,
-                                            const float* cosines, const float* sines, Raw (&raw)[HOLD], float held) {
-    const int lane = threadIdx.x & 31, all = n * gr.chunks, bs = p.block_shift;
+                                            const float* cosines, const float* sines, Raw (&raw)[HOLD], float held, const Team& team, float* tops) {
+    const int own = team.thread(), step = team.threads(), all = n * gr.chunks, bs = p.block_shift;
     const float old = fresh ? 0.f : fminf(fmaxf(held, kLeastScale), kMostScale);
     auto value = [&](int i, const Raw& w, Chunk& x, int& r, int& c) {
         r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
         unpack<PAIRS>(w, x);
-        if (r < gr.table_rows) turn_chunk<PAIRS>(x, c, half, cosines + r * half, sines + r * half);
+        if (!FAR || r < gr.table_rows) turn_chunk<PAIRS>(x, c, half, cosines + r * half, sines + r * half);
         else turn_chunk_far(p.rope, x, t + r, c, half);
     };
     float top = 0.f;
 #pragma unroll 1
-    for (int first = 0; first < all; first += 32 * HOLD) {
-        if (first > 0) load_rows<PAIRS>(gr, u, n, first, half, raw);
+    for (int first = own; first < all; first += step * HOLD) {
+        if (first != own) load_rows<PAIRS>(gr, u, n, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
-            if (first + 32 * j + lane < all) {
+            if (first + step * j < all) {
                 Chunk x;
                 int r, c;
-                value(first + 32 * j + lane, raw[j], x, r, c);
+                value(first + step * j, raw[j], x, r, c);
                 top = fmaxf(top, top_of(x));
             }
     }
     top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
+    if (team.warps > 1) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) tops[warp] = top;
+        team.sync();
+        for (int w = 0; w < team.warps; ++w) top = fmaxf(top, tops[team.index * team.warps + w]);
+    }
     const float scale = fmaxf(old, scale_for<I8>(top));
-    if (lane == 0) *u.scale = scale;
+    if (own == 0) *u.scale = scale;
     if (old > 0.f && old < scale) {
         // the block's codes to the new scale; those of this call's tokens are written after
         const float by = __fdiv_rn(old, scale);
 #pragma unroll 1
-        for (int i = lane; i < gr.chunks << bs; i += 32) {
+        for (int i = own; i < gr.chunks << bs; i += step) {
             const int r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
             uint4* at = reinterpret_cast<uint4*>(u.codes + (int64_t)r * p.rope.token_bytes + 16 * c);
             uint4 w = *at;
@@ -299,57 +317,72 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
             }
             *at = w;
         }
-        __syncwarp();
+        team.sync();
     }
     const float by = __frcp_rn(scale);
 #pragma unroll 1
-    for (int first = 0; first < all; first += 32 * HOLD) {
-        if (all > 32 * HOLD) load_rows<PAIRS>(gr, u, n, first, half, raw);
+    for (int first = own; first < all; first += step * HOLD) {
+        if (all > step * HOLD) load_rows<PAIRS>(gr, u, n, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
-            if (first + 32 * j + lane < all) {
+            if (first + step * j < all) {
                 Chunk x;
                 int r, c;
-                value(first + 32 * j + lane, raw[j], x, r, c);
+                value(first + step * j, raw[j], x, r, c);
                 const int place = p.rope.slots[t + r] & ((1 << bs) - 1);
                 store_codes<PAIRS, I8>(u.codes + (int64_t)place * p.rope.token_bytes, c, half, x, by);
             }
     }
 }
 
-template <int PAIRS, bool I8>
-__global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES ? 5 : 4) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
+// FAR: blocks whose tokens' sines do not all fit the table.
+template <int PAIRS, bool I8, bool FAR>
+__global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
     extern __shared__ __align__(16) float table[];       // cosines, sines: [row][rotary / 2]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const RopeParams& r = p.rope;
     const int half = r.rotary >> 1, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float* cosines = table;
     if ((int)blockIdx.x >= gr.kv_ctas) {
-        // ================= q of one token
-        const int at = (int)blockIdx.x - gr.kv_ctas;
-        const int64_t t = over(at, gr.m_q_parts, gr.q_parts);
-        const int part = at - (int)t * gr.q_parts, all = r.heads_q * gr.chunks, step = gr.q_parts * BA_THREADS;
-        float* sines = table + half;
-        const uint16_t* q = r.q + t * r.q_ts;
-        uint16_t* out = r.out + t * r.o_ts;
-        int i = part * BA_THREADS + tid;
-        Raw w, next;
-        auto load = [&](int i) {
-            const int h = over(i, gr.m_chunks, gr.chunks);
-            return load_chunk<PAIRS>(q + h * r.q_hs, i - h * gr.chunks, half);
+        // ================= q of a few tokens, or of a share of one's heads
+        const int at = (int)blockIdx.x - gr.kv_ctas, group = over(at, gr.m_q_parts, gr.q_parts);
+        const int64_t t0 = (int64_t)group * gr.q_tokens;
+        const int tokens = (int)min((int64_t)gr.q_tokens, r.tokens - t0), part = at - group * gr.q_parts;
+        const int all = tokens * r.heads_q * gr.chunks, step = gr.q_parts * BA_THREADS;
+        float* sines = table + gr.q_tokens * half;
+        auto place = [&](int i, int& token, int& h, int& c) {
+            const int row = over(i, gr.m_chunks, gr.chunks);
+            c = i - row * gr.chunks, token = over(row, gr.m_heads_q, r.heads_q), h = row - token * r.heads_q;
         };
-        if (i < all) w = load(i);
-        for (int k = tid; k < half; k += BA_THREADS) near_turn_of(r, t, k, sines + k, cosines + k);
+        Raw raw[HOLD];
+        auto load = [&](int first) {
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j)
+                if (first + j * step < all) {
+                    int token, h, c;
+                    place(first + j * step, token, h, c);
+                    raw[j] = load_chunk<PAIRS>(r.q + (t0 + token) * r.q_ts + h * r.q_hs, c, half);
+                }
+        };
+        int i = part * BA_THREADS + tid;
+        load(i);
+        for (int k = tid; k < tokens * half; k += BA_THREADS) {
+            const int token = over(k, gr.m_half, half);
+            near_turn_of(r, t0 + token, k - token * half, sines + k, cosines + k);
+        }
         __syncthreads();
 #pragma unroll 1
-        for (; i < all; i += step) {
-            if (i + step < all) next = load(i + step);
-            const int h = over(i, gr.m_chunks, gr.chunks), c = i - h * gr.chunks;
-            Chunk x;
-            unpack<PAIRS>(w, x);
-            turn_chunk<PAIRS>(x, c, half, cosines, sines);
-            store_bf16<PAIRS>(out + h * r.o_hs, c, half, x);
-            w = next;
+        for (; i < all; i += HOLD * step, load(i)) {
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j)
+                if (i + j * step < all) {
+                    int token, h, c;
+                    place(i + j * step, token, h, c);
+                    Chunk x;
+                    unpack<PAIRS>(raw[j], x);
+                    turn_chunk<PAIRS>(x, c, half, cosines + token * half, sines + token * half);
+                    store_bf16<PAIRS>(r.out + (t0 + token) * r.o_ts + h * r.o_hs, c, half, x);
+                }
         }
         return;
     }
@@ -359,31 +392,38 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES ? 5 : 4) block_app
     const int units = 2 * r.heads_kv, u0 = part * units / gr.parts, u1 = (part + 1) * units / gr.parts;   // k's heads, then v's
     const int bs = p.block_shift;
     float* sines = table + gr.table_rows * half;
+    __shared__ float tops[BA_WARPS];
+    // lane l has the slot of token t0 - 1 + l; the tokens that begin a block's rows
+    auto slot_at = [&](int64_t i) { return i >= 0 && i < r.tokens ? r.slots[i] : -1; };
+    const int32_t own = slot_at(t0 - 1 + lane), before = __shfl_up_sync(~0u, own, 1);
+    const bool there = own >= 0 && own >> r.page_shift < r.pages, mine = lane >= 1 && lane <= gr.rows;
+    uint32_t leaders = __ballot_sync(~0u, mine && there && !(before >= 0 && before >> bs == own >> bs));
+    if (mine && own != -1 && !there && r.status && part == 0 && warp == 0) atomicOr(r.status, 2u);
 #pragma unroll 1
-    for (int64_t t = t0; t < min(t0 + gr.rows, r.tokens); ++t) {
-        // lane l has the slot of token t - 1 + l
-        auto slot_at = [&](int64_t i) { return i >= 0 && i < r.tokens ? r.slots[i] : -1; };
-        const int32_t own = slot_at(t - 1 + lane), slot = __shfl_sync(~0u, own, 1), before = __shfl_sync(~0u, own, 0);
+    for (; leaders; leaders &= leaders - 1u) {
+        const int l = __ffs(leaders) - 1;
+        const int64_t t = t0 - 1 + l;
+        const int32_t slot = __shfl_sync(~0u, own, l);
         const int64_t page = slot >> r.page_shift;
-        if (slot < 0 || page >= r.pages) {
-            if (slot != -1 && r.status && part == 0 && tid == 0) atomicOr(r.status, 2u);
-            continue;
-        }
         const int block = slot >> bs;
-        if (before >= 0 && before >> bs == block) continue;
         // how many of the tokens from t on lie in the block, and whether its first one is among them
         int n = 0;
         bool fresh = false;
-        for (int32_t s = own;;) {
-            const uint32_t skip = n == 0 ? 1u : 0u;                    // lane 0 of the first round
-            const uint32_t same = __ballot_sync(~0u, s >= 0 && s >> bs == block) | skip, first = __ballot_sync(~0u, (s & ((1 << bs) - 1)) == 0);
-            const int run = same == ~0u ? 32 : __ffs(~same) - 1;
-            fresh |= (first & ~skip & (run == 32 ? ~0u : (1u << run) - 1u)) != 0;
-            n += run - (int)skip;
-            if (run < 32 || n >= 1 << bs) break;
+        int32_t s = own;
+        for (int from = l;; from = 0) {
+            const uint32_t behind = ~0u << from, same = __ballot_sync(~0u, s >= 0 && s >> bs == block), first = __ballot_sync(~0u, (s & ((1 << bs) - 1)) == 0);
+            const uint32_t other = ~same & behind, run = other ? (1u << (__ffs(other) - 1)) - 1u : ~0u;   // lanes before the first other one
+            fresh |= (first & run & behind) != 0;
+            n += __popc(run & behind);
+            if (other || n >= 1 << bs) break;
             s = slot_at(t + n + lane);
         }
         n = min(n, 1 << bs);                 // more would name a slot twice
+        // as many warps to a block's rows as keep them in registers
+        Team team = {1, 0};
+        while (team.warps < BA_WARPS && n * gr.chunks > 32 * HOLD * team.warps) team.warps *= 2;
+        team.index = warp / team.warps;
+        const int teams = BA_WARPS / team.warps;
         const int first_of_block = (block << bs) & ((1 << r.page_shift) - 1);
         const int64_t at = page * r.page_bytes + first_of_block * r.token_bytes, scale_at = page * p.s_ps + (int64_t)(first_of_block >> bs) * p.s_bs;
         auto rows_of = [&](int u) {
@@ -398,12 +438,13 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES ? 5 : 4) block_app
         auto load = [&](int u) {
             x = rows_of(u);
             held = *x.scale;
-            if (u < r.heads_kv) load_rows<PAIRS>(gr, x, n, 0, half, raw);
-            else load_rows<HALVES>(gr, x, n, 0, 0, raw);
+            const int turns = u < r.heads_kv ? half : 0;
+            if (PAIRS == HALVES || u < r.heads_kv) load_rows<PAIRS>(gr, x, n, team.thread(), team.threads(), turns, raw);
+            else load_rows<HALVES>(gr, x, n, team.thread(), team.threads(), 0, raw);
         };
-        int u = u0 + warp;
+        int u = u0 + team.index;
         if (u < u1) load(u);
-        if (u0 < r.heads_kv) {
+        if (u0 < u1 && u0 < r.heads_kv) {
             const int many = min(n, gr.table_rows) * half;
             for (int i = tid; i < many; i += BA_THREADS) {
                 const int row = over(i, gr.m_half, half);
@@ -413,10 +454,12 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES ? 5 : 4) block_app
         }
 #pragma unroll 1
         while (u < u1) {
-            if (u < r.heads_kv) write_block<PAIRS, I8>(p, gr, t, n, fresh, x, half, cosines, sines, raw, held);
-            else write_block<HALVES, I8>(p, gr, t, n, fresh, x, 0, cosines, sines, raw, held);
-            u += BA_WARPS;
+            const int turns = u < r.heads_kv ? half : 0;
+            if (PAIRS == HALVES || u < r.heads_kv) write_block<PAIRS, I8, FAR>(p, gr, t, n, fresh, x, turns, cosines, sines, raw, held, team, tops);
+            else write_block<HALVES, I8, false>(p, gr, t, n, fresh, x, 0, cosines, sines, raw, held, team, tops);
+            u += teams;
             if (u < u1) load(u);
+            if (team.warps > 1) team.sync();   // `tops` serves the next
         }
         __syncthreads();
     }
@@ -431,32 +474,40 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
     auto reciprocal = [](int d) { return d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u; };
     Grid g = {};
     g.chunks = r.dim / 16;
-    // k and v: CTAs enough that every SM has several, a warp to a unit at most, and then rows to each of them
-    const int units = 2 * r.heads_kv, most = (units + BA_WARPS - 1) / BA_WARPS;
-    int64_t parts = (4 * sms + r.tokens - 1) / r.tokens;
-    if (parts < 2) parts = 2;
-    g.parts = (int)(parts < most ? parts : most);
+    // k and v: parts enough that each SM has four CTAs with a block to write, but no more than give every team of a CTA
+    // (block_append_kernel) one key head; and several rows to a CTA where that still leaves CTAs enough to find the blocks
+    const int units = 2 * r.heads_kv, chunks = block * g.chunks;
+    int team = 1;
+    while (team < BA_WARPS && chunks > 32 * HOLD * team) team *= 2;
+    const int64_t want = ((int64_t)4 * sms * block + r.tokens - 1) / r.tokens;
+    const int most = (units * team + BA_WARPS - 1) / BA_WARPS;
+    g.parts = (int)(want < 2 ? 2 : want < most ? want : most);
     g.rows = r.tokens * g.parts > 16 * sms ? 8 : 1;
     g.kv_ctas = (int)((r.tokens + g.rows - 1) / g.rows) * g.parts;
     g.table_rows = half ? (int)(BA_TABLE / (8 * half)) : block;
     if (g.table_rows > block) g.table_rows = block;
-    // q: as many CTAs a token as fill the SMs and find a chunk for each thread
-    int64_t split = (2 * sms + r.tokens - 1) / r.tokens;
+    // q: several tokens to a CTA, or with few of them as many CTAs a token as fill the SMs and find a chunk for each thread
+    const int64_t split = (2 * sms + r.tokens - 1) / r.tokens;
     const int wide = (r.heads_q * g.chunks + BA_THREADS - 1) / BA_THREADS;
-    g.q_parts = (int)(split < wide ? split : wide);
+    g.q_tokens = r.tokens >= 16 * sms ? 4 : r.tokens >= 8 * sms ? 2 : 1;
+    g.q_parts = g.q_tokens > 1 ? 1 : (int)(split < wide ? split : wide);
     g.m_chunks = reciprocal(g.chunks), g.m_half = reciprocal(half), g.m_parts = reciprocal(g.parts), g.m_q_parts = reciprocal(g.q_parts);
-    const size_t smem = (size_t)(g.table_rows > 1 ? g.table_rows : 1) * 8 * half;
-    auto pick = [&](auto i8) {
-        constexpr bool I8 = decltype(i8)::value;
-        return pairs == HALVES ? block_append_kernel<HALVES, I8> : pairs == NEIGHBOURS ? block_append_kernel<NEIGHBOURS, I8>
-                                                                                       : block_append_kernel<ODD_HALVES, I8>;
+    g.m_heads_q = reciprocal(r.heads_q);
+    const int64_t q_ctas = (r.tokens + g.q_tokens - 1) / g.q_tokens * g.q_parts;
+    const size_t smem = (size_t)(g.table_rows > g.q_tokens ? g.table_rows : g.q_tokens) * 8 * half;
+    auto pick = [&](auto i8, auto far) {
+        constexpr bool I8 = decltype(i8)::value, FAR = decltype(far)::value;
+        return pairs == HALVES ? block_append_kernel<HALVES, I8, FAR> : pairs == NEIGHBOURS ? block_append_kernel<NEIGHBOURS, I8, FAR>
+                                                                                            : block_append_kernel<ODD_HALVES, I8, FAR>;
     };
-    auto* kernel = r.e4m3 ? pick(std::false_type{}) : pick(std::true_type{});
-    if (smem > 48 << 10) {
+    const bool far = g.table_rows < block;
+    auto* kernel = r.e4m3 ? (far ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{}))
+                          : (far ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{}));
+    if (smem > 40 << 10) {                   // the kernel has some of its own beside it
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BA_TABLE);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kernel, dim3((unsigned)(g.kv_ctas + r.tokens * g.q_parts)), BA_THREADS, smem, st, p, g);
+    return launch_pdl(kernel, dim3((unsigned)(g.kv_ctas + q_ctas)), BA_THREADS, smem, st, p, g);
 }
 
 }  // namespace affqmm

@@ -4,8 +4,9 @@
 //
 // Bound by memory: a value is read once (two bytes, or one) and written once
 // (two).  A CTA takes a few rows, whose requests, pages and places its first
-// threads find (the request by bisection of `starts`), and all heads of k and
-// v; a thread takes eight neighbouring values, 16 bytes to write.
+// threads find (the request by bisection of `starts`, which are brought to
+// shared memory first), and all heads of k and v; a thread takes eight
+// neighbouring values, 16 bytes to write.
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
 #include "rope_pieces.cuh"
@@ -13,7 +14,8 @@
 namespace affqmm {
 namespace {
 
-constexpr int PR_THREADS = 256, PR_ROWS = 8;
+constexpr int PR_THREADS = 256, PR_ROWS = 32;   // most rows of a CTA
+constexpr int PR_STARTS = 2048;                 // most requests whose starts shared memory holds
 
 // n / d by m = ceil(2^32 / d) where that is exact (m not 0)
 __device__ __forceinline__ int part_of(int n, uint32_t m, int d) { return m ? (int)__umulhi((uint32_t)n, m) : n / d; }
@@ -21,9 +23,9 @@ __device__ __forceinline__ int part_of(int n, uint32_t m, int d) { return m ? (i
 template <int KIND>
 __device__ __forceinline__ uint4 eight(const uint8_t* from, float scale) {
     if constexpr (KIND == READ_BF16) {
-        return *reinterpret_cast<const uint4*>(from);
+        return __ldcs(reinterpret_cast<const uint4*>(from));
     } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(from);
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(from));
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -36,26 +38,33 @@ __device__ __forceinline__ uint4 eight(const uint8_t* from, float scale) {
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(PR_THREADS) paged_read_kernel(const __grid_constant__ ReadParams p, int pieces, uint32_t m_pieces, int per_row,
-                                                                uint32_t m_row) {
+__global__ void __launch_bounds__(PR_THREADS) paged_read_kernel(const __grid_constant__ ReadParams p, int rows, int pieces, uint32_t m_pieces,
+                                                                int per_row, uint32_t m_row) {
     constexpr bool BLOCKS = KIND == READ_E4M3_BLOCKS || KIND == READ_I8_BLOCKS;
     __shared__ int64_t at[PR_ROWS], scale_at[PR_ROWS];   // of the row's token in the cache (-1: none), and of its block's scales
+    __shared__ int32_t kept[PR_STARTS];
     __shared__ int rows_here;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row0 = (int64_t)blockIdx.x * PR_ROWS;
+    const int64_t row0 = (int64_t)blockIdx.x * rows;
     const int tid = threadIdx.x;
-    if (tid < PR_ROWS) {
-        const int64_t row = row0 + tid, end = min((int64_t)p.starts[p.batch], p.rows);
-        if (tid == 0) rows_here = (int)max((int64_t)0, min((int64_t)PR_ROWS, end - row0));
-        if (p.status && row == 0 && p.starts[p.batch] > p.rows) atomicOr(p.status, 2u);
+    const int32_t* ends = p.starts + 1;                  // of the requests
+    if (p.batch <= PR_STARTS) {
+        for (int i = tid; i < p.batch; i += PR_THREADS) kept[i] = ends[i];
+        ends = kept;
+        __syncthreads();
+    }
+    if (tid < rows) {
+        const int64_t row = row0 + tid, end = min((int64_t)ends[p.batch - 1], p.rows);
+        if (tid == 0) rows_here = (int)max((int64_t)0, min((int64_t)rows, end - row0));
+        if (p.status && row == 0 && ends[p.batch - 1] > p.rows) atomicOr(p.status, 2u);
         if (row < end) {
             int lo = 0, hi = p.batch - 1;                // the first request that ends behind the row
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (p.starts[mid + 1] > row) hi = mid;
+                if (ends[mid] > row) hi = mid;
                 else lo = mid + 1;
             }
-            const int64_t token = (p.first ? (int64_t)p.first[lo] : 0) + row - p.starts[lo];
+            const int64_t token = (p.first ? (int64_t)p.first[lo] : 0) + row - (lo > 0 ? ends[lo - 1] : p.starts[0]);
             int page = -1;
             if (token >= 0 && token < (int64_t)p.wide << p.page_shift) page = p.table[lo * p.table_stride + (token >> p.page_shift)];
             const bool there = page >= 0 && page < p.pages;
@@ -82,21 +91,22 @@ __global__ void __launch_bounds__(PR_THREADS) paged_read_kernel(const __grid_con
             else if (KIND == READ_E4M3 && scales) scale = scales[h];
             w = eight<KIND>((is_v ? p.vc : p.kc) + at[r] + h * p.head_bytes + (KIND == READ_BF16 ? 2 * d : d), scale);
         }
-        *reinterpret_cast<uint4*>(to) = w;
+        __stcs(reinterpret_cast<uint4*>(to), w);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_read(const ReadParams& p, int kind, int sms, cudaStream_t st) {
-    (void)sms;
+    // a CTA's first threads find its rows while nothing is read: many rows to each, where there are enough of them
+    const int rows = p.rows >= 16 * PR_ROWS * (int64_t)sms ? PR_ROWS : p.rows >= 64 * (int64_t)sms ? 8 : 1;
     const int pieces = p.dim / 8, per_row = 2 * p.heads * pieces;
     auto reciprocal = [](int64_t most, int d) {          // of numbers below `most`
         return d > 1 && most * d < (int64_t)1 << 32 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u;
     };
     auto* kernel = kind == READ_BF16 ? paged_read_kernel<READ_BF16> : kind == READ_E4M3 ? paged_read_kernel<READ_E4M3>
                    : kind == READ_E4M3_BLOCKS ? paged_read_kernel<READ_E4M3_BLOCKS> : paged_read_kernel<READ_I8_BLOCKS>;
-    return launch_pdl(kernel, dim3((unsigned)((p.rows + PR_ROWS - 1) / PR_ROWS)), PR_THREADS, 0, st, p, pieces, reciprocal(per_row, pieces), per_row,
+    return launch_pdl(kernel, dim3((unsigned)((p.rows + rows - 1) / rows)), PR_THREADS, 0, st, p, rows, pieces, reciprocal(per_row, pieces), per_row,
                       reciprocal((int64_t)PR_ROWS * per_row, per_row));
 }
 
