@@ -7,6 +7,8 @@
 // threads find (the request by bisection of `starts`, which are brought to
 // shared memory first), and all heads of k and v; a thread takes eight
 // neighbouring values, 16 bytes to write.
+#include <type_traits>
+
 #include "affqmm_internal.h"
 #include "affqmm_paged.h"
 #include "rope_pieces.cuh"
@@ -14,18 +16,22 @@
 namespace affqmm {
 namespace {
 
-constexpr int PR_THREADS = 256, PR_ROWS = 32;   // most rows of a CTA
+constexpr int PR_THREADS = 256, PR_ROWS = 128;   // most rows of a CTA
+constexpr int PR_BATCH = 4;                     // pieces of k and of v that a thread has in flight
 constexpr int PR_STARTS = 2048;                 // most requests whose starts shared memory holds
 
 // n / d by m = ceil(2^32 / d) where that is exact (m not 0)
 __device__ __forceinline__ int part_of(int n, uint32_t m, int d) { return m ? (int)__umulhi((uint32_t)n, m) : n / d; }
 
+// Eight stored values as they are read, and as bf16.
 template <int KIND>
-__device__ __forceinline__ uint4 eight(const uint8_t* from, float scale) {
+using Stored = std::conditional_t<KIND == READ_BF16, uint4, uint2>;
+
+template <int KIND>
+__device__ __forceinline__ uint4 eight(const Stored<KIND>& w, float scale) {
     if constexpr (KIND == READ_BF16) {
-        return __ldcs(reinterpret_cast<const uint4*>(from));
+        return w;
     } else {
-        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(from));
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -38,7 +44,7 @@ __device__ __forceinline__ uint4 eight(const uint8_t* from, float scale) {
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(PR_THREADS) paged_read_kernel(const __grid_constant__ ReadParams p, int rows, int pieces, uint32_t m_pieces,
+__global__ void __launch_bounds__(PR_THREADS, 4) paged_read_kernel(const __grid_constant__ ReadParams p, int rows, int pieces, uint32_t m_pieces,
                                                                 int per_row, uint32_t m_row) {
     constexpr bool BLOCKS = KIND == READ_E4M3_BLOCKS || KIND == READ_I8_BLOCKS;
     __shared__ int64_t at[PR_ROWS], scale_at[PR_ROWS];   // of the row's token in the cache (-1: none), and of its block's scales
@@ -75,32 +81,56 @@ __global__ void __launch_bounds__(PR_THREADS) paged_read_kernel(const __grid_con
         }
     }
     __syncthreads();
-    const int all = rows_here * per_row;                 // a row's pieces of k, then of v
-#pragma unroll 4
-    for (int i = tid; i < all; i += PR_THREADS) {
-        const int r = part_of(i, m_row, per_row), x = i - r * per_row;
-        const bool is_v = x >= per_row >> 1;
-        const int y = is_v ? x - (per_row >> 1) : x, h = part_of(y, m_pieces, pieces), d = 8 * (y - h * pieces);
-        const int64_t row = row0 + r;
-        uint16_t* to = is_v ? p.v + row * p.v_ts + h * p.v_hs + d : p.k + row * p.k_ts + h * p.k_hs + d;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (at[r] >= 0) {
-            const float* scales = is_v ? p.v_scale : p.k_scale;
-            float scale = 1.f;
-            if (BLOCKS) scale = scales[scale_at[r] + h * p.s_hs];
-            else if (KIND == READ_E4M3 && scales) scale = scales[h];
-            w = eight<KIND>((is_v ? p.vc : p.kc) + at[r] + h * p.head_bytes + (KIND == READ_BF16 ? 2 * d : d), scale);
+    const int all = rows_here * per_row;                 // pieces of k, and of v
+#pragma unroll 1
+    for (int first = tid; first < all; first += PR_BATCH * PR_THREADS) {
+        Stored<KIND> k[PR_BATCH], v[PR_BATCH];
+        float ks[PR_BATCH], vs[PR_BATCH];
+        auto place = [&](int j, int& r, int& h, int& d) {
+            const int i = first + j * PR_THREADS;
+            r = part_of(i, m_row, per_row);
+            const int x = i - r * per_row;
+            h = part_of(x, m_pieces, pieces), d = 8 * (x - h * pieces);
+            return i < all;
+        };
+#pragma unroll
+        for (int j = 0; j < PR_BATCH; ++j) {
+            int r, h, d;
+            const bool there = place(j, r, h, d) && at[r] >= 0;
+            k[j] = v[j] = {};
+            ks[j] = vs[j] = 1.f;
+            if (there) {
+                const int64_t from = at[r] + h * p.head_bytes + (KIND == READ_BF16 ? 2 * d : d);
+                k[j] = __ldcs(reinterpret_cast<const Stored<KIND>*>(p.kc + from));
+                v[j] = __ldcs(reinterpret_cast<const Stored<KIND>*>(p.vc + from));
+                if (BLOCKS) {
+                    const int64_t of = scale_at[r] + h * p.s_hs;
+                    ks[j] = p.k_scale[of], vs[j] = p.v_scale[of];
+                } else if (KIND == READ_E4M3) {
+                    if (p.k_scale) ks[j] = p.k_scale[h];
+                    if (p.v_scale) vs[j] = p.v_scale[h];
+                }
+            }
         }
-        __stcs(reinterpret_cast<uint4*>(to), w);
+#pragma unroll
+        for (int j = 0; j < PR_BATCH; ++j) {
+            int r, h, d;
+            if (!place(j, r, h, d)) continue;
+            __stcs(reinterpret_cast<uint4*>(p.k + (row0 + r) * p.k_ts + h * p.k_hs + d), eight<KIND>(k[j], ks[j]));
+            __stcs(reinterpret_cast<uint4*>(p.v + (row0 + r) * p.v_ts + h * p.v_hs + d), eight<KIND>(v[j], vs[j]));
+        }
     }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_read(const ReadParams& p, int kind, int sms, cudaStream_t st) {
-    // a CTA's first threads find its rows while nothing is read: many rows to each, where there are enough of them
-    const int rows = p.rows >= 16 * PR_ROWS * (int64_t)sms ? PR_ROWS : p.rows >= 64 * (int64_t)sms ? 8 : 1;
-    const int pieces = p.dim / 8, per_row = 2 * p.heads * pieces;
+    // rows to a CTA: two rounds of its threads, as finding the rows takes a while; fewer where that would leave SMs without
+    // work, but not so few that threads are left without
+    const int pieces = p.dim / 8, per_row = p.heads * pieces;
+    const int64_t most = 2 * PR_BATCH * PR_THREADS / per_row, fair = p.rows / (4 * sms), least = PR_THREADS / per_row;
+    const int64_t want = fair < least ? least : fair < most ? fair : most;
+    const int rows = (int)(want < 1 ? 1 : want < PR_ROWS ? want : PR_ROWS);
     auto reciprocal = [](int64_t most, int d) {          // of numbers below `most`
         return d > 1 && most * d < (int64_t)1 << 32 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u;
     };
