@@ -26,13 +26,13 @@ constexpr int BA_THREADS = 256, BA_WARPS = BA_THREADS / 32;
 constexpr int HOLD = 4;                  // chunks of 16 values that a lane has in flight, and keeps while a block's maximum is found
 constexpr size_t BA_TABLE = 136 << 10;   // most shared memory for sines: all but those of 128 tokens at rotary 512
 
-// How a head's values pair: HALVES i with i + rotary / 2, in whole chunks of
-// 8 pairs (rotary a multiple of 16); NEIGHBOURS 2i with 2i + 1; ODD_HALVES as
-// HALVES, at any even rotary.
-enum Pairs { HALVES, NEIGHBOURS, ODD_HALVES };
+// How a head's values pair: HALVES i with i + rotary / 2, where values lie in
+// aligned runs of 8 (rotary a multiple of 16), 4 (of 8) or 1; NEIGHBOURS 2i
+// with 2i + 1.
+enum Pairs { NEIGHBOURS = 0, HALVES_1 = 1, HALVES_4 = 4, HALVES_8 = 8 };
 
 // Eight pairs of a head: chunk c has the pairs 8c .. 8c + 7, where values that do not turn are pairs of neighbours
-// (HALVES: of one run of eight and the next).  Raw: as they are read, two runs of eight.
+// (HALVES: of one run and the next).  Raw: as they are read.
 struct Raw {
     uint4 a, b;
 };
@@ -40,30 +40,40 @@ struct Chunk {
     float a[8], b[8];
 };
 
-// Where chunk c's two runs of eight values begin (HALVES).
-__device__ __forceinline__ void runs_of(int c, int half, int& d0, int& d1) {
-    const bool turns = 8 * c < half;
-    d0 = turns ? 8 * c : 16 * c;                    // 2 half + 16 (c - half / 8)
-    d1 = d0 + (turns ? half : 8);
+// Where the two runs that begin with pair i begin (HALVES).
+template <int RUN>
+__device__ __forceinline__ void runs_of(int i, int half, int& d0, int& d1) {
+    const bool turns = i < half;
+    d0 = turns ? i : 2 * i;                         // 2 half + 2 (i - half)
+    d1 = d0 + (turns ? half : RUN);
 }
 
 template <int PAIRS>
 __device__ __forceinline__ Raw load_chunk(const uint16_t* src, int c, int half) {
     Raw x;
-    if constexpr (PAIRS == HALVES) {
-        int d0, d1;
-        runs_of(c, half, d0, d1);
-        x.a = *reinterpret_cast<const uint4*>(src + d0);
-        x.b = *reinterpret_cast<const uint4*>(src + d1);
-    } else if constexpr (PAIRS == NEIGHBOURS) {
+    if constexpr (PAIRS == NEIGHBOURS) {
         x.a = *reinterpret_cast<const uint4*>(src + 16 * c);
         x.b = *reinterpret_cast<const uint4*>(src + 16 * c + 8);
+    } else if constexpr (PAIRS == HALVES_8) {
+        int d0, d1;
+        runs_of<8>(8 * c, half, d0, d1);
+        x.a = *reinterpret_cast<const uint4*>(src + d0);
+        x.b = *reinterpret_cast<const uint4*>(src + d1);
+    } else if constexpr (PAIRS == HALVES_4) {
+        int d0, d1;
+        runs_of<4>(8 * c, half, d0, d1);
+        const uint2 a = *reinterpret_cast<const uint2*>(src + d0), b = *reinterpret_cast<const uint2*>(src + d1);
+        runs_of<4>(8 * c + 4, half, d0, d1);
+        const uint2 e = *reinterpret_cast<const uint2*>(src + d0), f = *reinterpret_cast<const uint2*>(src + d1);
+        x.a = make_uint4(a.x, a.y, e.x, e.y);
+        x.b = make_uint4(b.x, b.y, f.x, f.y);
     } else {
         uint32_t a[8], b[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int i = 8 * c + e;
-            a[e] = src[i < half ? i : 2 * i], b[e] = src[i < half ? i + half : 2 * i + 1];
+            int d0, d1;
+            runs_of<1>(8 * c + e, half, d0, d1);
+            a[e] = src[d0], b[e] = src[d1];
         }
         x.a = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
         x.b = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
@@ -104,7 +114,7 @@ template <int PAIRS>
 __device__ __forceinline__ void turn_chunk(Chunk& x, int c, int half, const float* cosines, const float* sines) {
     if (8 * c >= half) return;
     float co[8], si[8];
-    if constexpr (PAIRS == HALVES) {
+    if constexpr (PAIRS == HALVES_8) {
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
             const float4 u = *reinterpret_cast<const float4*>(cosines + 8 * c + e), w = *reinterpret_cast<const float4*>(sines + 8 * c + e);
@@ -118,7 +128,7 @@ __device__ __forceinline__ void turn_chunk(Chunk& x, int c, int half, const floa
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        if (PAIRS != HALVES && 8 * c + e >= half) continue;
+        if (PAIRS != HALVES_8 && 8 * c + e >= half) continue;
         const float a = x.a[e], b = x.b[e];
         x.a[e] = a * co[e] - b * si[e];
         x.b[e] = a * si[e] + b * co[e];
@@ -158,41 +168,58 @@ __device__ __forceinline__ void values4(uint32_t w, float (&x)[4]) {
 
 template <int PAIRS, bool I8>
 __device__ __forceinline__ void store_codes(uint8_t* dst, int c, int half, const Chunk& x, float by) {
-    if constexpr (PAIRS == HALVES) {
-        int d0, d1;
-        runs_of(c, half, d0, d1);
-        *reinterpret_cast<uint2*>(dst + d0) = make_uint2(codes4<I8>(x.a[0], x.a[1], x.a[2], x.a[3], by), codes4<I8>(x.a[4], x.a[5], x.a[6], x.a[7], by));
-        *reinterpret_cast<uint2*>(dst + d1) = make_uint2(codes4<I8>(x.b[0], x.b[1], x.b[2], x.b[3], by), codes4<I8>(x.b[4], x.b[5], x.b[6], x.b[7], by));
-    } else if constexpr (PAIRS == NEIGHBOURS) {
+    if constexpr (PAIRS == NEIGHBOURS) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = codes4<I8>(x.a[2 * i], x.b[2 * i], x.a[2 * i + 1], x.b[2 * i + 1], by);
         *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
+        uint32_t a[2], b[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = 8 * c + e, d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
-            const uint32_t w = codes4<I8>(x.a[e], x.b[e], 0.f, 0.f, by);
-            dst[d0] = (uint8_t)w, dst[d1] = (uint8_t)(w >> 8);
+        for (int i = 0; i < 2; ++i) {
+            a[i] = codes4<I8>(x.a[4 * i], x.a[4 * i + 1], x.a[4 * i + 2], x.a[4 * i + 3], by);
+            b[i] = codes4<I8>(x.b[4 * i], x.b[4 * i + 1], x.b[4 * i + 2], x.b[4 * i + 3], by);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += PAIRS) {
+            int d0, d1;
+            runs_of<PAIRS>(8 * c + i, half, d0, d1);
+            if constexpr (PAIRS == HALVES_8) {
+                *reinterpret_cast<uint2*>(dst + d0) = make_uint2(a[0], a[1]);
+                *reinterpret_cast<uint2*>(dst + d1) = make_uint2(b[0], b[1]);
+            } else if constexpr (PAIRS == HALVES_4) {
+                *reinterpret_cast<uint32_t*>(dst + d0) = a[i >> 2];
+                *reinterpret_cast<uint32_t*>(dst + d1) = b[i >> 2];
+            } else {
+                dst[d0] = (uint8_t)(a[i >> 2] >> (8 * (i & 3)));
+                dst[d1] = (uint8_t)(b[i >> 2] >> (8 * (i & 3)));
+            }
         }
     }
 }
 template <int PAIRS>
 __device__ __forceinline__ void store_bf16(uint16_t* dst, int c, int half, const Chunk& x) {
-    if constexpr (PAIRS == HALVES) {
-        int d0, d1;
-        runs_of(c, half, d0, d1);
-        *reinterpret_cast<uint4*>(dst + d0) = make_uint4(bf2(x.a[0], x.a[1]), bf2(x.a[2], x.a[3]), bf2(x.a[4], x.a[5]), bf2(x.a[6], x.a[7]));
-        *reinterpret_cast<uint4*>(dst + d1) = make_uint4(bf2(x.b[0], x.b[1]), bf2(x.b[2], x.b[3]), bf2(x.b[4], x.b[5]), bf2(x.b[6], x.b[7]));
-    } else if constexpr (PAIRS == NEIGHBOURS) {
+    if constexpr (PAIRS == NEIGHBOURS) {
         *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(bf2(x.a[0], x.b[0]), bf2(x.a[1], x.b[1]), bf2(x.a[2], x.b[2]), bf2(x.a[3], x.b[3]));
         *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(bf2(x.a[4], x.b[4]), bf2(x.a[5], x.b[5]), bf2(x.a[6], x.b[6]), bf2(x.a[7], x.b[7]));
     } else {
+        uint32_t a[4], b[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = 8 * c + e, d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
-            const uint32_t w = bf2(x.a[e], x.b[e]);
-            dst[d0] = (uint16_t)w, dst[d1] = (uint16_t)(w >> 16);
+        for (int i = 0; i < 4; ++i) a[i] = bf2(x.a[2 * i], x.a[2 * i + 1]), b[i] = bf2(x.b[2 * i], x.b[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 8; i += PAIRS) {
+            int d0, d1;
+            runs_of<PAIRS>(8 * c + i, half, d0, d1);
+            if constexpr (PAIRS == HALVES_8) {
+                *reinterpret_cast<uint4*>(dst + d0) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4*>(dst + d1) = make_uint4(b[0], b[1], b[2], b[3]);
+            } else if constexpr (PAIRS == HALVES_4) {
+                *reinterpret_cast<uint2*>(dst + d0) = make_uint2(a[i >> 1], a[(i >> 1) + 1]);
+                *reinterpret_cast<uint2*>(dst + d1) = make_uint2(b[i >> 1], b[(i >> 1) + 1]);
+            } else {
+                dst[d0] = (uint16_t)(a[i >> 1] >> (16 * (i & 1)));
+                dst[d1] = (uint16_t)(b[i >> 1] >> (16 * (i & 1)));
+            }
         }
     }
 }
@@ -228,35 +255,55 @@ __device__ __forceinline__ float scale_for(float top) {
 }
 
 struct Grid {
-    int kv_ctas, rows, parts;            // of k and v: CTAs, rows of the call to a CTA, CTAs that share the heads
+    int kv_ctas, rows, parts;            // of k and v: CTAs, rows of the call to a CTA, CTAs that share k's (v's) heads
     int q_tokens, q_parts;               // of q: tokens to a CTA, or (one token) CTAs that share its heads
     int table_rows;                      // rows whose sines shared memory holds
     int chunks;                          // of a head
     uint32_t m_chunks, m_half, m_parts, m_q_parts, m_heads_q;
 };
 
-// One block's rows t .. t + n - 1 of the call, of one key head.
+// The threads that share a block's rows: `threads`, a power of two, the `index`-th of the CTA's teams.
+struct Team {
+    int threads, index;
+    __device__ __forceinline__ int thread() const { return (int)threadIdx.x & (threads - 1); }
+    __device__ __forceinline__ void sync() const {
+        if (threads <= 32) __syncwarp();
+        else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + index), "r"(threads) : "memory");
+    }
+    // The largest of the team's; `tops`: a word for each warp, free again after the team's next sync().
+    __device__ __forceinline__ float largest(float x, float* tops) const {
+        if (threads >= 32) {
+            x = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(x)));
+            if (threads == 32) return x;
+            if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = x;
+            sync();
+            for (int w = 0; w < threads >> 5; ++w) x = fmaxf(x, tops[index * (threads >> 5) + w]);
+            return x;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            const float y = __shfl_xor_sync(~0u, x, d);
+            if (d < threads) x = fmaxf(x, y);
+        }
+        return x;
+    }
+};
+
+// One block's rows of the call, of one key head: tokens t .. t + n - 1 (none: n = 0).
 struct Rows {
+    int64_t t;
+    int n;
+    bool fresh;                          // the block's first token is among them
     const uint16_t* src;                 // rows `ts` apart
     int64_t ts;
     uint8_t* codes;                      // of the block's first token
     float* scale;
-};
-
-// The warps that share a block's rows: `warps` of them, the `index`-th of the CTA's teams.
-struct Team {
-    int warps, index;
-    __device__ __forceinline__ int threads() const { return 32 * warps; }
-    __device__ __forceinline__ int thread() const { return (int)threadIdx.x & (threads() - 1); }
-    __device__ __forceinline__ void sync() const {
-        if (warps == 1) __syncwarp();
-        else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + index), "r"(threads()) : "memory");
-    }
+    int table;                           // the first one's row in the table of sines
 };
 
 template <int PAIRS>
-__device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int n, int first, int step, int half, Raw (&raw)[HOLD]) {
-    const int all = n * gr.chunks;
+__device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int first, int step, int half, Raw (&raw)[HOLD]) {
+    const int all = u.n * gr.chunks;
 #pragma unroll
     for (int j = 0; j < HOLD; ++j) {
         const int i = first + step * j;
@@ -267,23 +314,24 @@ __device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int n, 
     }
 }
 
-// The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale, `tops`: of the
-// CTA's warps.
+// The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale.  Every thread of
+// a warp calls it, whatever its team has to do.
 template <int PAIRS, bool I8, bool FAR>
-__device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, int64_t t, int n, bool fresh, const Rows& u, int half,
-                                            const float* cosines, const float* sines, Raw (&raw)[HOLD], float held, const Team& team, float* tops) {
-    const int own = team.thread(), step = team.threads(), all = n * gr.chunks, bs = p.block_shift;
-    const float old = fresh ? 0.f : fminf(fmaxf(held, kLeastScale), kMostScale);
+__device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, const Rows& u, int half, const float* cosines,
+                                            const float* sines, Raw (&raw)[HOLD], float held, const Team& team, float* tops) {
+    const int own = team.thread(), step = team.threads, all = u.n * gr.chunks, bs = p.block_shift;
+    const float old = u.fresh ? 0.f : fminf(fmaxf(held, kLeastScale), kMostScale);
     auto value = [&](int i, const Raw& w, Chunk& x, int& r, int& c) {
         r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
         unpack<PAIRS>(w, x);
-        if (!FAR || r < gr.table_rows) turn_chunk<PAIRS>(x, c, half, cosines + r * half, sines + r * half);
-        else turn_chunk_far(p.rope, x, t + r, c, half);
+        const int row = u.table + r;
+        if (!FAR || row < gr.table_rows) turn_chunk<PAIRS>(x, c, half, cosines + row * half, sines + row * half);
+        else turn_chunk_far(p.rope, x, u.t + r, c, half);
     };
     float top = 0.f;
 #pragma unroll 1
     for (int first = own; first < all; first += step * HOLD) {
-        if (first != own) load_rows<PAIRS>(gr, u, n, first, step, half, raw);
+        if (first != own) load_rows<PAIRS>(gr, u, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (first + step * j < all) {
@@ -293,16 +341,11 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
                 top = fmaxf(top, top_of(x));
             }
     }
-    top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));
-    if (team.warps > 1) {
-        const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) tops[warp] = top;
-        team.sync();
-        for (int w = 0; w < team.warps; ++w) top = fmaxf(top, tops[team.index * team.warps + w]);
-    }
+    __syncwarp();
+    top = team.largest(top, tops);
     const float scale = fmaxf(old, scale_for<I8>(top));
-    if (own == 0) *u.scale = scale;
-    if (old > 0.f && old < scale) {
+    if (own == 0 && all > 0) *u.scale = scale;
+    if (all > 0 && old > 0.f && old < scale) {
         // the block's codes to the new scale; those of this call's tokens are written after
         const float by = __fdiv_rn(old, scale);
 #pragma unroll 1
@@ -317,27 +360,28 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
             }
             *at = w;
         }
-        team.sync();
     }
+    team.sync();
     const float by = __frcp_rn(scale);
 #pragma unroll 1
     for (int first = own; first < all; first += step * HOLD) {
-        if (all > step * HOLD) load_rows<PAIRS>(gr, u, n, first, step, half, raw);
+        if (all > step * HOLD) load_rows<PAIRS>(gr, u, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (first + step * j < all) {
                 Chunk x;
                 int r, c;
                 value(first + step * j, raw[j], x, r, c);
-                const int place = p.rope.slots[t + r] & ((1 << bs) - 1);
+                const int place = p.rope.slots[u.t + r] & ((1 << bs) - 1);
                 store_codes<PAIRS, I8>(u.codes + (int64_t)place * p.rope.token_bytes, c, half, x, by);
             }
     }
+    __syncwarp();
 }
 
 // FAR: blocks whose tokens' sines do not all fit the table.
 template <int PAIRS, bool I8, bool FAR>
-__global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
+__global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
     extern __shared__ __align__(16) float table[];       // cosines, sines: [row][rotary / 2]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const RopeParams& r = p.rope;
@@ -386,82 +430,96 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES && !FAR ? 3 : 2) b
         }
         return;
     }
-    // ================= k and v of the blocks that begin, for this call, in these rows
-    const int chunk_of_rows = over((int)blockIdx.x, gr.m_parts, gr.parts), part = (int)blockIdx.x - chunk_of_rows * gr.parts;
-    const int64_t t0 = (int64_t)chunk_of_rows * gr.rows;
-    const int units = 2 * r.heads_kv, u0 = part * units / gr.parts, u1 = (part + 1) * units / gr.parts;   // k's heads, then v's
+    // ================= k, or v, of the blocks that begin, for this call, in these rows
+    const int window = over((int)blockIdx.x, gr.m_parts, 2 * gr.parts), part = (int)blockIdx.x - window * 2 * gr.parts;
+    const bool is_v = part >= gr.parts;
+    const int h0 = (is_v ? part - gr.parts : part) * r.heads_kv / gr.parts, heads = ((is_v ? part - gr.parts : part) + 1) * r.heads_kv / gr.parts - h0;
+    const int64_t t0 = (int64_t)window * gr.rows;
     const int bs = p.block_shift;
-    float* sines = table + gr.table_rows * half;
     __shared__ float tops[BA_WARPS];
-    // lane l has the slot of token t0 - 1 + l; the tokens that begin a block's rows
+    __shared__ int8_t leader[BA_WARPS][32];
+    // Lane l has the slot of token t0 - 1 + l.  A token of these whose predecessor lies in another block begins the rows of its
+    // block, as many as follow in it.
     auto slot_at = [&](int64_t i) { return i >= 0 && i < r.tokens ? r.slots[i] : -1; };
     const int32_t own = slot_at(t0 - 1 + lane), before = __shfl_up_sync(~0u, own, 1);
     const bool there = own >= 0 && own >> r.page_shift < r.pages, mine = lane >= 1 && lane <= gr.rows;
-    uint32_t leaders = __ballot_sync(~0u, mine && there && !(before >= 0 && before >> bs == own >> bs));
+    const bool follows = lane >= 1 && before >= 0 && before >> bs == own >> bs;
     if (mine && own != -1 && !there && r.status && part == 0 && warp == 0) atomicOr(r.status, 2u);
-#pragma unroll 1
-    for (; leaders; leaders &= leaders - 1u) {
-        const int l = __ffs(leaders) - 1;
-        const int64_t t = t0 - 1 + l;
+    const uint32_t leaders = __ballot_sync(~0u, mine && there && !follows);
+    if (leaders == 0) return;
+    const uint32_t following = __ballot_sync(~0u, follows), begins = __ballot_sync(~0u, (own & ((1 << bs) - 1)) == 0);
+    const uint32_t stop = lane < 31 ? ~following >> (lane + 1) : 0u;     // the first token behind that does not follow
+    int n = stop && lane + __ffs(stop) < 32 ? __ffs(stop) : 32 - lane;
+    bool fresh = (begins >> lane & (n == 32 ? ~0u : (1u << n) - 1u)) != 0;
+    const int last = 31 - __clz(leaders);
+    if (last + __shfl_sync(~0u, n, last) == 32 && 32 - last < 1 << bs) {
+        // the last block's rows may go on behind lane 31
+        const int block = __shfl_sync(~0u, own, last) >> bs;
+        int more = 0;
+        bool any = false;
+        for (;;) {
+            const int32_t s = slot_at(t0 + 31 + more + lane);
+            const uint32_t other = ~__ballot_sync(~0u, s >= 0 && s >> bs == block), first = __ballot_sync(~0u, (s & ((1 << bs) - 1)) == 0);
+            const int run = other ? __ffs(other) - 1 : 32;
+            any |= (first & (run == 32 ? ~0u : (1u << run) - 1u)) != 0;
+            more += run;
+            if (run < 32 || more >= 1 << bs) break;
+        }
+        if (lane == last) n += more, fresh |= any;
+    }
+    n = min(n, 1 << bs);                     // more would name a slot twice
+    if (leaders >> lane & 1u) leader[warp][__popc(leaders & ((1u << lane) - 1u))] = (int8_t)lane;
+    __syncwarp();
+    const int most = __reduce_max_sync(~0u, leaders >> lane & 1u ? n : 0), total = __popc(leaders) * heads, first_lane = __ffs(leaders) - 1;
+    // As many threads to a block's rows as keep them in registers, or find something to do when each has a team.
+    Team team = {1, 0};
+    while (team.threads < BA_THREADS && (most * gr.chunks > HOLD * team.threads || (most * gr.chunks > team.threads && 2 * team.threads * total <= BA_THREADS)))
+        team.threads *= 2;
+    team.index = tid / team.threads;
+    const int teams = BA_THREADS / team.threads;
+    float* sines = table + gr.table_rows * half;
+    const int turns = is_v ? 0 : half;
+    Raw raw[HOLD];
+    float held = 0.f;
+    Rows x;
+    auto load = [&](int i) {                 // the team's i-th block and head
+        const int which = i < total ? i / heads : 0, h = h0 + i - which * heads, l = leader[warp][which];
         const int32_t slot = __shfl_sync(~0u, own, l);
+        x.n = __shfl_sync(~0u, n, l);
+        x.fresh = __shfl_sync(~0u, (int)fresh, l) != 0;
+        if (i >= total) {
+            x.n = 0;
+            return;
+        }
         const int64_t page = slot >> r.page_shift;
-        const int block = slot >> bs;
-        // how many of the tokens from t on lie in the block, and whether its first one is among them
-        int n = 0;
-        bool fresh = false;
-        int32_t s = own;
-        for (int from = l;; from = 0) {
-            const uint32_t behind = ~0u << from, same = __ballot_sync(~0u, s >= 0 && s >> bs == block), first = __ballot_sync(~0u, (s & ((1 << bs) - 1)) == 0);
-            const uint32_t other = ~same & behind, run = other ? (1u << (__ffs(other) - 1)) - 1u : ~0u;   // lanes before the first other one
-            fresh |= (first & run & behind) != 0;
-            n += __popc(run & behind);
-            if (other || n >= 1 << bs) break;
-            s = slot_at(t + n + lane);
-        }
-        n = min(n, 1 << bs);                 // more would name a slot twice
-        // as many warps to a block's rows as keep them in registers
-        Team team = {1, 0};
-        while (team.warps < BA_WARPS && n * gr.chunks > 32 * HOLD * team.warps) team.warps *= 2;
-        team.index = warp / team.warps;
-        const int teams = BA_WARPS / team.warps;
-        const int first_of_block = (block << bs) & ((1 << r.page_shift) - 1);
-        const int64_t at = page * r.page_bytes + first_of_block * r.token_bytes, scale_at = page * p.s_ps + (int64_t)(first_of_block >> bs) * p.s_bs;
-        auto rows_of = [&](int u) {
-            const bool is_v = u >= r.heads_kv;
-            const int h = is_v ? u - r.heads_kv : u;
-            return is_v ? Rows{r.v + t * r.v_ts + h * r.v_hs, r.v_ts, r.vc + at + h * r.head_bytes, p.v_scales + scale_at + h * p.s_hs}
-                        : Rows{r.k + t * r.k_ts + h * r.k_hs, r.k_ts, r.kc + at + h * r.head_bytes, p.k_scales + scale_at + h * p.s_hs};
-        };
-        Raw raw[HOLD];
-        float held = 0.f;
-        Rows x = {};
-        auto load = [&](int u) {
-            x = rows_of(u);
-            held = *x.scale;
-            const int turns = u < r.heads_kv ? half : 0;
-            if (PAIRS == HALVES || u < r.heads_kv) load_rows<PAIRS>(gr, x, n, team.thread(), team.threads(), turns, raw);
-            else load_rows<HALVES>(gr, x, n, team.thread(), team.threads(), 0, raw);
-        };
-        int u = u0 + team.index;
-        if (u < u1) load(u);
-        if (u0 < u1 && u0 < r.heads_kv) {
-            const int many = min(n, gr.table_rows) * half;
-            for (int i = tid; i < many; i += BA_THREADS) {
-                const int row = over(i, gr.m_half, half);
-                near_turn_of(r, t + row, i - row * half, sines + i, cosines + i);
-            }
-            __syncthreads();
-        }
-#pragma unroll 1
-        while (u < u1) {
-            const int turns = u < r.heads_kv ? half : 0;
-            if (PAIRS == HALVES || u < r.heads_kv) write_block<PAIRS, I8, FAR>(p, gr, t, n, fresh, x, turns, cosines, sines, raw, held, team, tops);
-            else write_block<HALVES, I8, false>(p, gr, t, n, fresh, x, 0, cosines, sines, raw, held, team, tops);
-            u += teams;
-            if (u < u1) load(u);
-            if (team.warps > 1) team.sync();   // `tops` serves the next
+        const int in_page = (slot >> bs << bs) & ((1 << r.page_shift) - 1);
+        x.t = t0 - 1 + l;
+        x.table = l - first_lane;
+        x.ts = is_v ? r.v_ts : r.k_ts;
+        x.src = (is_v ? r.v : r.k) + x.t * x.ts + h * (is_v ? r.v_hs : r.k_hs);
+        x.codes = (is_v ? r.vc : r.kc) + page * r.page_bytes + in_page * r.token_bytes + h * r.head_bytes;
+        x.scale = (is_v ? p.v_scales : p.k_scales) + page * p.s_ps + (int64_t)(in_page >> bs) * p.s_bs + h * p.s_hs;
+        held = *x.scale;
+        if (PAIRS == HALVES_8 || !is_v) load_rows<PAIRS>(gr, x, team.thread(), team.threads, turns, raw);
+        else load_rows<HALVES_8>(gr, x, team.thread(), team.threads, 0, raw);
+    };
+    int i = team.index;
+    load(i);
+    if (!is_v) {
+        const int rows = last + __shfl_sync(~0u, n, last) - first_lane, many = min(rows, gr.table_rows) * half;
+        for (int k = tid; k < many; k += BA_THREADS) {
+            const int row = over(k, gr.m_half, half);
+            near_turn_of(r, min(t0 - 1 + first_lane + row, r.tokens - 1), k - row * half, sines + k, cosines + k);
         }
         __syncthreads();
+    }
+#pragma unroll 1
+    for (int round = 0; round < total; round += teams) {
+        if (PAIRS == HALVES_8 || !is_v) write_block<PAIRS, I8, FAR>(p, gr, x, turns, cosines, sines, raw, held, team, tops);
+        else write_block<HALVES_8, I8, false>(p, gr, x, 0, cosines, sines, raw, held, team, tops);
+        i += teams;
+        if (round + teams < total) load(i);
+        if (team.threads > 32) team.sync();  // `tops` serves the next
     }
 }
 
@@ -469,38 +527,38 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES && !FAR ? 3 : 2) b
 
 cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) {
     const RopeParams& r = p.rope;
-    const int pairs = r.neighbour ? NEIGHBOURS : r.rotary % 16 == 0 ? HALVES : ODD_HALVES;
+    const int pairs = r.neighbour ? NEIGHBOURS : r.rotary % 16 == 0 ? HALVES_8 : r.rotary % 8 == 0 ? HALVES_4 : HALVES_1;
     const int half = r.rotary / 2, block = 1 << p.block_shift;
     auto reciprocal = [](int d) { return d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0u; };
     Grid g = {};
     g.chunks = r.dim / 16;
-    // k and v: parts enough that each SM has four CTAs with a block to write, but no more than give every team of a CTA
-    // (block_append_kernel) one key head; and several rows to a CTA where that still leaves CTAs enough to find the blocks
-    const int units = 2 * r.heads_kv, chunks = block * g.chunks;
-    int team = 1;
-    while (team < BA_WARPS && chunks > 32 * HOLD * team) team *= 2;
-    const int64_t want = ((int64_t)4 * sms * block + r.tokens - 1) / r.tokens;
-    const int most = (units * team + BA_WARPS - 1) / BA_WARPS;
-    g.parts = (int)(want < 2 ? 2 : want < most ? want : most);
-    g.rows = r.tokens * g.parts > 16 * sms ? 8 : 1;
-    g.kv_ctas = (int)((r.tokens + g.rows - 1) / g.rows) * g.parts;
+    // k and v: some rows to a CTA, so that a CTA of short blocks has several and one in which none begins is soon done; and
+    // parts that share the heads, where there are few CTAs even if a block begins in each row (a decode step of 64 tokens:
+    // 3.3 us; with a part for each of 8 heads 8.4), or so many rows that they are prompts' and most blocks are whole
+    g.rows = r.tokens >= 32 * sms ? 16 : r.tokens >= 8 * sms ? 8 : r.tokens >= 2 * sms ? 2 : 1;
+    const int64_t whole = (r.tokens + block - 1) / block;
+    const int64_t want = r.tokens >= 8 * sms ? (sms + whole - 1) / whole : 3 * sms * g.rows / (4 * r.tokens);
+    g.parts = (int)(want < 1 ? 1 : want < r.heads_kv ? want : r.heads_kv);
+    g.kv_ctas = (int)((r.tokens + g.rows - 1) / g.rows) * 2 * g.parts;
     g.table_rows = half ? (int)(BA_TABLE / (8 * half)) : block;
-    if (g.table_rows > block) g.table_rows = block;
+    if (g.table_rows > block + g.rows - 1) g.table_rows = block + g.rows - 1;
     // q: several tokens to a CTA, or with few of them as many CTAs a token as fill the SMs and find a chunk for each thread
     const int64_t split = (2 * sms + r.tokens - 1) / r.tokens;
     const int wide = (r.heads_q * g.chunks + BA_THREADS - 1) / BA_THREADS;
     g.q_tokens = r.tokens >= 16 * sms ? 4 : r.tokens >= 8 * sms ? 2 : 1;
     g.q_parts = g.q_tokens > 1 ? 1 : (int)(split < wide ? split : wide);
-    g.m_chunks = reciprocal(g.chunks), g.m_half = reciprocal(half), g.m_parts = reciprocal(g.parts), g.m_q_parts = reciprocal(g.q_parts);
+    g.m_chunks = reciprocal(g.chunks), g.m_half = reciprocal(half), g.m_parts = reciprocal(2 * g.parts), g.m_q_parts = reciprocal(g.q_parts);
     g.m_heads_q = reciprocal(r.heads_q);
     const int64_t q_ctas = (r.tokens + g.q_tokens - 1) / g.q_tokens * g.q_parts;
     const size_t smem = (size_t)(g.table_rows > g.q_tokens ? g.table_rows : g.q_tokens) * 8 * half;
     auto pick = [&](auto i8, auto far) {
         constexpr bool I8 = decltype(i8)::value, FAR = decltype(far)::value;
-        return pairs == HALVES ? block_append_kernel<HALVES, I8, FAR> : pairs == NEIGHBOURS ? block_append_kernel<NEIGHBOURS, I8, FAR>
-                                                                                            : block_append_kernel<ODD_HALVES, I8, FAR>;
+        return pairs == HALVES_8   ? block_append_kernel<HALVES_8, I8, FAR>
+               : pairs == HALVES_4 ? block_append_kernel<HALVES_4, I8, FAR>
+               : pairs == HALVES_1 ? block_append_kernel<HALVES_1, I8, FAR>
+                                   : block_append_kernel<NEIGHBOURS, I8, FAR>;
     };
-    const bool far = g.table_rows < block;
+    const bool far = half && g.table_rows < block + g.rows - 1;
     auto* kernel = r.e4m3 ? (far ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{}))
                           : (far ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{}));
     if (smem > 40 << 10) {                   // the kernel has some of its own beside it
