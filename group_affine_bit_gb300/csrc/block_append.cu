@@ -109,22 +109,23 @@ __device__ __forceinline__ void near_turn_of(const RopeParams& p, int64_t t, int
     *cosine = quarter & 2u ? -c : c;
 }
 
-// Chunk c turned, by a token's table of sines or, where that has no room for it, by sines made here (token t).
+// A token's table of sines, of `groups` = ceil(rotary / 16) chunks: the cosines of a chunk's first four pairs, chunk behind
+// chunk, then those of its last four, then the sines in the same way, so that neighbouring lanes read neighbouring words.
+__device__ __forceinline__ int cosine_at(int pair, int groups) { return (pair >> 2 & 1) * 4 * groups + (pair >> 3) * 4 + (pair & 3); }
+__device__ __forceinline__ void put_sines(const RopeParams& p, int64_t t, int pair, int groups, float* row) {
+    float* at = row + cosine_at(pair, groups);
+    near_turn_of(p, t, pair, at + 8 * groups, at);
+}
+// Chunk c turned by it.
 template <int PAIRS>
-__device__ __forceinline__ void turn_chunk(Chunk& x, int c, int half, const float* cosines, const float* sines) {
+__device__ __forceinline__ void turn_chunk(Chunk& x, int c, int half, int groups, const float* row) {
     if (8 * c >= half) return;
     float co[8], si[8];
-    if constexpr (PAIRS == HALVES_8) {
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(cosines + 8 * c + e), w = *reinterpret_cast<const float4*>(sines + 8 * c + e);
-            co[e] = u.x, co[e + 1] = u.y, co[e + 2] = u.z, co[e + 3] = u.w;
-            si[e] = w.x, si[e + 1] = w.y, si[e + 2] = w.z, si[e + 3] = w.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (8 * c + e < half) co[e] = cosines[8 * c + e], si[e] = sines[8 * c + e];
+    for (int e = 0; e < 8; e += 4) {                // pairs that do not turn: whatever is there
+        const float4 u = *reinterpret_cast<const float4*>(row + (e + 0) * groups + 4 * c), w = *reinterpret_cast<const float4*>(row + (e + 8) * groups + 4 * c);
+        co[e] = u.x, co[e + 1] = u.y, co[e + 2] = u.z, co[e + 3] = u.w;
+        si[e] = w.x, si[e + 1] = w.y, si[e + 2] = w.z, si[e + 3] = w.w;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -259,7 +260,8 @@ struct Grid {
     int q_tokens, q_parts;               // of q: tokens to a CTA, or (one token) CTAs that share its heads
     int table_rows;                      // rows whose sines shared memory holds
     int chunks;                          // of a head
-    uint32_t m_chunks, m_half, m_parts, m_q_parts, m_heads_q;
+    int groups;                          // chunks of a head that turn, the last perhaps in part
+    uint32_t m_chunks, m_half, m_parts, m_q_parts;
 };
 
 // The threads that share a block's rows: `threads`, a power of two, the `index`-th of the CTA's teams.
@@ -317,15 +319,15 @@ __device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int fir
 // The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale.  Every thread of
 // a warp calls it, whatever its team has to do.
 template <int PAIRS, bool I8, bool FAR>
-__device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, const Rows& u, int half, const float* cosines,
-                                            const float* sines, Raw (&raw)[HOLD], float held, const Team& team, float* tops) {
+__device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, const Rows& u, int half, const float* table,
+                                            Raw (&raw)[HOLD], float held, const Team& team, float* tops) {
     const int own = team.thread(), step = team.threads, all = u.n * gr.chunks, bs = p.block_shift;
     const float old = u.fresh ? 0.f : fminf(fmaxf(held, kLeastScale), kMostScale);
     auto value = [&](int i, const Raw& w, Chunk& x, int& r, int& c) {
         r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
         unpack<PAIRS>(w, x);
         const int row = u.table + r;
-        if (!FAR || row < gr.table_rows) turn_chunk<PAIRS>(x, c, half, cosines + row * half, sines + row * half);
+        if (!FAR || row < gr.table_rows) turn_chunk<PAIRS>(x, c, half, gr.groups, table + row * 16 * gr.groups);
         else turn_chunk_far(p.rope, x, u.t + r, c, half);
     };
     float top = 0.f;
@@ -382,51 +384,45 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
 // FAR: blocks whose tokens' sines do not all fit the table.
 template <int PAIRS, bool I8, bool FAR>
 __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
-    extern __shared__ __align__(16) float table[];       // cosines, sines: [row][rotary / 2]
+    extern __shared__ __align__(16) float table[];       // sines of a few tokens
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const RopeParams& r = p.rope;
     const int half = r.rotary >> 1, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float* cosines = table;
     if ((int)blockIdx.x >= gr.kv_ctas) {
-        // ================= q of a few tokens, or of a share of one's heads
+        // ================= q of a few tokens, or of a share of one's heads: a thread takes a chunk of each token
         const int at = (int)blockIdx.x - gr.kv_ctas, group = over(at, gr.m_q_parts, gr.q_parts);
         const int64_t t0 = (int64_t)group * gr.q_tokens;
         const int tokens = (int)min((int64_t)gr.q_tokens, r.tokens - t0), part = at - group * gr.q_parts;
-        const int all = tokens * r.heads_q * gr.chunks, step = gr.q_parts * BA_THREADS;
-        float* sines = table + gr.q_tokens * half;
-        auto place = [&](int i, int& token, int& h, int& c) {
-            const int row = over(i, gr.m_chunks, gr.chunks);
-            c = i - row * gr.chunks, token = over(row, gr.m_heads_q, r.heads_q), h = row - token * r.heads_q;
-        };
+        const int all = r.heads_q * gr.chunks, step = gr.q_parts * BA_THREADS;
+        const uint16_t* q = r.q + t0 * r.q_ts;
+        uint16_t* out = r.out + t0 * r.o_ts;
         Raw raw[HOLD];
-        auto load = [&](int first) {
+        int h, c;
+        auto load = [&](int i) {
+            h = over(i, gr.m_chunks, gr.chunks), c = i - h * gr.chunks;
 #pragma unroll
             for (int j = 0; j < HOLD; ++j)
-                if (first + j * step < all) {
-                    int token, h, c;
-                    place(first + j * step, token, h, c);
-                    raw[j] = load_chunk<PAIRS>(r.q + (t0 + token) * r.q_ts + h * r.q_hs, c, half);
-                }
+                if (j < tokens) raw[j] = load_chunk<PAIRS>(q + j * r.q_ts + h * r.q_hs, c, half);
         };
         int i = part * BA_THREADS + tid;
-        load(i);
+        if (i < all) load(i);
         for (int k = tid; k < tokens * half; k += BA_THREADS) {
             const int token = over(k, gr.m_half, half);
-            near_turn_of(r, t0 + token, k - token * half, sines + k, cosines + k);
+            put_sines(r, t0 + token, k - token * half, gr.groups, table + token * 16 * gr.groups);
         }
         __syncthreads();
 #pragma unroll 1
-        for (; i < all; i += HOLD * step, load(i)) {
+        while (i < all) {
 #pragma unroll
             for (int j = 0; j < HOLD; ++j)
-                if (i + j * step < all) {
-                    int token, h, c;
-                    place(i + j * step, token, h, c);
+                if (j < tokens) {
                     Chunk x;
                     unpack<PAIRS>(raw[j], x);
-                    turn_chunk<PAIRS>(x, c, half, cosines + token * half, sines + token * half);
-                    store_bf16<PAIRS>(r.out + (t0 + token) * r.o_ts + h * r.o_hs, c, half, x);
+                    turn_chunk<PAIRS>(x, c, half, gr.groups, table + j * 16 * gr.groups);
+                    store_bf16<PAIRS>(out + j * r.o_ts + h * r.o_hs, c, half, x);
                 }
+            i += step;
+            if (i < all) load(i);
         }
         return;
     }
@@ -477,7 +473,6 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
         team.threads *= 2;
     team.index = tid / team.threads;
     const int teams = BA_THREADS / team.threads;
-    float* sines = table + gr.table_rows * half;
     const int turns = is_v ? 0 : half;
     Raw raw[HOLD];
     float held = 0.f;
@@ -509,14 +504,14 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
         const int rows = last + __shfl_sync(~0u, n, last) - first_lane, many = min(rows, gr.table_rows) * half;
         for (int k = tid; k < many; k += BA_THREADS) {
             const int row = over(k, gr.m_half, half);
-            near_turn_of(r, min(t0 - 1 + first_lane + row, r.tokens - 1), k - row * half, sines + k, cosines + k);
+            put_sines(r, min(t0 - 1 + first_lane + row, r.tokens - 1), k - row * half, gr.groups, table + row * 16 * gr.groups);
         }
         __syncthreads();
     }
 #pragma unroll 1
     for (int round = 0; round < total; round += teams) {
-        if (PAIRS == HALVES_8 || !is_v) write_block<PAIRS, I8, FAR>(p, gr, x, turns, cosines, sines, raw, held, team, tops);
-        else write_block<HALVES_8, I8, false>(p, gr, x, 0, cosines, sines, raw, held, team, tops);
+        if (PAIRS == HALVES_8 || !is_v) write_block<PAIRS, I8, FAR>(p, gr, x, turns, table, raw, held, team, tops);
+        else write_block<HALVES_8, I8, false>(p, gr, x, 0, table, raw, held, team, tops);
         i += teams;
         if (round + teams < total) load(i);
         if (team.threads > 32) team.sync();  // `tops` serves the next
@@ -540,7 +535,8 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
     const int64_t want = r.tokens >= 8 * sms ? (sms + whole - 1) / whole : 3 * sms * g.rows / (4 * r.tokens);
     g.parts = (int)(want < 1 ? 1 : want < r.heads_kv ? want : r.heads_kv);
     g.kv_ctas = (int)((r.tokens + g.rows - 1) / g.rows) * 2 * g.parts;
-    g.table_rows = half ? (int)(BA_TABLE / (8 * half)) : block;
+    g.groups = (half + 7) / 8;
+    g.table_rows = half ? (int)(BA_TABLE / (64 * g.groups)) : block;
     if (g.table_rows > block + g.rows - 1) g.table_rows = block + g.rows - 1;
     // q: several tokens to a CTA, or with few of them as many CTAs a token as fill the SMs and find a chunk for each thread
     const int64_t split = (2 * sms + r.tokens - 1) / r.tokens;
@@ -548,9 +544,8 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
     g.q_tokens = r.tokens >= 16 * sms ? 4 : r.tokens >= 8 * sms ? 2 : 1;
     g.q_parts = g.q_tokens > 1 ? 1 : (int)(split < wide ? split : wide);
     g.m_chunks = reciprocal(g.chunks), g.m_half = reciprocal(half), g.m_parts = reciprocal(2 * g.parts), g.m_q_parts = reciprocal(g.q_parts);
-    g.m_heads_q = reciprocal(r.heads_q);
     const int64_t q_ctas = (r.tokens + g.q_tokens - 1) / g.q_tokens * g.q_parts;
-    const size_t smem = (size_t)(g.table_rows > g.q_tokens ? g.table_rows : g.q_tokens) * 8 * half;
+    const size_t smem = (size_t)(g.table_rows > g.q_tokens ? g.table_rows : g.q_tokens) * 64 * g.groups;
     auto pick = [&](auto i8, auto far) {
         constexpr bool I8 = decltype(i8)::value, FAR = decltype(far)::value;
         return pairs == HALVES_8   ? block_append_kernel<HALVES_8, I8, FAR>
