@@ -23,7 +23,8 @@ namespace affqmm {
 namespace {
 
 constexpr int BA_THREADS = 256, BA_WARPS = BA_THREADS / 32;
-constexpr int HOLD = 4;                  // chunks of 16 values that a lane has in flight, and keeps while a block's maximum is found
+constexpr int HOLD = 4;                  // chunks of 16 values that a lane keeps between a block's maximum and its codes
+constexpr int Q_TOKENS = 4;              // tokens of q to a CTA, at most
 constexpr size_t BA_TABLE = 136 << 10;   // most shared memory for sines: all but those of 128 tokens at rotary 512
 
 // How a head's values pair: HALVES i with i + rotary / 2, where values lie in
@@ -396,12 +397,12 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
         const int all = r.heads_q * gr.chunks, step = gr.q_parts * BA_THREADS;
         const uint16_t* q = r.q + t0 * r.q_ts;
         uint16_t* out = r.out + t0 * r.o_ts;
-        Raw raw[HOLD];
+        Raw raw[Q_TOKENS];
         int h, c;
         auto load = [&](int i) {
             h = over(i, gr.m_chunks, gr.chunks), c = i - h * gr.chunks;
 #pragma unroll
-            for (int j = 0; j < HOLD; ++j)
+            for (int j = 0; j < Q_TOKENS; ++j)
                 if (j < tokens) raw[j] = load_chunk<PAIRS>(q + j * r.q_ts + h * r.q_hs, c, half);
         };
         int i = part * BA_THREADS + tid;
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
 #pragma unroll 1
         while (i < all) {
 #pragma unroll
-            for (int j = 0; j < HOLD; ++j)
+            for (int j = 0; j < Q_TOKENS; ++j)
                 if (j < tokens) {
                     Chunk x;
                     unpack<PAIRS>(raw[j], x);
@@ -502,6 +503,7 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
     load(i);
     if (!is_v) {
         const int rows = last + __shfl_sync(~0u, n, last) - first_lane, many = min(rows, gr.table_rows) * half;
+#pragma unroll 4
         for (int k = tid; k < many; k += BA_THREADS) {
             const int row = over(k, gr.m_half, half);
             put_sines(r, min(t0 - 1 + first_lane + row, r.tokens - 1), k - row * half, gr.groups, table + row * 16 * gr.groups);
@@ -541,7 +543,7 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
     // q: several tokens to a CTA, or with few of them as many CTAs a token as fill the SMs and find a chunk for each thread
     const int64_t split = (2 * sms + r.tokens - 1) / r.tokens;
     const int wide = (r.heads_q * g.chunks + BA_THREADS - 1) / BA_THREADS;
-    g.q_tokens = r.tokens >= 16 * sms ? 4 : r.tokens >= 8 * sms ? 2 : 1;
+    g.q_tokens = r.tokens >= 16 * sms ? Q_TOKENS : r.tokens >= 8 * sms ? 2 : 1;
     g.q_parts = g.q_tokens > 1 ? 1 : (int)(split < wide ? split : wide);
     g.m_chunks = reciprocal(g.chunks), g.m_half = reciprocal(half), g.m_parts = reciprocal(2 * g.parts), g.m_q_parts = reciprocal(g.q_parts);
     const int64_t q_ctas = (r.tokens + g.q_tokens - 1) / g.q_tokens * g.q_parts;
