@@ -1,7 +1,7 @@
 #!/usr/bin/env python
 """The attention half of a decoder's layers served from a paged cache.
 
-    python examples/paged_decode.py [--batch 16] [--prompt 256] [--answer 64] [--layers 4]
+    python examples/paged_decode.py [--batch 16] [--prompt 256] [--answer 64] [--layers 4] [--e4m3 | --int8]
 
 Each layer is what the library runs between a layer's input and its residual sum:
 the stacked q/k/v projection (affqmm_run_stacked), rotary positions with the append
@@ -9,8 +9,10 @@ to the cache (affqmm_rope_append), attention over the pages (affqmm_paged_attent
 and the o projection (affqmm_run).  A step's slots and positions are planned once
 for all layers (affqmm_paged_plan).  Prompts go in chunks of equal length; the
 answer's steps are one captured CUDA graph, which the lengths on the GPU drive: the
-host sends nothing but the replay.  Norms and feed-forward blocks are left out, and
-the weights are synthetic.
+host sends nothing but the replay.  The cache is bf16, e4m3 with a scale for each
+head (--e4m3), or int8 with a scale for each block of tokens and head that is made as
+the cache is written (--int8, affqmm_block_append and affqmm_block_attention).  Norms
+and feed-forward blocks are left out, and the weights are synthetic.
 """
 from __future__ import annotations
 
@@ -38,6 +40,9 @@ class Layer:
         for i, (n, k) in enumerate(shapes):
             codes, scales, biases = synth.affine_table(bits, group, n, k, synth.generator(seed + i))
             self.tables.append(api.pack(codes.cuda(), scales.cuda(), biases.cuda(), bits, group))
+        if kv_dtype == torch.int8:
+            self.cache = api.BlockCache.empty(pages, page, kv_heads, dim)
+            return
         scale = [torch.full((kv_heads,), 1 / 16, device="cuda") for _ in "kv"] if kv_dtype == torch.float8_e4m3fn else [None, None]
         self.cache = api.KVCache.empty(pages, page, kv_heads, dim, kv_dtype, k_scale=scale[0], v_scale=scale[1])
 
@@ -107,12 +112,13 @@ def main():
     ap.add_argument("--answer", type=int, default=64)
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--hidden", type=int, default=5376)
-    ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
+    ap.add_argument("--e4m3", action="store_true", help="a cache of 8-bit floats")
+    ap.add_argument("--int8", action="store_true", help="a cache of 8-bit integers with a scale for each block of tokens")
     args = ap.parse_args()
     page, longest = 32, args.prompt + args.answer
     pages = args.batch * -(-longest // page)
     server = Server(args.layers, args.batch, args.hidden, heads=32, kv_heads=8, dim=256, page=page, pages=pages, longest=longest,
-                    kv_dtype=torch.float8_e4m3fn if args.e4m3 else torch.bfloat16)
+                    kv_dtype=torch.int8 if args.int8 else torch.float8_e4m3fn if args.e4m3 else torch.bfloat16)
     g = torch.Generator(device="cuda").manual_seed(0)
     chunk = 8
     for at in range(0, args.prompt, chunk):

@@ -348,27 +348,36 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
     top = team.largest(top, tops);
     const float scale = fmaxf(old, scale_for<I8>(top));
     if (own == 0 && all > 0) *u.scale = scale;
-    if (all > 0 && old > 0.f && old < scale) {
+    const bool grows = all > 0 && old > 0.f && old < scale;
+    if (grows) {
         // the block's codes to the new scale; those of this call's tokens are written after
         const float by = __fdiv_rn(old, scale);
+        auto at = [&](int i) {
+            const int r = over(i, gr.m_chunks, gr.chunks);
+            return reinterpret_cast<uint4*>(u.codes + (int64_t)r * p.rope.token_bytes + 16 * (i - r * gr.chunks));
+        };
 #pragma unroll 1
-        for (int i = own; i < gr.chunks << bs; i += step) {
-            const int r = over(i, gr.m_chunks, gr.chunks), c = i - r * gr.chunks;
-            uint4* at = reinterpret_cast<uint4*>(u.codes + (int64_t)r * p.rope.token_bytes + 16 * c);
-            uint4 w = *at;
-            for (uint32_t* k : {&w.x, &w.y, &w.z, &w.w}) {
-                float x[4];
-                values4<I8>(*k, x);
-                *k = codes4<I8>(x[0], x[1], x[2], x[3], by);
-            }
-            *at = w;
+        for (int first = own; first < gr.chunks << bs; first += HOLD * step) {
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j)       // in flight together, in the rows' place
+                if (first + j * step < gr.chunks << bs) raw[j].a = *at(first + j * step);
+#pragma unroll
+            for (int j = 0; j < HOLD; ++j)
+                if (first + j * step < gr.chunks << bs) {
+                    for (uint32_t* k : {&raw[j].a.x, &raw[j].a.y, &raw[j].a.z, &raw[j].a.w}) {
+                        float x[4];
+                        values4<I8>(*k, x);
+                        *k = codes4<I8>(x[0], x[1], x[2], x[3], by);
+                    }
+                    *at(first + j * step) = raw[j].a;
+                }
         }
     }
     team.sync();
     const float by = __frcp_rn(scale);
 #pragma unroll 1
     for (int first = own; first < all; first += step * HOLD) {
-        if (all > step * HOLD) load_rows<PAIRS>(gr, u, first, step, half, raw);
+        if (grows || all > step * HOLD) load_rows<PAIRS>(gr, u, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (first + step * j < all) {
@@ -468,9 +477,12 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
     if (leaders >> lane & 1u) leader[warp][__popc(leaders & ((1u << lane) - 1u))] = (int8_t)lane;
     __syncwarp();
     const int most = __reduce_max_sync(~0u, leaders >> lane & 1u ? n : 0), total = __popc(leaders) * heads, first_lane = __ffs(leaders) - 1;
-    // As many threads to a block's rows as keep them in registers, or find something to do when each has a team.
+    // As many threads to a block's rows as keep them in registers, or find something to do when each has a team: with the
+    // rows, or with what the block holds already, should its scale grow.
+    const bool joins = __any_sync(~0u, (leaders >> lane & 1u) && !fresh);
+    const int work = max(most, joins ? 1 << bs : 0) * gr.chunks;
     Team team = {1, 0};
-    while (team.threads < BA_THREADS && (most * gr.chunks > HOLD * team.threads || (most * gr.chunks > team.threads && 2 * team.threads * total <= BA_THREADS)))
+    while (team.threads < BA_THREADS && (most * gr.chunks > HOLD * team.threads || (work > team.threads && 2 * team.threads * total <= BA_THREADS)))
         team.threads *= 2;
     team.index = tid / team.threads;
     const int teams = BA_THREADS / team.threads;

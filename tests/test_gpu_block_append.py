@@ -131,6 +131,30 @@ def test_one_token_and_many(T, hq, hk, kv):
     run([(i * 5 % 48, 1) for i in range(T)], hq, hk, 64, 16, 16, kv, seed=T)
 
 
+@pytest.mark.parametrize("neighbour", [False, True])
+def test_far_and_negative_positions(neighbour):
+    """Phases are exact at any position: every quarter of a turn, from both ends of 32 bits."""
+    g = torch.Generator().manual_seed(13)
+    pool = Pool(8, 16, 2, 64, "int8", 8, seed=13)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (2, 40), generator=g).to(torch.int32)
+    pos[0, :4] = torch.tensor([2 ** 31 - 1, -2 ** 31, 0, -1])
+    axis = torch.tensor([i % 2 for i in range(32)], dtype=torch.uint8)
+    append(pool, rows_of(40, 3, 2, 64, g), pos, torch.arange(16, 56, dtype=torch.int32), 3, 2, 64, paged_ref.turns_of(64), axis, neighbour)
+    # frequencies of a quarter, an eighth and three eighths of a turn, and just beside them: the borders between quarters
+    freqs = [x * 2 * 3.141592653589793 for x in (0.25, 0.125, 0.375, 0.5, 0.75, 0.125 + 2.0 ** -40, 0.125 - 2.0 ** -40, 0.9999999)] * 4
+    append(pool, rows_of(40, 3, 2, 64, g), torch.arange(40, dtype=torch.int32)[None], torch.arange(16, 56, dtype=torch.int32), 3, 2, 64, freqs,
+           torch.zeros(32, dtype=torch.uint8), neighbour)
+
+
+@pytest.mark.parametrize("kv", ["int8", "e4m3"])
+@pytest.mark.parametrize("block", [1, 4, 16, 64])
+def test_calls_of_many_sizes(block, kv):
+    """Every way in which rows are shared out: a row to a CTA and sixteen, blocks that begin anywhere in them, none at all."""
+    for T, spans in ((40, [(i, 1) for i in range(40)]), (330, [(7, 300), (0, 30)]), (1300, [(3, 1200), (60, 100)]),
+                     (5000, [(5, 4000), (1, 900), (2, 100)]), (4900, [(i % 64, 1 + i % 3) for i in range(2450)])):
+        run(spans, 1, 1, 32, 64, block, kv, seed=T)
+
+
 @pytest.mark.parametrize("kv", ["int8", "e4m3"])
 def test_a_block_filled_token_by_token(kv):
     """The scale follows the largest value so far; what is there already is rounded again where it grows."""

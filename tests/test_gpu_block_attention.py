@@ -177,6 +177,27 @@ def test_tables_with_room_for_much_more(hq, hk, tokens, dim, kv):
     check(long)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [1, 8, 32])
+def test_two_key_heads_to_a_cta_whose_scales_lie_anywhere(block, dim):
+    """The two heads' scales side by side on eight bytes or not, or apart: the same bits."""
+    s = scene([5003, 17, 900], 8, 4, dim, 32, "int8", block, seed=block)
+    wide = torch.full((3, 40000), -1, dtype=torch.int32)
+    wide[:, : s["table"].shape[1]] = s["table"]
+    s["table"] = wide
+    want, wl = check(s)
+    k, v, table, lens, q = s["k"].cuda(), s["v"].cuda(), wide.cuda(), s["lens"].cuda(), s["q"].cuda()
+    shape = s["ks"].shape
+    flat = [torch.zeros(shape.numel() + 3, device="cuda")[3:].view(shape) for _ in "kv"]       # four bytes off the boundary
+    odd = [torch.zeros(shape[0], shape[1], shape[2] + 1, device="cuda")[:, :, :-1] for _ in "kv"]  # an odd stride of blocks
+    apart = [torch.zeros(shape[2], shape[0], shape[1], device="cuda").permute(1, 2, 0) for _ in "kv"]
+    for ks, vs in (flat, odd, apart):
+        ks.copy_(s["ks"]), vs.copy_(s["vs"])
+        lse = torch.empty(q.shape[:3], device="cuda")
+        out = api.paged_attention(q, api.BlockCache(k, v, ks, vs), table, lens, lse=lse)
+        assert torch.equal(out.cpu(), want) and torch.equal(lse.cpu(), wl)
+
+
 def test_same_inputs_same_bits():
     s = scene([8000, 17, 3000, 1, 500], 8, 2, 128, 16, seed=4)
     first = attend(s)
