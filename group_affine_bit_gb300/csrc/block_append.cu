@@ -6,13 +6,32 @@
 //     scale = max(old, top / 127) or, e4m3, max(old, 2^ceil(log2(top / 448)))
 //     code = round(x / scale), and the block's other codes times old / scale
 //
-// Every value of a block waits for the largest of them, so a block's rows are
-// one warp's work, for one key head and k or v: it turns them, reduces the
-// maximum and writes the codes.  One launch has two kinds of CTAs: those of q
-// take a token each (the sines once for all heads), those of k and v a few
-// rows of the call and a share of the heads.  A row whose predecessor lies in
-// the same block belongs to that row's warp; the first one's warp finds how
-// many follow.
+// Every value of a block waits for the largest of them, so the rows that a call
+// brings for a block are one team's work, for one key head and k or v: it reads
+// them once, keeps them in registers as they are (32 of them, for 4 chunks of 16
+// values a thread), turns them for the maximum and once more for the codes.  A
+// team is 2 to 256 threads: as many as hold its rows, and more where a CTA's
+// teams would leave threads without work (one token of 128 values: 8 threads; a
+// block of 64 tokens: 128).  A row whose predecessor in the call lies in the same
+// block belongs to that row's team, so no two CTAs write one block; every CTA
+// finds from the slots which rows of its own begin one and how many follow.
+//
+// A block's scale only grows, and with it the codes that are there are rounded
+// again, so a scale is as tight as its block's largest value.  e4m3 scales are
+// powers of two: growth then only shifts exponents, and codes lose bits below the
+// normal ones alone.
+//
+// One launch has CTAs for k and v, which come first, and for q (up to four tokens,
+// a chunk of each to a thread).  Sines are made once a CTA, from the nearest
+// quarter of a turn.  Bound by memory and, nearly as much, by instructions
+// (issue slots 61 % taken for a chunk of prompts): measured (GB300, device time)
+// 25.7 us for 6.4 thousand tokens of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 72 %
+// of the copy rate (68 us with a warp to a block and the rows as fp32; 33 with
+// them as read; 30 with several tokens of q to a CTA); 29 us for 6210 tokens with a
+// scale for each (81 with a warp to each); 4.0 us for a decode step of 64 tokens,
+// 4.6 to 5.1 while its blocks grow.  More CTAs an SM (64 registers, two chunks a
+// thread) were no faster, two instead of three 15 % slower; loads and stores that
+// leave L2 first changed nothing.
 #include <type_traits>
 
 #include "affqmm_internal.h"

@@ -10,8 +10,8 @@
 // head: query heads of the group x tokens, 1 .. 64 to a tile).
 //
 // Roles.  A CTA has four consumer warps (or two groups of four, below), two
-// producer warps and one for q.  A tile is 64 or 128 keys.  The producers (one
-// for K, one for V) gather it through the block table with TMA, a box to a
+// producer warps, one for q and, where blocks have scales, one for those.  A
+// tile is 64 or 128 keys.  The producers (one for K, one for V) gather it through the block table with TMA, a box to a
 // page's rows of the tile, in 128-byte panels whose swizzle keeps the fragment
 // loads free of bank conflicts; K and V tiles take turns in one ring.  Rows of
 // pages that no query may see are not read, an entry that is no page reads as
@@ -26,7 +26,7 @@
 // keys x 16 dims: S^T = K Q^T, a warp to 16 (or 2 x 16) keys; then O^T = V^T
 // P^T, a warp to a quarter of the dims, P^T through shared memory.  The running
 // maximum is shared by the group and lazy: a tile is rescaled only if a score
-// exceeds it by more than 2^8 (e4m3: 2^2; an OR over the barrier that P^T needs
+// exceeds it by more than 2^8 (8-bit caches: 2^2; an OR over the barrier that P^T needs
 // anyway), so most tiles cost one barrier and no shuffles.  Scores, maxima, sums and
 // outputs are fp32.  P meets V in the matrix type.  Beside a bf16 cache it is
 // the sum of two bf16 numbers, what the first leaves being in the second, each
@@ -45,6 +45,22 @@
 // pipe is far from busy, and from 32 rows on it is what bounds the kernel (64
 // rows at dim 128: 192 instructions of 16 cycles a tile, 168 us of the measured
 // 170).
+//
+// Scales of blocks.  Beside codes with a scale for each block of tokens and head
+// (e4m3 or int8), K's scale multiplies a key's score, and V's enters the exponent:
+//     z = log2(e) s + log2 vs,   P = 2^(z - m + lift) in f16,   l = sum P / vs
+// with m the running maximum of z, so that what meets V's codes in f16 is again at
+// most 2^15 whatever the scales are.  A scale is between 2^-48 and 2^48, which
+// keeps P / vs within fp32.  A warp of its own brings the scales: it loads the
+// next tile's (8 bytes a block, gathered through the table) while this one's wait
+// for their place beside the ring, and leaves K's scale and log2 of V's, so that a
+// consumer spends two multiply-adds a score and a shared load and an exponential a
+// key.  (64 requests of up to 32768 keys, dim 128, int8: with the loads in K's
+// producer 378 us in blocks of 32 and 839 with a scale for every token; with a
+// warp of its own 310 and 367; e4m3 with a scale for each head 305.)  Four int8
+// codes become f16 by two byte permutations and two packed subtractions.
+// 16 rows of dim 256 fit two CTAs an SM in registers (12 requests x 5 tokens,
+// window 1024: 40 -> 33 us against two groups that convert the same keys).
 //
 // Groups.  Where one CTA fills an SM and the rows fill two row tiles or more,
 // they go to two groups of four consumer warps that share the ring and q: two

@@ -4,9 +4,13 @@
 //
 // Bound by memory: a value is read once (two bytes, or one) and written once
 // (two).  A CTA takes a few rows, whose requests, pages and places its first
-// threads find (the request by bisection of `starts`, which are brought to
-// shared memory first), and all heads of k and v; a thread takes eight
-// neighbouring values, 16 bytes to write.
+// threads find (the request by bisection of `starts`, which are brought to shared
+// memory first), and all heads of k and v; a thread has four pieces of k and of v
+// in flight, of eight neighbouring values each, 16 bytes to write.  Measured
+// (GB300, device time): 16 requests of up to 8192 tokens, int8, 372 MB, in 59.7
+// us, 93 % of the copy rate (72 with one piece after the other: the loads'
+// latency); 32,606 tokens of one head of 128 in 7.2 us (14.4 with 32 rows to every
+// CTA, whose threads then had little to do).
 #include <type_traits>
 
 #include "affqmm_internal.h"
