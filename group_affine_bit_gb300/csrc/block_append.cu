@@ -25,7 +25,7 @@
 // a chunk of each to a thread).  Sines are made once a CTA, from the nearest
 // quarter of a turn.  Bound by memory and, nearly as much, by instructions
 // (issue slots 61 % taken for a chunk of prompts): measured (GB300, device time)
-// 25.7 us for 6.4 thousand tokens of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 72 %
+// 25.7 us for 5456 tokens of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 72 %
 // of the copy rate (68 us with a warp to a block and the rows as fp32; 33 with
 // them as read; 30 with several tokens of q to a CTA); 29 us for 6210 tokens with a
 // scale for each (81 with a warp to each); 4.0 us for a decode step of 64 tokens,
