@@ -665,10 +665,10 @@ class Rope:
         """The address of the C view for positions of `axes` axes."""
         c = self._c.get(axes)
         if c is None:
-            c = self._c[axes] = CRope(self.turns.data_ptr() if self.rotary else None,
-                                      self.axis.data_ptr() if self.axis is not None else None, self.rotary,
-                                      int(self.neighbour), axes)
-        return ctypes.addressof(c)
+            view = CRope(self.turns.data_ptr() if self.rotary else None, self.axis.data_ptr() if self.axis is not None else None,
+                         self.rotary, int(self.neighbour), axes)
+            c = self._c[axes] = (ctypes.addressof(view), view)
+        return c[0]
 
 
 def rope_turns(frequencies, device="cuda") -> torch.Tensor:
@@ -766,11 +766,12 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     if T == 0:
         return out
     axes = pshape[0] if len(pshape) == 2 else 1
+    rope_view = rope._c.get(axes)
     rc = getattr(_lib or lib(), cache._append)(
-        cache._ref, rope.cstruct(axes), _ROWS(q.data_ptr(), sq[0], sq[1]), _ROWS(k.data_ptr(), sk[0], sk[1]),
+        cache._ref, rope_view[0] if rope_view is not None else rope.cstruct(axes), _ROWS(q.data_ptr(), sq[0], sq[1]), _ROWS(k.data_ptr(), sk[0], sk[1]),
         _ROWS(v.data_ptr(), sv[0], sv[1]), _ROWS(out.data_ptr(), so[0], so[1]), T, shape[1], positions.data_ptr(),
-        sp[0] if axes > 1 else 0, slots.data_ptr(), _status_ptr(status, dev),
-        _stream_ptr(stream, dev))
+        sp[0] if axes > 1 else 0, slots.data_ptr(), None if status is None else _status_ptr(status, dev),
+        _stream_ptr(stream, dev) if stream is not None or _raw_stream is None else _raw_stream(dev))
     if rc:
         rows = _unstepped(rc, q, k, v, out)
         if rows is None:
@@ -829,7 +830,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache | BlockCache, table: torch.T
         cache._ref, _LANES(q.data_ptr(), sq[0], sq[-3], sq[-2]), _LANES(out.data_ptr(), so[0], so[-3], so[-2]),
         lse.data_ptr() if lse is not None else None, batch, tokens, heads, table.data_ptr(), st[0], tshape[1],
         lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
-        _status_ptr(status, dev), buf.data_ptr(), buf.numel(), sp)
+        None if status is None else _status_ptr(status, dev), buf.data_ptr(), buf.numel(), sp)
     if rc:
         lanes = _unstepped(rc, q, out)
         if lanes is None:
@@ -865,8 +866,9 @@ def paged_read(cache: KVCache | BlockCache, table: torch.Tensor, starts: torch.T
                          f"{cache.device}")
     rc = getattr(_lib or lib(), cache._read)(
         cache._ref, _ROWS(k.data_ptr(), sk[0], sk[1]), _ROWS(v.data_ptr(), sv[0], sv[1]), shape[0], tshape[0], table.data_ptr(),
-        st[0], tshape[1], starts.data_ptr(), first.data_ptr() if first is not None else None, _status_ptr(status, dev),
-        _stream_ptr(stream, dev))
+        st[0], tshape[1], starts.data_ptr(), None if first is None else first.data_ptr(),
+        None if status is None else _status_ptr(status, dev),
+        _stream_ptr(stream, dev) if stream is not None or _raw_stream is None else _raw_stream(dev))
     if rc:
         plain = _unstepped(rc, k, v)
         if plain is None:

@@ -1056,7 +1056,7 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
                 wait(full(slot), phase);
                 {
                     const uint32_t kt = ring_u + (uint32_t)slot * C::TILE + own_head;
-#pragma unroll 2
+#pragma unroll (BLOCKS ? 4 : 2)
                     for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
                         uint32_t a0[KB][4], a1[KB][4];
 #pragma unroll
