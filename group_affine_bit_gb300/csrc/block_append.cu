@@ -412,7 +412,7 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
 
 // FAR: blocks whose tokens' sines do not all fit the table.
 template <int PAIRS, bool I8, bool FAR>
-__global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
+__global__ void __launch_bounds__(BA_THREADS, PAIRS != HALVES_1 && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
     extern __shared__ __align__(16) float table[];       // sines of a few tokens
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const RopeParams& r = p.rope;
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
         x.codes = (is_v ? r.vc : r.kc) + page * r.page_bytes + in_page * r.token_bytes + h * r.head_bytes;
         x.scale = (is_v ? p.v_scales : p.k_scales) + page * p.s_ps + (int64_t)(in_page >> bs) * p.s_bs + h * p.s_hs;
         held = *x.scale;
-        if (PAIRS == HALVES_8 || !is_v) load_rows<PAIRS>(gr, x, team.thread(), team.threads, turns, raw);
+        if (PAIRS != HALVES_1 || !is_v) load_rows<PAIRS>(gr, x, team.thread(), team.threads, turns, raw);
         else load_rows<HALVES_8>(gr, x, team.thread(), team.threads, 0, raw);
     };
     int i = team.index;
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS == HALVES_8 && !FAR ? 3 : 2)
     }
 #pragma unroll 1
     for (int round = 0; round < total; round += teams) {
-        if (PAIRS == HALVES_8 || !is_v) write_block<PAIRS, I8, FAR>(p, gr, x, turns, table, raw, held, team, tops);
+        if (PAIRS != HALVES_1 || !is_v) write_block<PAIRS, I8, FAR>(p, gr, x, turns, table, raw, held, team, tops);
         else write_block<HALVES_8, I8, false>(p, gr, x, 0, table, raw, held, team, tops);
         i += teams;
         if (round + teams < total) load(i);
