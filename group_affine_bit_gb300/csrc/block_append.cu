@@ -8,11 +8,11 @@
 //
 // Every value of a block waits for the largest of them, so the rows that a call
 // brings for a block are one team's work, for one key head and k or v: it reads
-// them once, keeps them in registers as they are (32 of them, for 4 chunks of 16
-// values a thread), turns them for the maximum and once more for the codes.  A
-// team is 2 to 256 threads: as many as hold its rows, and more where a CTA's
-// teams would leave threads without work (one token of 128 values: 8 threads; a
-// block of 64 tokens: 128).  A row whose predecessor in the call lies in the same
+// them once, keeps them in registers as they are (two or four chunks of 16 values
+// a thread), turns them for the maximum and once more for the codes.  A team is 1
+// to 256 threads: as many as hold its rows, and more where a CTA's teams would
+// leave threads without work (one token of 128 values: 8 threads or more; a block
+// of 64 tokens: 128 or 256).  A row whose predecessor in the call lies in the same
 // block belongs to that row's team, so no two CTAs write one block; every CTA
 // finds from the slots which rows of its own begin one and how many follow.
 //
@@ -23,15 +23,16 @@
 //
 // One launch has CTAs for k and v, which come first, and for q (up to four tokens,
 // a chunk of each to a thread).  Sines are made once a CTA, from the nearest
-// quarter of a turn.  Bound by memory and, nearly as much, by instructions
-// (issue slots 61 % taken for a chunk of prompts): measured (GB300, device time)
-// 25.7 us for 5456 tokens of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 72 %
-// of the copy rate (68 us with a warp to a block and the rows as fp32; 33 with
-// them as read; 30 with several tokens of q to a CTA); 29 us for 6210 tokens with a
-// scale for each (81 with a warp to each); 4.0 us for a decode step of 64 tokens,
-// 4.6 to 5.1 while its blocks grow.  More CTAs an SM (64 registers, two chunks a
-// thread) were no faster, two instead of three 15 % slower; loads and stores that
-// leave L2 first changed nothing.
+// quarter of a turn.  Bound by memory and, nearly as much, by the way of a CTA
+// from its slots to its codes (24 warps an SM; issue slots 61 % taken for a chunk
+// of prompts): measured (GB300, device time) 25.6 us for 5456 tokens of 32 + 2 x 8
+// heads of 128, e4m3, 123 MB, 72 % of the copy rate (68 us with a warp to a block
+// and the rows as fp32; 33 with them as read; 30 with several tokens of q to a
+// CTA); 29 us for 6210 tokens with a scale for each (81 with a warp to each); 3.3
+// us for a decode step of 64 tokens, 4.2 to 4.8 while its blocks grow.  Two CTAs an
+// SM instead of three are 15 to 20 % slower, four (64 registers) no faster; loads
+// and stores that leave L2 first, packed fp32 arithmetic, and CTAs of k and v
+// spread among those of q changed nothing.
 #include <type_traits>
 
 #include "affqmm_internal.h"
@@ -42,7 +43,6 @@ namespace affqmm {
 namespace {
 
 constexpr int BA_THREADS = 256, BA_WARPS = BA_THREADS / 32;
-constexpr int HOLD = 4;                  // chunks of 16 values that a lane keeps between a block's maximum and its codes
 constexpr int Q_TOKENS = 4;              // tokens of q to a CTA, at most
 constexpr size_t BA_TABLE = 136 << 10;   // most shared memory for sines: all but those of 128 tokens at rotary 512
 
@@ -276,7 +276,8 @@ __device__ __forceinline__ float scale_for(float top) {
 }
 
 struct Grid {
-    int kv_ctas, rows, parts;            // of k and v: CTAs, rows of the call to a CTA, CTAs that share k's (v's) heads
+    int kv_ctas, rows;                   // of k and v: CTAs, rows of the call to a CTA
+    int parts, least_parts;              // CTAs that may share k's (v's) heads, and that do so in any case
     int q_tokens, q_parts;               // of q: tokens to a CTA, or (one token) CTAs that share its heads
     int table_rows;                      // rows whose sines shared memory holds
     int chunks;                          // of a head
@@ -323,7 +324,8 @@ struct Rows {
     int table;                           // the first one's row in the table of sines
 };
 
-template <int PAIRS>
+// HOLD: chunks of 16 values that a thread keeps between a block's maximum and its codes.
+template <int PAIRS, int HOLD>
 __device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int first, int step, int half, Raw (&raw)[HOLD]) {
     const int all = u.n * gr.chunks;
 #pragma unroll
@@ -338,7 +340,7 @@ __device__ __forceinline__ void load_rows(const Grid& gr, const Rows& u, int fir
 
 // The codes and the scale of a block's rows; `raw`: their first chunks, loaded already, `held`: its scale.  Every thread of
 // a warp calls it, whatever its team has to do.
-template <int PAIRS, bool I8, bool FAR>
+template <int PAIRS, bool I8, bool FAR, int HOLD>
 __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr, const Rows& u, int half, const float* table,
                                             Raw (&raw)[HOLD], float held, const Team& team, float* tops) {
     const int own = team.thread(), step = team.threads, all = u.n * gr.chunks, bs = p.block_shift;
@@ -353,7 +355,7 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
     float top = 0.f;
 #pragma unroll 1
     for (int first = own; first < all; first += step * HOLD) {
-        if (first != own) load_rows<PAIRS>(gr, u, first, step, half, raw);
+        if (first != own) load_rows<PAIRS, HOLD>(gr, u, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (first + step * j < all) {
@@ -396,7 +398,7 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
     const float by = __frcp_rn(scale);
 #pragma unroll 1
     for (int first = own; first < all; first += step * HOLD) {
-        if (grows || all > step * HOLD) load_rows<PAIRS>(gr, u, first, step, half, raw);
+        if (grows || all > step * HOLD) load_rows<PAIRS, HOLD>(gr, u, first, step, half, raw);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (first + step * j < all) {
@@ -411,7 +413,7 @@ __device__ __forceinline__ void write_block(const BlockParams& p, const Grid& gr
 }
 
 // FAR: blocks whose tokens' sines do not all fit the table.
-template <int PAIRS, bool I8, bool FAR>
+template <int PAIRS, bool I8, bool FAR, int HOLD>
 __global__ void __launch_bounds__(BA_THREADS, PAIRS != HALVES_1 && !FAR ? 3 : 2) block_append_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ Grid gr) {
     extern __shared__ __align__(16) float table[];       // sines of a few tokens
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -458,7 +460,6 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS != HALVES_1 && !FAR ? 3 : 2)
     // ================= k, or v, of the blocks that begin, for this call, in these rows
     const int window = over((int)blockIdx.x, gr.m_parts, 2 * gr.parts), part = (int)blockIdx.x - window * 2 * gr.parts;
     const bool is_v = part >= gr.parts;
-    const int h0 = (is_v ? part - gr.parts : part) * r.heads_kv / gr.parts, heads = ((is_v ? part - gr.parts : part) + 1) * r.heads_kv / gr.parts - h0;
     const int64_t t0 = (int64_t)window * gr.rows;
     const int bs = p.block_shift;
     __shared__ float tops[BA_WARPS];
@@ -495,7 +496,13 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS != HALVES_1 && !FAR ? 3 : 2)
     n = min(n, 1 << bs);                     // more would name a slot twice
     if (leaders >> lane & 1u) leader[warp][__popc(leaders & ((1u << lane) - 1u))] = (int8_t)lane;
     __syncwarp();
-    const int most = __reduce_max_sync(~0u, leaders >> lane & 1u ? n : 0), total = __popc(leaders) * heads, first_lane = __ffs(leaders) - 1;
+    const int most = __reduce_max_sync(~0u, leaders >> lane & 1u ? n : 0), first_lane = __ffs(leaders) - 1;
+    // As many CTAs share the heads as make two rounds of them, or what there are; the others have nothing to do.
+    int parts = gr.least_parts;
+    while (parts < gr.parts && most * gr.chunks * r.heads_kv > 2 * HOLD * BA_THREADS * parts) parts = min(2 * parts, gr.parts);
+    const int mine_of = is_v ? part - gr.parts : part;
+    if (mine_of >= parts) return;
+    const int h0 = mine_of * r.heads_kv / parts, heads = (mine_of + 1) * r.heads_kv / parts - h0, total = __popc(leaders) * heads;
     // As many threads to a block's rows as keep them in registers, or find something to do when each has a team: with the
     // rows, or with what the block holds already, should its scale grow.
     const bool joins = __any_sync(~0u, (leaders >> lane & 1u) && !fresh);
@@ -527,8 +534,8 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS != HALVES_1 && !FAR ? 3 : 2)
         x.codes = (is_v ? r.vc : r.kc) + page * r.page_bytes + in_page * r.token_bytes + h * r.head_bytes;
         x.scale = (is_v ? p.v_scales : p.k_scales) + page * p.s_ps + (int64_t)(in_page >> bs) * p.s_bs + h * p.s_hs;
         held = *x.scale;
-        if (PAIRS != HALVES_1 || !is_v) load_rows<PAIRS>(gr, x, team.thread(), team.threads, turns, raw);
-        else load_rows<HALVES_8>(gr, x, team.thread(), team.threads, 0, raw);
+        if (PAIRS != HALVES_1 || !is_v) load_rows<PAIRS, HOLD>(gr, x, team.thread(), team.threads, turns, raw);
+        else load_rows<HALVES_8, HOLD>(gr, x, team.thread(), team.threads, 0, raw);
     };
     int i = team.index;
     load(i);
@@ -543,8 +550,8 @@ __global__ void __launch_bounds__(BA_THREADS, PAIRS != HALVES_1 && !FAR ? 3 : 2)
     }
 #pragma unroll 1
     for (int round = 0; round < total; round += teams) {
-        if (PAIRS != HALVES_1 || !is_v) write_block<PAIRS, I8, FAR>(p, gr, x, turns, table, raw, held, team, tops);
-        else write_block<HALVES_8, I8, false>(p, gr, x, 0, table, raw, held, team, tops);
+        if (PAIRS != HALVES_1 || !is_v) write_block<PAIRS, I8, FAR, HOLD>(p, gr, x, turns, table, raw, held, team, tops);
+        else write_block<HALVES_8, I8, false, HOLD>(p, gr, x, 0, table, raw, held, team, tops);
         i += teams;
         if (round + teams < total) load(i);
         if (team.threads > 32) team.sync();  // `tops` serves the next
@@ -562,11 +569,15 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
     g.chunks = r.dim / 16;
     // k and v: some rows to a CTA, so that a CTA of short blocks has several and one in which none begins is soon done; and
     // parts that share the heads, where there are few CTAs even if a block begins in each row (a decode step of 64 tokens:
-    // 3.3 us; with a part for each of 8 heads 8.4), or so many rows that they are prompts' and most blocks are whole
+    // 3.3 us; with a part for each of 8 heads 8.4), or so many rows that they are prompts' and most blocks are whole.  Of a few
+    // tokens nobody knows here how many come to a block: parts for whole ones are there, and those that have nothing to do
+    // end (237 tokens in blocks of 64: 19.4 -> 9.7 us; 256 single tokens of such blocks 15.2 -> 18.6)
     g.rows = r.tokens >= 32 * sms ? 16 : r.tokens >= 8 * sms ? 8 : r.tokens >= 2 * sms ? 2 : 1;
     const int64_t whole = (r.tokens + block - 1) / block;
     const int64_t want = r.tokens >= 8 * sms ? (sms + whole - 1) / whole : 3 * sms * g.rows / (4 * r.tokens);
-    g.parts = (int)(want < 1 ? 1 : want < r.heads_kv ? want : r.heads_kv);
+    g.least_parts = (int)(want < 1 ? 1 : want < r.heads_kv ? want : r.heads_kv);
+    const int large = (block * g.chunks + 127) / 128;    // parts for a block that is brought whole, should one be
+    g.parts = r.tokens >= 8 * sms || large <= g.least_parts ? g.least_parts : large < r.heads_kv ? large : r.heads_kv;
     g.kv_ctas = (int)((r.tokens + g.rows - 1) / g.rows) * 2 * g.parts;
     g.groups = (half + 7) / 8;
     g.table_rows = half ? (int)(BA_TABLE / (64 * g.groups)) : block;
@@ -579,16 +590,24 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
     g.m_chunks = reciprocal(g.chunks), g.m_half = reciprocal(half), g.m_parts = reciprocal(2 * g.parts), g.m_q_parts = reciprocal(g.q_parts);
     const int64_t q_ctas = (r.tokens + g.q_tokens - 1) / g.q_tokens * g.q_parts;
     const size_t smem = (size_t)(g.table_rows > g.q_tokens ? g.table_rows : g.q_tokens) * 64 * g.groups;
-    auto pick = [&](auto i8, auto far) {
+    // Two chunks to a thread where there are few tokens: a call's time is then the kernel's way through its code, cold (64
+    // tokens of a decode step: 3.8 us with four, 3.2 with two; 7646 rows of prompts: 34.5 with four, 36.0 with two).
+    auto pick = [&](auto i8, auto far, auto hold) {
         constexpr bool I8 = decltype(i8)::value, FAR = decltype(far)::value;
-        return pairs == HALVES_8   ? block_append_kernel<HALVES_8, I8, FAR>
-               : pairs == HALVES_4 ? block_append_kernel<HALVES_4, I8, FAR>
-               : pairs == HALVES_1 ? block_append_kernel<HALVES_1, I8, FAR>
-                                   : block_append_kernel<NEIGHBOURS, I8, FAR>;
+        constexpr int HOLD = decltype(hold)::value;
+        return pairs == HALVES_8   ? block_append_kernel<HALVES_8, I8, FAR, HOLD>
+               : pairs == HALVES_4 ? block_append_kernel<HALVES_4, I8, FAR, HOLD>
+               : pairs == HALVES_1 ? block_append_kernel<HALVES_1, I8, FAR, HOLD>
+                                   : block_append_kernel<NEIGHBOURS, I8, FAR, HOLD>;
     };
-    const bool far = half && g.table_rows < block + g.rows - 1;
-    auto* kernel = r.e4m3 ? (far ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{}))
-                          : (far ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{}));
+    using Four = std::integral_constant<int, 4>;
+    const bool far = half && g.table_rows < block + g.rows - 1, few = r.tokens < 16 * sms;
+    auto typed = [&](auto i8) {
+        return far   ? pick(i8, std::true_type{}, Four{})
+               : few ? pick(i8, std::false_type{}, std::integral_constant<int, 2>{})
+                     : pick(i8, std::false_type{}, Four{});
+    };
+    auto* kernel = r.e4m3 ? typed(std::false_type{}) : typed(std::true_type{});
     if (smem > 40 << 10) {                   // the kernel has some of its own beside it
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BA_TABLE);
         if (e != cudaSuccess) return e;

@@ -587,7 +587,7 @@ typedef struct {
  *     scale = top / 127 (AFFQMM_KV_I8), or the least power of two from top / 448
  *             on (AFFQMM_KV_E4M3), within 2^-48 and 2^48
  *     code = value / scale, rounded to nearest (ties to even) and saturating
- * in fp32.  A call that brings a block's first token begins the block anew: what
+ * in fp32 (the quotient as a product with the scale's inverse).  A call that brings a block's first token begins the block anew: what
  * it held counts as gone.  Else the block's scale is kept where it is large
  * enough already; where it is not, the block's other codes are brought to the
  * new scale, and rounded once more (an e4m3 code loses bits only if it falls below
