@@ -131,6 +131,15 @@ def test_one_token_and_many(T, hq, hk, kv):
     run([(i * 5 % 48, 1) for i in range(T)], hq, hk, 64, 16, 16, kv, seed=T)
 
 
+@pytest.mark.parametrize("kv", ["int8", "e4m3"])
+@pytest.mark.parametrize("spans", [[(0, 200), (70, 60)], [(5, 1), (64, 1), (0, 30)], [(i * 9, 1 + i % 2) for i in range(40)]])
+@pytest.mark.parametrize("dim,block", [(128, 64), (256, 128), (64, 128)])
+def test_heads_shared_out_by_what_a_block_is_brought(dim, block, spans, kv):
+    """Few tokens and large blocks: one CTA for all heads, or several, as whole blocks or single tokens come."""
+    run(spans, 3, 8, dim, 128, block, kv, seed=dim + block)
+    run(spans, 1, 5, dim, 128, block, kv, neighbour=True, seed=block)
+
+
 @pytest.mark.parametrize("neighbour", [False, True])
 def test_far_and_negative_positions(neighbour):
     """Phases are exact at any position: every quarter of a turn, from both ends of 32 bits."""

@@ -95,6 +95,7 @@ def test_entries_that_are_no_page_read_as_zeros(kv):
 
 def test_many_requests_and_many_heads():
     check(*pool(40, 8, 1, 16, "int8", 8, 3), [(i % 5, i * 7 % 4) for i in range(1500)], seed=3)
+    check(*pool(40, 8, 1, 16, "e4m3", 8, 3), [(i % 5, i * 5 % 3) for i in range(3000)], seed=5)   # more than shared memory keeps
     check(*pool(3, 2, 300, 512, "int8", 2, 4), [(0, 5), (1, 2)], seed=4)
 
 
