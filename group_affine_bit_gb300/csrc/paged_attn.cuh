@@ -143,7 +143,9 @@ struct Cfg {
     static constexpr int JOIN = 32;                    // most parts that a join takes at once
     static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PN * NA * KEYS * 16 + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
                                     JOIN * ROWS * 4 + (BLOCKS ? 448 : 512);   // and the barriers
-    static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= (BLOCKS ? 48 : 32);   // registers allow two CTAs an SM
+    // Registers allow two CTAs an SM.  Two row tiles of dim 256 beside scales of blocks just fit (12 x 5 tokens, window 1024:
+    // 40 -> 33 us); four of dim 64, as many accumulators but more scores, spill (12 requests of 1000 keys 12.7 -> 15.6).
+    static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= (BLOCKS && DP == 256 ? 48 : 32);
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
     static constexpr int CPS = (!PAIR && LIGHT && FIXED + 3 * TILE + 2 * SCALES * 4 <= HALF) ? 2 : 1;
     // With one CTA an SM, the rows go to two groups of consumer warps (where there are two row tiles), which share
