@@ -744,8 +744,9 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: to
     positions on q and k, and k and v written to their slots of the cache.  q [tokens, query heads, dim], k and v [tokens,
     cache heads, dim], bf16, token and head strides multiples of 8 (views of the
     stacked projection's output serve); positions int32 [tokens] or [axes,
-    tokens]; slots int32 [tokens], -1 for a token that is not kept.  Returns q turned,
-    in `out` (which may be q)."""
+    tokens]; slots int32 [tokens], -1 for a token that is not kept (for a
+    BlockCache, a block's tokens one after another; bit 2 of `status` says where
+    they are not).  Returns q turned, in `out` (which may be q)."""
     dev, dim = cache._dev, cache.dim
     shape, kshape, pshape = q.shape, k.shape, positions.shape
     if len(shape) != 3:

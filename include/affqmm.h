@@ -561,6 +561,8 @@ AFFQMM_API int affqmm_paged_attention(const affqmm_kv_cache* cache, const affqmm
 
 /* Most tokens of a block, and the bounds of a scale: 2^-48 and 2^48. */
 #define AFFQMM_BLOCK_MAX 128
+/* Most tokens of an append whose order is looked at. */
+#define AFFQMM_BLOCK_ORDER 262144
 
 /* Such a cache: a non-owning view.
  *   kv            as for the other calls, with type AFFQMM_KV_E4M3 or
@@ -598,6 +600,10 @@ typedef struct {
  *   slots     as for affqmm_rope_append; and the tokens of one block come one
  *             after another in the call (as affqmm_paged_plan orders them), with
  *             no token of another block and no -1 between them
+ *   status    as for affqmm_rope_append; and in calls of up to
+ *             AFFQMM_BLOCK_ORDER tokens bit 2 is set where a block's tokens do not
+ *             come one after another, or are more than it has: what that block
+ *             holds is then undefined, out and all other blocks are as they should be
  * The other arguments and the errors are those of affqmm_rope_append. */
 AFFQMM_API int affqmm_block_append(const affqmm_block_cache* cache, const affqmm_rope* rope, const affqmm_rows* q,
                                    const affqmm_rows* k, const affqmm_rows* v, const affqmm_rows* out, int64_t tokens,
