@@ -403,12 +403,12 @@ int read_rows(const affqmm_kv_cache* cache, const Scales* scales, const affqmm_r
     if (!k || !v) return AFFQMM_E_NULL;
     if (batch < 0 || batch > AFFQMM_PAGED_MAX_BATCH || rows < 0 || rows >= kMost || wide < 0 || table_stride < 0) return AFFQMM_E_SHAPE;
     if (wide >= kMost || wide * cache->page >= (int64_t)1 << 31) return AFFQMM_E_SHAPE;
-    if (batch == 0 || rows == 0) return AFFQMM_OK;
+    if (batch == 0 || (rows == 0 && !status)) return AFFQMM_OK;   // no rows: whether any were wanted
     if (!starts || (wide > 0 && !table)) return AFFQMM_E_NULL;
     if (!aligned(starts, 4) || !aligned(first, 4) || !aligned(table, 4) || !aligned(status, 4)) return AFFQMM_E_ALIGN;
     int rc;
     for (const affqmm_rows* r : {k, v})
-        if ((rc = check_rows(r->p, r->token_stride, r->head_stride, 0))) return rc;
+        if (rows > 0 && (rc = check_rows(r->p, r->token_stride, r->head_stride, 0))) return rc;
     int sms = 0;
     if ((rc = device_sms(&sms))) return rc;
     const int es = value_bytes(cache);

@@ -140,7 +140,8 @@ cudaError_t launch_paged_read(const ReadParams& p, int kind, int sms, cudaStream
     };
     auto* kernel = kind == READ_BF16 ? paged_read_kernel<READ_BF16> : kind == READ_E4M3 ? paged_read_kernel<READ_E4M3>
                    : kind == READ_E4M3_BLOCKS ? paged_read_kernel<READ_E4M3_BLOCKS> : paged_read_kernel<READ_I8_BLOCKS>;
-    return launch_pdl(kernel, dim3((unsigned)((p.rows + rows - 1) / rows)), PR_THREADS, 0, st, p, rows, pieces, reciprocal(per_row, pieces), per_row,
+    const int64_t ctas = p.rows > 0 ? (p.rows + rows - 1) / rows : 1;
+    return launch_pdl(kernel, dim3((unsigned)ctas), PR_THREADS, 0, st, p, rows, pieces, reciprocal(per_row, pieces), per_row,
                       reciprocal((int64_t)PR_ROWS * per_row, per_row));
 }
 
