@@ -599,6 +599,12 @@ class KVCache:
         return cls(k, v, k_scale, v_scale)
 
 
+def _block_tokens(block: int) -> int:
+    if block < 1 or block > BLOCK_MAX or block & (block - 1):
+        raise ValueError(f"a block must have a power of two of tokens, {BLOCK_MAX} at most, not {block}")
+    return block
+
+
 class BlockCache:
     """A pool of pages whose 8-bit values have a scale for each block of tokens
     and key head, made as the cache is written: k and v [pages, page, heads,
@@ -614,17 +620,21 @@ class BlockCache:
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.device != v.device:
             raise ValueError("k and v must be [pages, page, heads, dim] tensors of one type, shape, stride and device")
-        if k.dtype not in _BLOCK_TYPES or not k.is_cuda:
-            raise ValueError("k and v must be CUDA int8 or float8_e4m3fn tensors")
-        if k.stride(3) != 1 and k.shape[3] > 1:
-            raise ValueError("the values of a head must be contiguous")
         self.pages, self.page, self.heads, self.dim = k.shape
         blocks = k_scale.shape[1] if k_scale.dim() == 3 else 0
         if blocks < 1 or self.page % blocks or k_scale.stride() != v_scale.stride():
             raise ValueError("k_scale and v_scale must be [pages, blocks of a page, heads] tensors of one stride")
+        self.block = _block_tokens(self.page // blocks)
+        steps = sorted((s, n) for s, n in zip(k_scale.stride(), k_scale.shape) if n > 1)
+        if any(s < before * n for (before, n), (s, _) in zip([(1, 1)] + steps, steps)):
+            raise ValueError("the scales of two blocks or heads must not share a place")
+        if k.dtype not in _BLOCK_TYPES or not k.is_cuda:
+            raise ValueError("k and v must be CUDA int8 or float8_e4m3fn tensors")
+        if k.stride(3) != 1 and k.shape[3] > 1:
+            raise ValueError("the values of a head must be contiguous")
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _check_ints(t, name, (self.pages, blocks, self.heads), k.device, torch.float32, contiguous=False)
-        self.k, self.v, self.k_scale, self.v_scale, self.block = k, v, k_scale, v_scale, self.page // blocks
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device, self._dev = k.device, k.get_device()
         ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
         self._c = CBlockCache(CCache(_BLOCK_TYPES[k.dtype], self.page, self.heads, self.dim, self.pages, *k.stride()[:3],
@@ -636,8 +646,8 @@ class BlockCache:
     def empty(cls, pages: int, page: int, heads: int, dim: int, dtype=torch.int8, block: int | None = None,
               device="cuda") -> "BlockCache":
         """A pool of pages in blocks of `block` tokens (None: 16, or a page's fewer)."""
-        block = min(page, 16) if block is None else block
-        if block < 1 or page % block:
+        block = _block_tokens(min(page, 16) if block is None else block)
+        if page % block:
             raise ValueError("a block must divide a page")
         k, v = (torch.empty(pages, page, heads, dim, dtype=dtype, device=device) for _ in "kv")
         return cls(k, v, *(torch.zeros(pages, page // block, heads, device=device) for _ in "kv"))
