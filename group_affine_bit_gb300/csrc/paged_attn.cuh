@@ -141,8 +141,9 @@ struct Cfg {
     static constexpr int PN = BYTES ? 1 : 2;           // numbers that make one P
     static constexpr int MT = DP / (16 * W);           // 16-dim tiles of a consumer warp
     static constexpr int JOIN = 32;                    // most parts that a join takes at once
+    static constexpr int BARRIER_BYTES = BLOCKS ? 448 : 512;      // more than the barriers (below) take
     static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PN * NA * KEYS * 16 + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
-                                    JOIN * ROWS * 4 + (BLOCKS ? 448 : 512);   // and the barriers
+                                    JOIN * ROWS * 4 + BARRIER_BYTES;
     // Registers allow two CTAs an SM.  Two row tiles of dim 256 beside scales of blocks just fit (12 x 5 tokens, window 1024:
     // 40 -> 33 us); four of dim 64, as many accumulators but more scores, spill (12 requests of 1000 keys 12.7 -> 15.6).
     static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= (BLOCKS && DP == 256 ? 48 : 32);
@@ -168,6 +169,12 @@ struct Cfg {
     static constexpr size_t PART_FLOATS = STATS + 2 * GROWS;
     static constexpr size_t SLOT_FLOATS = NG * PART_FLOATS;
     static_assert(NS >= 3, "ring too short");
+    // The barriers, in units of one: full[], empty[], qfull[2], stored[2], counted, finished, decided, joined[2], drained, never,
+    // scaled[].
+    static constexpr int B_EMPTY = MAX_SLOTS, B_QFULL = B_EMPTY + MAX_SLOTS, B_STORED = B_QFULL + 2, B_COUNTED = B_STORED + 2,
+                         B_FINISHED = B_COUNTED + 1, B_DECIDED = B_FINISHED + 1, B_JOINED = B_DECIDED + 1, B_DRAINED = B_JOINED + 2,
+                         B_NEVER = B_DRAINED + 1, B_SCALED = B_NEVER + 1, BARRIERS = B_SCALED + (BLOCKS ? NSC : 0);
+    static_assert(QBUF <= 2 && NG <= 2 && 8 * BARRIERS <= BARRIER_BYTES, "more barriers than there is room for");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -381,16 +388,16 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
     uint64_t* bars = reinterpret_cast<uint64_t*>(weight + C::JOIN * C::ROWS);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (MAX_SLOTS + s); };
-    auto qfull = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + s); };
-    auto stored = [&](int s) { return bar0 + 8u * (2 * MAX_SLOTS + 2 + s); };   // a segment's rows, or the run's first part, are there
-    const uint32_t counted = bar0 + 8u * (2 * MAX_SLOTS + 4);    // the run's first part has been counted in
-    const uint32_t finished = counted + 8u;                      // the run's last tile has been added
-    const uint32_t decided = counted + 16u;                      // whether the other parts of its unit are there
-    auto joined = [&](int s) { return counted + 24u + 8u * s; };  // parts of other runs are in the group's share of the ring
-    const uint32_t drained = counted + 40u;                      // the q warp has written every row
-    const uint32_t never = counted + 48u;                        // completed by nothing: the fault_wait test hook waits on it
-    auto scaled = [&](int s) { return counted + 56u + 8u * s; };  // a K tile's scales are there (and its V tile's), of each set
+    auto empty = [&](int s) { return bar0 + 8u * (C::B_EMPTY + s); };
+    auto qfull = [&](int s) { return bar0 + 8u * (C::B_QFULL + s); };
+    auto stored = [&](int s) { return bar0 + 8u * (C::B_STORED + s); };   // a segment's rows, or the run's first part, are there
+    const uint32_t counted = bar0 + 8u * C::B_COUNTED;           // the run's first part has been counted in
+    const uint32_t finished = bar0 + 8u * C::B_FINISHED;         // the run's last tile has been added
+    const uint32_t decided = bar0 + 8u * C::B_DECIDED;           // whether the other parts of its unit are there
+    auto joined = [&](int s) { return bar0 + 8u * (C::B_JOINED + s); };  // parts of other runs are in the group's share of the ring
+    const uint32_t drained = bar0 + 8u * C::B_DRAINED;           // the q warp has written every row
+    const uint32_t never = bar0 + 8u * C::B_NEVER;               // completed by nothing: the fault_wait test hook waits on it
+    auto scaled = [&](int s) { return bar0 + 8u * (C::B_SCALED + s); };  // a K tile's scales are there (and its V tile's), of each set
     __shared__ uint32_t sums[THREADS / 32], found_unit0;
     __shared__ float kscale[4], vscale[4];   // of each q buffer, of each key head of the unit
     __shared__ int found_b;
