@@ -25,7 +25,7 @@
 // a chunk of each to a thread).  Sines are made once a CTA, from the nearest
 // quarter of a turn.  Bound by memory and, nearly as much, by the way of a CTA
 // from its slots to its codes (24 warps an SM; issue slots 61 % taken for a chunk
-// of prompts): measured (GB300, device time) 25.6 us for 5456 tokens of 32 + 2 x 8
+// of prompts; 44 to 56 bytes of spill beside 80 registers where pairs lie in runs): measured (GB300, device time) 25.6 us for 5456 tokens of 32 + 2 x 8
 // heads of 128, e4m3, 123 MB, 72 % of the copy rate (68 us with a warp to a block
 // and the rows as fp32; 33 with them as read; 30 with several tokens of q to a
 // CTA); 29 us for 6210 tokens with a scale for each (81 with a warp to each); 3.3
@@ -44,7 +44,9 @@ namespace {
 
 constexpr int BA_THREADS = 256, BA_WARPS = BA_THREADS / 32;
 constexpr int Q_TOKENS = 4;              // tokens of q to a CTA, at most
-constexpr size_t BA_TABLE = 136 << 10;   // most shared memory for sines: all but those of 128 tokens at rotary 512
+// Most shared memory for sines: 2176 / ceil(rotary / 16) tokens', where a block's and the CTA's rows before it are up to 128 + 15.
+// Too few in long calls from rotary 242 on for blocks of 128 (136 of 143) and 434 on for blocks of 64 (68 of 79 at 512).
+constexpr size_t BA_TABLE = 136 << 10;
 
 // How a head's values pair: HALVES i with i + rotary / 2, where values lie in
 // aligned runs of 8 (rotary a multiple of 16), 4 (of 8) or 1; NEIGHBOURS 2i
@@ -650,7 +652,7 @@ cudaError_t launch_block_append(const BlockParams& p, int sms, cudaStream_t st) 
         if (smem < (size_t)g.order_words * 4) smem = (size_t)g.order_words * 4;
     }
     // Two chunks to a thread where there are few tokens: a call's time is then the kernel's way through its code, cold (64
-    // tokens of a decode step: 3.8 us with four, 3.2 with two; 7646 rows of prompts: 34.5 with four, 36.0 with two).
+    // tokens of a decode step: 3.8 us with four, 3.3 with two; 7646 rows of prompts: 34.5 with four, 36.0 with two).
     auto pick = [&](auto i8, auto far, auto hold) {
         constexpr bool I8 = decltype(i8)::value, FAR = decltype(far)::value;
         constexpr int HOLD = decltype(hold)::value;

@@ -144,8 +144,8 @@ struct Cfg {
     static constexpr int BARRIER_BYTES = BLOCKS ? 448 : 512;      // more than the barriers (below) take
     static constexpr size_t FIXED = (size_t)QBUF * QBYTES + 2 * PN * NA * KEYS * 16 + 2 * W * ROWS * 4 + 5 * QBUF * ROWS * 4 +
                                     JOIN * ROWS * 4 + BARRIER_BYTES;
-    // Registers allow two CTAs an SM.  Two row tiles of dim 256 beside scales of blocks just fit (12 x 5 tokens, window 1024:
-    // 40 -> 33 us); four of dim 64, as many accumulators but more scores, spill (12 requests of 1000 keys 12.7 -> 15.6).
+    // Registers allow two CTAs an SM.  Two row tiles of dim 256 beside scales of blocks fit but for 4 to 8 bytes (12 x 5 tokens,
+    // window 1024: 40 -> 33 us); four of dim 64, as many accumulators but more scores, spill (12 requests of 1000 keys 12.7 -> 15.6).
     static constexpr bool LIGHT = MT * NA * 4 + NA * 8 <= (BLOCKS && DP == 256 ? 48 : 32);
     static constexpr size_t HALF = SM_SMEM / 2 - 1024 - STATIC_SMEM;
     static constexpr int CPS = (!PAIR && LIGHT && FIXED + 3 * TILE + 2 * SCALES * 4 <= HALF) ? 2 : 1;
@@ -1065,6 +1065,9 @@ __global__ void __launch_bounds__(Cfg<DP, NA, KIND, KBLOCKS, PAIRED>::THREADS, C
                 wait(full(slot), phase);
                 {
                     const uint32_t kt = ring_u + (uint32_t)slot * C::TILE + own_head;
+                    // Four steps under way beside scales of blocks, whatever the rows: 16 of dim 128 take 54 us instead of 56 (e4m3 57
+                    // instead of 60), 32 take 108 instead of 113, 64 take 167 instead of 170 (e4m3: 151 either way, with four 146
+                    // bytes of spill), 32 of dim 256 take 186 instead of 188; 64 requests of up to 8192 keys, 4 key heads.
 #pragma unroll (BLOCKS ? 4 : 2)
                     for (int s2 = 0; s2 < DP / 32; ++s2) {               // 32 dims
                         uint32_t a0[KB][4], a1[KB][4];

@@ -589,12 +589,17 @@ typedef struct {
  *     scale = top / 127 (AFFQMM_KV_I8), or the least power of two from top / 448
  *             on (AFFQMM_KV_E4M3), within 2^-48 and 2^48
  *     code = value / scale, rounded to nearest (ties to even) and saturating
- * in fp32 (the quotient as a product with the scale's inverse).  A call that brings a block's first token begins the block anew: what
- * it held counts as gone.  Else the block's scale is kept where it is large
- * enough already; where it is not, the block's other codes are brought to the
- * new scale, and rounded once more (an e4m3 code loses bits only if it falls below
- * the normal ones).  So a pool's pages can be used again as they are, the scales
- * need no first value, and the same calls give the same codes.
+ * in fp32 (the quotient as a product with the scale's inverse).  A call that
+ * brings a block's first token begins the block anew: what it held counts as
+ * gone.  Else the block's scale is kept where it is large enough already; where
+ * it is not, the block's other codes are brought to the new scale, and rounded
+ * once more (an e4m3 code loses bits only if it falls below the normal ones).  So
+ * a pool's pages can be used again as they are, the scales need no first value,
+ * and the same calls give the same codes.
+ * An int8 value is off by half a step of each scale that its block has had since
+ * it was written: half of the last one's where that did not grow, and more with
+ * every growth, however small.  An e4m3 value is off by 2^-4 of itself, or 2^-10
+ * of the scale below its normal codes, and there by 2^-10 of each later scale.
  * Infinities do not count for `top` and get the largest code; NaN stays NaN in
  * e4m3 and becomes 0 in int8.
  *   slots     as for affqmm_rope_append; and the tokens of one block come one
