@@ -25,8 +25,10 @@
 // a chunk of each to a thread).  Sines are made once a CTA, from the nearest
 // quarter of a turn.  Bound by memory and, nearly as much, by the way of a CTA
 // from its slots to its codes (24 warps an SM; issue slots 61 % taken for a chunk
-// of prompts; 44 to 56 bytes of spill beside 80 registers where pairs lie in runs): measured (GB300, device time) 25.6 us for 5456 tokens of 32 + 2 x 8
-// heads of 128, e4m3, 123 MB, 72 % of the copy rate (68 us with a warp to a block
+// of prompts; 44 to 56 bytes of spill beside 80 registers where eight or four
+// values or neighbours make a run): measured (GB300, device time) 25.8 us for 5456
+// tokens of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 71 % of the copy rate (68 us
+// with a warp to a block
 // and the rows as fp32; 33 with them as read; 30 with several tokens of q to a
 // CTA); 29 us for 6210 tokens with a scale for each (81 with a warp to each); 3.3
 // us for a decode step of 64 tokens, 4.2 to 4.8 while its blocks grow.  Two CTAs an
