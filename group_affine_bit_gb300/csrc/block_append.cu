@@ -21,20 +21,20 @@
 // powers of two: growth then only shifts exponents, and codes lose bits below the
 // normal ones alone.
 //
-// One launch has CTAs for k and v, which come first, and for q (up to four tokens,
-// a chunk of each to a thread).  Sines are made once a CTA, from the nearest
-// quarter of a turn.  Bound by memory and, nearly as much, by the way of a CTA
-// from its slots to its codes (24 warps an SM; issue slots 61 % taken for a chunk
-// of prompts; 44 to 56 bytes of spill beside 80 registers where eight or four
-// values or neighbours make a run): measured (GB300, device time) 25.8 us for 5456
-// tokens of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 71 % of the copy rate (68 us
-// with a warp to a block
-// and the rows as fp32; 33 with them as read; 30 with several tokens of q to a
-// CTA); 29 us for 6210 tokens with a scale for each (81 with a warp to each); 3.3
-// us for a decode step of 64 tokens, 4.2 to 4.8 while its blocks grow.  Two CTAs an
-// SM instead of three are 15 to 20 % slower, four (64 registers) no faster; loads
-// and stores that leave L2 first, packed fp32 arithmetic, and CTAs of k and v
-// spread among those of q changed nothing.
+// One launch has CTAs for k and v, which come first, for q (up to four tokens, a
+// chunk of each to a thread) and, with a status word, a few that look whether each
+// block's tokens come one after another.  Sines are made once a CTA, from the
+// nearest quarter of a turn.  Bound by memory and, nearly as much, by the way of a
+// CTA from its slots to its codes (24 warps an SM; issue slots 61 % taken for a
+// chunk of prompts; 44 to 56 bytes of spill beside 80 registers where values lie in
+// runs or neighbours pair): measured (GB300, device time) 25.8 us for 5456 tokens
+// of 32 + 2 x 8 heads of 128, e4m3, 123 MB, 71 % of the copy rate (68 us with a warp
+// to a block and the rows as fp32; 33 with them as read; 30 with several tokens of q
+// to a CTA); 29 us for 6210 tokens with a scale for each (81 with a warp to each);
+// 3.3 to 3.5 us for a decode step of 64 tokens, 4.2 to 4.9 while its blocks grow.
+// Two CTAs an SM instead of three are 15 to 20 % slower, four (64 registers) no
+// faster; loads and stores that leave L2 first, packed fp32 arithmetic, and CTAs of
+// k and v spread among those of q changed nothing.
 #include <type_traits>
 
 #include "affqmm_internal.h"
